@@ -229,3 +229,9 @@ def alloc_state(desc: Desc, device="cuda"):
         item = torch.empty((), dtype=dt).element_size()
         out[name] = torch.zeros(nbytes // item, dtype=dt, device=device)
     return out
+
+
+# The operators around the state in its layer (include/gdnq_layer.h).
+from .layer import (CONV_SILU, NORM_GATE_FIRST, NORM_GATE_SIGMOID, NORM_GROUP_WEIGHT, NORM_RES_F32,  # noqa: E402,F401
+                    SSM_SOFTPLUS, ConvDesc, NormDesc, SsmDesc, gdnq_conv_prefill, gdnq_conv_step, gdnq_norm_gated,
+                    gdnq_norm_residual, gdnq_ssm_prefill, gdnq_ssm_step, gdnq_ssm_workspace)

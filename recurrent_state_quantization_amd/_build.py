@@ -29,8 +29,9 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdnq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["api.cpp", "decode.hip", "window.hip", "codec.hip", "calibrate.hip", "prefill.hip", "prefill_kda.hip"]
-HEADERS = ["tile.hpp", "codec.hpp", "launch.hpp", "launchers.hpp"]
+SOURCES = ["api.cpp", "decode.hip", "window.hip", "codec.hip", "calibrate.hip", "prefill.hip", "prefill_kda.hip",
+           "layer_api.cpp", "conv.hip", "ssm_step.hip", "ssm_prefill.hip", "norm.hip"]
+HEADERS = ["tile.hpp", "codec.hpp", "launch.hpp", "launchers.hpp", "errors.hpp", "rows.hpp", "layer_launchers.hpp"]
 
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

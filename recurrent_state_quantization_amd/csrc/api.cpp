@@ -9,13 +9,14 @@
 #include <cstring>
 #include <vector>
 
+#include "errors.hpp"
 #include "gdnq.h"
 #include "launch.hpp"
 #include "launchers.hpp"
 
-namespace {
+namespace gdnq {
 
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char *fmt, ...)
 {
@@ -32,20 +33,22 @@ int ok()
     return GDNQ_OK;
 }
 
-struct Span {
-    const void *p;
-    size_t n;
-    const char *name;
-};
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlap(const Span &a, const Span &b)
+int launched(hipError_t e)
 {
-    if (!a.p || !b.p || a.n == 0 || b.n == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.n && b0 < a0 + a.n;
+    if (e != hipSuccess) return fail(GDNQ_ELAUNCH, "HIP launch failed: %s", hipGetErrorString(e));
+    return ok();
 }
+
+}  // namespace gdnq
+
+namespace {
+
+using gdnq::aligned16;
+using gdnq::fail;
+using gdnq::launched;
+using gdnq::ok;
+using gdnq::overlap;
+using gdnq::Span;
 
 size_t io_size(const gdnq_desc &d) { return d.io_dtype == GDNQ_IO_BF16 ? 2 : 4; }
 size_t nheads(const gdnq_desc &d) { return (size_t)d.B * (size_t)d.H; }
@@ -206,17 +209,11 @@ int check_step_io(const gdnq_desc &d, const void *q, const void *k, const void *
     return GDNQ_OK;
 }
 
-int launched(hipError_t e)
-{
-    if (e != hipSuccess) return fail(GDNQ_ELAUNCH, "HIP launch failed: %s", hipGetErrorString(e));
-    return ok();
-}
-
 }  // namespace
 
 extern "C" {
 
-const char *gdnq_last_error(void) { return g_err; }
+const char *gdnq_last_error(void) { return gdnq::g_err; }
 
 int gdnq_state_sizes(const gdnq_desc *desc, size_t bytes_out[12])
 {

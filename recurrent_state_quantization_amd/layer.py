@@ -1,0 +1,253 @@
+"""Binding of the operators around a recurrent state (``include/gdnq_layer.h``):
+short causal convolution, selective state space scan, gated norm, residual norm.
+
+Argument marshalling only, as in the package itself.  Token tensors are 2-D
+(one row per token; the row distance is the tensor's own), or 3-D with the
+heads as the middle dimension; descriptors are the dataclasses below or their
+marshalled form (``.c()``).  Device pointers given as integers stand for
+contiguous rows.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+
+from . import EINVAL, IO_BF16, GdnqError, _check, _stream, lib
+
+CONV_SILU = 1
+SSM_SOFTPLUS = 1
+NORM_GATE_SIGMOID, NORM_GATE_FIRST, NORM_GROUP_WEIGHT, NORM_RES_F32 = 1, 2, 4, 8
+
+_i32, _u32, _i64, _f32, _P = ctypes.c_int32, ctypes.c_uint32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+class _ConvDesc(ctypes.Structure):
+    _fields_ = [("C", _i32), ("width", _i32), ("io_dtype", _i32), ("flags", _u32)]
+
+
+class _SsmDesc(ctypes.Structure):
+    _fields_ = [("H", _i32), ("dk", _i32), ("dv", _i32), ("hk", _i32), ("io_dtype", _i32), ("flags", _u32),
+                ("dt_min", _f32), ("dt_max", _f32)]
+
+
+class _SsmIo(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("x", "B", "C", "dt", "y", "A", "D", "dt_bias")]
+    _fields_ += [(n, _i64) for n in ("ldx", "ldb", "ldc", "lddt", "ldy")]
+
+
+class _NormDesc(ctypes.Structure):
+    _fields_ = [("D", _i32), ("group", _i32), ("io_dtype", _i32), ("flags", _u32), ("eps", _f32), ("w_offset", _f32)]
+
+
+@dataclasses.dataclass
+class ConvDesc:
+    """Mirror of gdnq_conv_desc."""
+    C: int
+    width: int = 4
+    io_dtype: int = IO_BF16
+    flags: int = CONV_SILU
+
+    def c(self) -> _ConvDesc:
+        return _ConvDesc(*dataclasses.astuple(self))
+
+
+@dataclasses.dataclass
+class SsmDesc:
+    """Mirror of gdnq_ssm_desc."""
+    H: int
+    dk: int = 128
+    dv: int = 64
+    hk: int = 0
+    io_dtype: int = IO_BF16
+    flags: int = SSM_SOFTPLUS
+    dt_min: float = 0.0
+    dt_max: float = float("inf")
+
+    def c(self) -> _SsmDesc:
+        return _SsmDesc(*dataclasses.astuple(self))
+
+
+@dataclasses.dataclass
+class NormDesc:
+    """Mirror of gdnq_norm_desc."""
+    D: int
+    group: int = 0
+    io_dtype: int = IO_BF16
+    flags: int = 0
+    eps: float = 1e-6
+    w_offset: float = 0.0
+
+    def c(self) -> _NormDesc:
+        return _NormDesc(*dataclasses.astuple(self))
+
+
+def _load():
+    D, S, N = ctypes.POINTER(_ConvDesc), ctypes.POINTER(_SsmDesc), ctypes.POINTER(_NormDesc)
+    io = ctypes.POINTER(_SsmIo)
+    sig = {
+        "gdnq_conv_prefill": [D, _P, _i64, _P, _P, _P, _i32, _P, _P, _P, _i32, _i32, _P, _i64, _P],
+        "gdnq_conv_step": [D, _P, _i64, _P, _P, _P, _i32, _P, _i32, _P, _i64, _P],
+        "gdnq_ssm_workspace": [S, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)],
+        "gdnq_ssm_prefill": [S, io, _P, _i32, _P, _P, _P, _i32, _i32, _P, ctypes.c_size_t, _P],
+        "gdnq_ssm_step": [S, io, _P, _i32, _P, _i32, _P],
+        "gdnq_norm_gated": [N, _P, _i64, _P, _i64, _P, _P, _i64, _i32, _P],
+        "gdnq_norm_residual": [N, _P, _i64, _P, _f32, _P, _i64, _P, _i64, _P, _P, _i64, _i32, _P],
+    }
+    for name, args in sig.items():
+        if not hasattr(lib, name):
+            raise ImportError(f"the built library does not export {name}: it predates its sources; rebuild it "
+                              "with __graft_entry__.build()")
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+
+
+_load()
+
+
+def _desc(d):
+    return d if isinstance(d, ctypes.Structure) else d.c()
+
+
+def _bad(msg):
+    raise GdnqError(EINVAL, msg)
+
+
+def _io_name(io):
+    return "torch.bfloat16" if io == IO_BF16 else "torch.float32"
+
+
+def _device(t, name):
+    import torch
+    if t.device.type != "cuda":
+        _bad(f"{name} is on {t.device}, not on a GPU")
+    if t.device.index != torch.cuda.current_device():
+        _bad(f"{name} is on {t.device}, not on the current device {torch.cuda.current_device()}")
+
+
+def _rows(t, n, width, dtype, name):
+    """(pointer, row distance) of n rows of `width` values."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    _device(t, name)
+    if str(t.dtype) != dtype:
+        _bad(f"{name} is {t.dtype}, not {dtype}")
+    shape, st = t.shape, t.stride()
+    if t.dim() == 3:
+        flat = shape[1] * shape[2] == width and st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
+    else:
+        flat = t.dim() == 2 and shape[1] == width and (st[1] == 1 or width == 1)
+    if not flat:
+        _bad(f"{name} must have rows of {width} consecutive values (got shape {tuple(shape)}, strides {st})")
+    if shape[0] < n:
+        _bad(f"{name} has {shape[0]} rows, {n} are needed")
+    # one row has no distance; a zero distance would read as "contiguous"
+    if shape[0] > 1 and st[0] < width:
+        _bad(f"the rows of {name} overlap")
+    return t.data_ptr(), (st[0] if shape[0] > 1 else width)
+
+
+def _flat(t, n, dtype, name):
+    """Pointer of at least n contiguous values."""
+    if t is None or isinstance(t, int):
+        return t
+    _device(t, name)
+    if str(t.dtype) != dtype:
+        _bad(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_contiguous():
+        _bad(f"{name} must be contiguous")
+    if t.numel() < n:
+        _bad(f"{name} has {t.numel()} values, {n} are needed")
+    return t.data_ptr()
+
+
+_F, _I = "torch.float32", "torch.int32"
+
+
+def gdnq_conv_prefill(desc, x, w, bias, state, n_slots, slots, cont, cu_seqlens, n_seqs, T, y, stream=None):
+    d = _desc(desc)
+    io = _io_name(d.io_dtype)
+    xp, ldx = _rows(x, T, d.C, io, "x")
+    yp, ldy = _rows(y, T, d.C, io, "y")
+    _check(lib.gdnq_conv_prefill(
+        d, xp, ldx, _flat(w, d.width * d.C, _F, "w"), _flat(bias, d.C, _F, "bias"),
+        _flat(state, n_slots * (d.width - 1) * d.C, io, "state"), n_slots, _flat(slots, n_seqs, _I, "slots"),
+        _flat(cont, n_seqs, _I, "cont"), _flat(cu_seqlens, n_seqs + 1, _I, "cu_seqlens"), n_seqs, T, yp, ldy,
+        _stream(stream)))
+
+
+def gdnq_conv_step(desc, x, w, bias, state, n_slots, slots, n, y, stream=None):
+    d = _desc(desc)
+    io = _io_name(d.io_dtype)
+    xp, ldx = _rows(x, n, d.C, io, "x")
+    yp, ldy = _rows(y, n, d.C, io, "y")
+    _check(lib.gdnq_conv_step(
+        d, xp, ldx, _flat(w, d.width * d.C, _F, "w"), _flat(bias, d.C, _F, "bias"),
+        _flat(state, n_slots * (d.width - 1) * d.C, io, "state"), n_slots, _flat(slots, n, _I, "slots"), n, yp, ldy,
+        _stream(stream)))
+
+
+def gdnq_ssm_workspace(desc, n_seqs, T) -> int:
+    """Bytes of workspace that gdnq_ssm_prefill needs."""
+    out = ctypes.c_size_t()
+    _check(lib.gdnq_ssm_workspace(_desc(desc), n_seqs, T, ctypes.byref(out)))
+    return out.value
+
+
+def _ssm_io(d, n, x, B, C, dt, A, D, dt_bias, y):
+    io = _io_name(d.io_dtype)
+    nb = (d.hk or d.H) * d.dk
+    xp, ldx = _rows(x, n, d.H * d.dv, io, "x")
+    bp, ldb = _rows(B, n, nb, io, "B")
+    cp, ldc = _rows(C, n, nb, io, "C")
+    tp, lddt = _rows(dt, n, d.H, io, "dt")
+    yp, ldy = _rows(y, n, d.H * d.dv, io, "y")
+    return _SsmIo(xp, bp, cp, tp, yp, _flat(A, d.H, _F, "A"), _flat(D, d.H, _F, "D"),
+                  _flat(dt_bias, d.H, _F, "dt_bias"), ldx, ldb, ldc, lddt, ldy)
+
+
+def gdnq_ssm_prefill(desc, x, B, C, dt, A, D, dt_bias, y, S, n_slots, slots, cont, cu_seqlens, n_seqs, T,
+                     workspace=None, stream=None):
+    d = _desc(desc)
+    nb = 0
+    if workspace is not None and not isinstance(workspace, int):
+        _device(workspace, "workspace")
+        if not workspace.is_contiguous():
+            _bad("workspace must be contiguous")
+        nb = workspace.numel() * workspace.element_size()
+        workspace = workspace.data_ptr()
+    elif workspace is not None:
+        nb = gdnq_ssm_workspace(d, n_seqs, T)
+    _check(lib.gdnq_ssm_prefill(
+        d, _ssm_io(d, T, x, B, C, dt, A, D, dt_bias, y), _flat(S, n_slots * d.H * d.dk * d.dv, _F, "S"), n_slots,
+        _flat(slots, n_seqs, _I, "slots"), _flat(cont, n_seqs, _I, "cont"),
+        _flat(cu_seqlens, n_seqs + 1, _I, "cu_seqlens"), n_seqs, T, workspace, nb, _stream(stream)))
+
+
+def gdnq_ssm_step(desc, x, B, C, dt, A, D, dt_bias, y, S, n_slots, slots, n, stream=None):
+    d = _desc(desc)
+    _check(lib.gdnq_ssm_step(
+        d, _ssm_io(d, n, x, B, C, dt, A, D, dt_bias, y), _flat(S, n_slots * d.H * d.dk * d.dv, _F, "S"), n_slots,
+        _flat(slots, n, _I, "slots"), n, _stream(stream)))
+
+
+def gdnq_norm_gated(desc, x, z, w, y, rows, stream=None):
+    d = _desc(desc)
+    io = _io_name(d.io_dtype)
+    xp, ldx = _rows(x, rows, d.D, io, "x")
+    zp, ldz = _rows(z, rows, d.D, io, "z")
+    yp, ldy = _rows(y, rows, d.D, io, "y")
+    nw = (d.group or d.D) if d.flags & NORM_GROUP_WEIGHT else d.D
+    _check(lib.gdnq_norm_gated(d, xp, ldx, zp, ldz, _flat(w, nw, _F, "w"), yp, ldy, rows, _stream(stream)))
+
+
+def gdnq_norm_residual(desc, x, post_w, scale, res, res_out, w, y, rows, stream=None):
+    d = _desc(desc)
+    io = _io_name(d.io_dtype)
+    rio = _F if d.flags & NORM_RES_F32 else io
+    xp, ldx = _rows(x, rows, d.D, io, "x")
+    rp, ldr = _rows(res, rows, d.D, rio, "res")
+    op, ldro = _rows(res_out, rows, d.D, rio, "res_out")
+    yp, ldy = _rows(y, rows, d.D, io, "y")
+    _check(lib.gdnq_norm_residual(d, xp, ldx, _flat(post_w, d.D, _F, "post_w"), scale, rp, ldr, op, ldro,
+                                  _flat(w, d.D, _F, "w"), yp, ldy, rows, _stream(stream)))
