@@ -5,27 +5,32 @@
 // LinQuant, appendix Table 3, Mamba-2 row, in the dk x dv orientation.
 //
 // The recurrence unrolled over a chunk of 64 tokens, with cs_i the running
-// sum of delta A inside the chunk and S the state at its start:
-//   M_ij = (C_i . B_j) e^{cs_i - cs_j} delta_j   (j <= i, else 0)
-//   Y    = M X + diag(e^{cs}) C S + D X
-//   S   <- e^{cs_63} S + B^T diag(e^{cs_63 - cs} delta) X.
-// Exponents are kept in base 2 and are never positive, so nothing overflows;
-// e^{cs_63 - cs_j} comes from a sum over the tokens behind j, which keeps it
-// exact where it is near one.
+// sum of delta A inside the chunk, w_j = e^{cs_63 - cs_j} delta_j, S the state
+// at the chunk's start and S' = e^{cs_63} S, takes all decays out of the
+// token-by-token product:
+//   Y = diag(e^{cs_i - cs_63}) (tril(C B^T) (w X) + C S') + D X,
+//   S <- S' + B^T (w X).
+// tril(C B^T) is the same for all heads that share B and C, so a workgroup
+// forms it once, and w X serves both lines.  A head whose chunk decays by
+// more than 2^-RANGE takes the first line as
+//   Y = (tril(C B^T) . e^{cs_i - cs_j} delta_j) X + diag(e^{cs_i}) C S + D X
+// instead, whose factors are all at most one.  Exponents are in base 2;
+// cs_63 - cs_j is summed over the tokens behind j, which keeps it exact where
+// it is small.
 //
-// Precision: the products run on v_mfma_f32_32x32x16_bf16 with fp32 sums.
-// B, C and x are bf16, so C B^T is exact up to the sum; the fp32 operands M
-// and S of the outputs are split into two bf16 parts (off by 2^-18), the
-// weighted x of the state's update into three (2^-26), so that states stay
-// as exact as fp32.
+// Precision: the products run on the bf16 matrix instructions with fp32
+// sums.  B, C and x are bf16, so C B^T is exact up to the sum.  The fp32
+// operands of the outputs, tril(C B^T), S' and w X, are taken in two bf16
+// parts (off by 2^-18); the state's update takes w X in three (2^-26), so
+// that states stay as exact as fp32.
 //
 // A wave owns 32 value columns of one head for the whole segment: its state
 // (dk x 32) stays in accumulators, which feed C S directly as the B operand
 // when the contraction index is taken in the accumulators' row order (slots
 // 0..3 of lane half h are rows 16t + 4h .. + 3, slots 4..7 rows 16t + 8 + 4h
-// .. + 3).  The transposed product B C^T likewise leaves M in the layout of
-// an A operand.  x and B are read by columns with the transposing LDS read.
-// A workgroup holds up to 8 waves: HPW heads that share B and C.
+// .. + 3).  x and B are read by columns with the transposing LDS read.  A
+// workgroup holds up to 8 waves: HPW heads that share B and C.  The next
+// chunk's rows are loaded into registers while a chunk is computed.
 //
 // Long sequences are cut into segments of 2^SH tokens (launch_ssm_prefill
 // says when): a first kernel forms each segment's own state and decay from
@@ -39,6 +44,7 @@ namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 typedef short shortx4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
@@ -51,7 +57,7 @@ struct SsmArgs {
     int sh;              // log2 of a segment's tokens
     unsigned ids;        // segment numbers
     float dt_min, dt_max;
-    bool sp, wide;
+    bool sp;
     Divisor byHB;        // head blocks per segment
     float *ws;           // [ids][H][dk*dv] states, then [ids][H] base-2 decay exponents
 };
@@ -83,26 +89,36 @@ __device__ __forceinline__ float lane_of(float x, int lane)
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
 
-// h + l = x up to 2^-18 of x
-__device__ __forceinline__ void split2(const float (&x)[8], bf16x8 &h, bf16x8 &l)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+// two values rounded to bf16 in one instruction, the first in the low half
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2{a, b}), bf16x2));
+}
+__device__ __forceinline__ float low_of(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float high_of(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
+
+// x[0..N) as the sum of P bf16 parts, off by 2^-(9 P) of x
+template <int P, int N>
+__device__ __forceinline__ void split(float (&x)[N], uint32_t (&part)[P][N / 2])
 {
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        h[e] = (__bf16)x[e];
-        l[e] = (__bf16)(x[e] - (float)h[e]);
-    }
+    for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int i = 0; i < N / 2; i++) {
+            part[p][i] = pack2(x[2 * i], x[2 * i + 1]);
+            if (p + 1 < P) {
+                x[2 * i] -= low_of(part[p][i]);
+                x[2 * i + 1] -= high_of(part[p][i]);
+            }
+        }
 }
 
-// h + m + l = x up to 2^-26 of x
-__device__ __forceinline__ void split3(const float (&x)[8], bf16x8 &h, bf16x8 &m, bf16x8 &l)
+__device__ __forceinline__ bf16x8 operand(const uint32_t (&p)[4])
 {
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-        h[e] = (__bf16)x[e];
-        const float r = x[e] - (float)h[e];
-        m[e] = (__bf16)r;
-        l[e] = (__bf16)(r - (float)m[e]);
-    }
+    return __builtin_bit_cast(bf16x8, (u32x4{p[0], p[1], p[2], p[3]}));
 }
 
 // Columns of a row-major LDS tile as an operand: lane (c, h) gets column c of
@@ -125,15 +141,26 @@ __device__ __forceinline__ bf16x8 ld_rows(const __bf16 *p)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// 8 consecutive bf16 values of a token row
-__device__ __forceinline__ u32x4 ld_global8(const void *base, size_t off, bool wide)
+// 8 consecutive bf16 values of a token row, in one load where rows are WIDE
+template <bool WIDE>
+__device__ __forceinline__ u32x4 ld_global8(const void *base, size_t off)
 {
     const uint16_t *p = reinterpret_cast<const uint16_t *>(base) + off;
-    if (wide) return *reinterpret_cast<const u32x4 *>(p);
+    if constexpr (WIDE) return *reinterpret_cast<const u32x4 *>(p);
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; i++) r[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
     return r;
+}
+
+template <bool WIDE>
+__device__ __forceinline__ void st_global8(void *base, size_t off, u32x4 v)
+{
+    uint16_t *p = reinterpret_cast<uint16_t *>(base) + off;
+    if constexpr (WIDE) *reinterpret_cast<u32x4 *>(p) = v;
+    else
+#pragma unroll
+        for (int i = 0; i < 4; i++) p[2 * i] = (uint16_t)v[i], p[2 * i + 1] = (uint16_t)(v[i] >> 16);
 }
 
 // Row strides in elements.  B is read by rows (C B^T) and by columns (the
@@ -151,19 +178,36 @@ struct SsmGeom {
     static constexpr int NBLK = DK / 32;
 };
 
-enum { V_CS, V_E, V_W, V_D, V_VE, V_N };   // per-token vectors in LDS
+// Per-token vectors of a head in LDS: the outputs' row factor, w, and for the
+// other form cs and delta.
+enum { V_F, V_W, V_CS, V_D, V_N };
+
+// Chunks that decay to 2^-RANGE or less take the second form: 2^RANGE and
+// 2^-RANGE times any usual value, and its second bf16 part, are normal numbers.
+constexpr float RANGE = 80.0f;
 
 template <class G>
 struct SsmLds {
+    static constexpr int HEADS = G::NW / G::SL;
     __bf16 b[CH * G::SB];
     __bf16 c[CH * G::SC];
     __bf16 x[CH * G::SX];
-    alignas(16) float v[G::NW / G::SL][V_N][CH];
-    float tot[G::NW / G::SL];
+    // tril(C B^T) as operands: rows 0..31 by tokens 0..15, 16..31, rows 32..63
+    // by tokens 0..15, .., 48..63; each in two parts of 8 values per lane
+    alignas(16) __bf16 g[6][2][64 * 8];
+    alignas(16) float v[2][HEADS][V_N][CH];
+    float tot[2][HEADS];
+    int far[2][HEADS];
+};
+
+// One chunk's rows on their way from memory to LDS.
+template <class G, bool STATE>
+struct SsmRows {
+    u32x4 b[G::NB], c[STATE ? 1 : G::NB], x[G::NX];
 };
 
 // STATE: only the segment's own state and decay, from zero.
-template <int DK, int DV, int HPW, bool STATE>
+template <int DK, int DV, int HPW, bool STATE, bool WIDE>
 __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(SsmArgs A)
 {
     using G = SsmGeom<DK, DV, HPW>;
@@ -201,174 +245,246 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
     const float Dh = io.D ? io.D[head] : 0.0f;
     float seglog = 0.0f;
 
-    for (int c0 = 0; c0 < ntok; c0 += CH) {
+    // rows behind the segment's end repeat its last one; their weights are zero
+    SsmRows<G, STATE> R;
+    const auto fetch = [&](int c0) {
+        const int nv = min(CH, ntok - c0);
+        const size_t row = row0 + c0;
+#pragma unroll
+        for (int i = 0; i < G::NB; i++) {
+            const int p = t + i * G::NT, k8 = p % (DK / 8);
+            const size_t src = row + min(p / (DK / 8), nv - 1), col = (size_t)hb * DK + k8 * 8;
+            R.b[i] = ld_global8<WIDE>(io.B, src * io.ldb + col);
+            if constexpr (!STATE) R.c[i] = ld_global8<WIDE>(io.C, src * io.ldc + col);
+        }
+#pragma unroll
+        for (int i = 0; i < G::NX; i++) {
+            constexpr int PR = HPW * DV / 8;
+            const int p = t + i * G::NT;
+            R.x[i] = ld_global8<WIDE>(io.x, (row + min(p / PR, nv - 1)) * io.ldx + (size_t)h0 * DV + p % PR * 8);
+        }
+    };
+    float dt_in = 0.0f;
+    const auto fetch_dt = [&](int c0) {
+        if (slice == 0) dt_in = load1<true>(io.dt, (row0 + c0 + min(lane, ntok - c0 - 1)) * io.lddt + head);
+    };
+    // decays of a chunk: one wave per head, one token per lane
+    const auto decays = [&](int nv, int buf) {
+        float d = dt_in + bias;
+        if (A.sp) d = softplus(d);
+        d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
+        const float la = d * Ah;
+        const float suf = __shfl(scan64(__shfl(la, 63 - lane)), 63 - lane) - la;   // the tokens behind this one
+        const float cs = scan64(la), tot = lane_of(cs, 63);
+        const bool far = !(tot > -RANGE);
+        float(&v)[V_N][CH] = L.v[buf][hw];
+        v[V_W][lane] = __builtin_amdgcn_exp2f(suf) * d;
+        if constexpr (!STATE) {
+            v[V_F][lane] = __builtin_amdgcn_exp2f(far ? cs : -suf);
+            v[V_CS][lane] = cs;
+            v[V_D][lane] = d;
+        }
+        seglog += tot;
+        if (lane == 0) {
+            L.tot[buf][hw] = __builtin_amdgcn_exp2f(tot);
+            L.far[buf][hw] = far;
+        }
+    };
+
+    if constexpr (!STATE) {   // the blocks above the diagonal stay zero
+        for (int i = t; i < 6 * 2 * 64; i += G::NT) *reinterpret_cast<uint4 *>(&L.g[0][0][i * 8]) = make_uint4(0, 0, 0, 0);
+    }
+    fetch_dt(0);
+    fetch(0);
+    if (slice == 0) decays(min(CH, ntok), 0);
+    if (CH < ntok) fetch_dt(CH);
+    int buf = 0;
+    for (int c0 = 0; c0 < ntok; c0 += CH, buf ^= 1) {
         const int nv = min(CH, ntok - c0);
         const size_t row = row0 + c0;
         __syncthreads();   // the previous chunk's reads are done
-        // ---- stage the chunk; rows behind the end repeat the last one (their weights are zero)
 #pragma unroll
         for (int i = 0; i < G::NB; i++) {
             const int p = t + i * G::NT, r = p / (DK / 8), k8 = p % (DK / 8);
-            const size_t src = row + min(r, nv - 1);
-            const u32x4 vb = ld_global8(io.B, src * io.ldb + (size_t)hb * DK + k8 * 8, A.wide);
-            *reinterpret_cast<u32x4 *>(&L.b[r * G::SB + k8 * 8]) = vb;
+            *reinterpret_cast<u32x4 *>(&L.b[r * G::SB + k8 * 8]) = R.b[i];
             if constexpr (!STATE) {
-                const u32x4 vc = ld_global8(io.C, src * io.ldc + (size_t)hb * DK + k8 * 8, A.wide);
                 // columns of each 16 in the order 0-3, 8-11, 4-7, 12-15
                 __bf16 *d = &L.c[r * G::SC + (k8 & ~1) * 8 + (k8 & 1) * 4];
-                *reinterpret_cast<uint2 *>(d) = make_uint2(vc[0], vc[1]);
-                *reinterpret_cast<uint2 *>(d + 8) = make_uint2(vc[2], vc[3]);
+                *reinterpret_cast<uint2 *>(d) = make_uint2(R.c[i][0], R.c[i][1]);
+                *reinterpret_cast<uint2 *>(d + 8) = make_uint2(R.c[i][2], R.c[i][3]);
             }
         }
 #pragma unroll
         for (int i = 0; i < G::NX; i++) {
             constexpr int PR = HPW * DV / 8;
-            const int p = t + i * G::NT, r = p / PR, k8 = p % PR;
-            const u32x4 vx = ld_global8(io.x, (row + min(r, nv - 1)) * io.ldx + (size_t)h0 * DV + k8 * 8, A.wide);
-            *reinterpret_cast<u32x4 *>(&L.x[r * G::SX + k8 * 8]) = vx;
-        }
-        // ---- decays: one wave per head, one token per lane
-        if (slice == 0) {
-            float d = load1<true>(io.dt, (row + min(lane, nv - 1)) * io.lddt + head) + bias;
-            if (A.sp) d = softplus(d);
-            d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
-            const float la = d * Ah;
-            const float cs = scan64(la);
-            const float suf = __shfl(scan64(__shfl(la, 63 - lane)), 63 - lane) - la;   // the tokens behind this one
-            const float mid = lane_of(cs, 31), tot = lane_of(cs, 63);
-            const float lr = exp2f(lane < 32 ? mid - cs : cs - mid);
-            L.v[hw][V_CS][lane] = cs;
-            L.v[hw][V_E][lane] = exp2f(cs);
-            L.v[hw][V_W][lane] = exp2f(suf) * d;
-            L.v[hw][V_D][lane] = d;
-            L.v[hw][V_VE][lane] = lane < 32 ? lr * d : lr;
-            seglog += tot;
-            if (lane == 0) L.tot[hw] = exp2f(tot);
+            const int p = t + i * G::NT;
+            *reinterpret_cast<u32x4 *>(&L.x[p / PR * G::SX + p % PR * 8]) = R.x[i];
         }
         __syncthreads();
+        const bool more = c0 + CH < ntok;
+        if (more) fetch(c0 + CH);
+
+        // ---- the first wave of a head forms the next chunk's decays, the others
+        // tril(C B^T): the 10 blocks of 16 x 16 tokens on and below the diagonal, by turns
+        if (slice == 0) {
+            if (more) {
+                decays(min(CH, ntok - c0 - CH), buf ^ 1);
+                if (c0 + 2 * CH < ntok) fetch_dt(c0 + 2 * CH);
+            }
+        } else if constexpr (!STATE) {
+            const int l16 = lane & 15, qd = lane >> 4;
+            for (int n = hw * (G::SL - 1) + slice - 1; n < 10; n += HPW * (G::SL - 1)) {
+                const int I = (int)((0x3333222110ull >> (4 * n)) & 15u), J = (int)((0x3210210100ull >> (4 * n)) & 15u);
+                floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < DK / 32; s++) {
+                    const bf16x8 bj = ld_rows(&L.b[(16 * J + l16) * G::SB + 32 * s + 16 * (qd / 2) + 4 * (qd & 1)]);
+                    const bf16x8 ci = *reinterpret_cast<const bf16x8 *>(&L.c[(16 * I + l16) * G::SC + 32 * s + 8 * qd]);
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bj, ci, acc, 0, 0, 0);
+                }
+                // row 4 qd + r of the block is token j, lane l16 token i
+                float m[4];
+                uint32_t part[2][2];
+#pragma unroll
+                for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
+                split<2, 4>(m, part);
+                const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
+#pragma unroll
+                for (int p = 0; p < 2; p++)
+                    *reinterpret_cast<uint2 *>(&L.g[f][p][at]) = make_uint2(part[p][0], part[p][1]);
+            }
+        }
+        if constexpr (!STATE) __syncthreads();
 
         const int l16 = lane & 15;
         const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
-        const float *vec = &L.v[hw][0][0];
+        const float(&vec)[V_N][CH] = L.v[buf][hw];
+        const float tot = L.tot[buf][hw];
+        const bool far = !STATE && __builtin_amdgcn_readfirstlane(L.far[buf][hw]);
         bf16x8 xf[4];   // x rows 16 f .. + 15, the wave's columns
 #pragma unroll
         for (int f = 0; f < 4; f++)
             xf[f] = ld_cols(&L.x[(16 * f + tr_r) * G::SX + hw * DV + slice * 32 + tr_c], G::SX);
 
-        if constexpr (!STATE) {
-            floatx16 Y[2], Gt[3];   // Gt: (j, i) blocks (0,0), (0,1), (1,1) of B C^T
+        const auto decay_state = [&] {
 #pragma unroll
-            for (int r = 0; r < 16; r++) Y[0][r] = Y[1][r] = Gt[0][r] = Gt[1][r] = Gt[2][r] = 0.0f;
+            for (int nb = 0; nb < G::NBLK; nb++)
 #pragma unroll
-            for (int s = 0; s < DK / 16; s++) {
-                const bf16x8 ca = *reinterpret_cast<const bf16x8 *>(&L.c[c * G::SC + 16 * s + 8 * hh]);
-                const bf16x8 cb = *reinterpret_cast<const bf16x8 *>(&L.c[(32 + c) * G::SC + 16 * s + 8 * hh]);
-                const bf16x8 ba = ld_rows(&L.b[c * G::SB + 16 * s + 4 * hh]);
-                const bf16x8 bb = ld_rows(&L.b[(32 + c) * G::SB + 16 * s + 4 * hh]);
-                float sv[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) sv[e] = S[s / 2][8 * (s & 1) + e];
-                bf16x8 sh, sl;
-                split2(sv, sh, sl);
-                Gt[0] = mma(ba, ca, Gt[0]);
-                Gt[1] = mma(ba, cb, Gt[1]);
-                Gt[2] = mma(bb, cb, Gt[2]);
-                Y[0] = mma(ca, sh, Y[0]);
-                Y[1] = mma(cb, sh, Y[1]);
-                Y[0] = mma(ca, sl, Y[0]);
-                Y[1] = mma(cb, sl, Y[1]);
-            }
+                for (int r = 0; r < 16; r++) S[nb][r] *= tot;
+        };
+        floatx16 Y[2];
+        const auto scale_rows = [&] {   // Y rows by V_F
 #pragma unroll
             for (int ib = 0; ib < 2; ib++)
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const float4 e = *reinterpret_cast<const float4 *>(&vec[V_E * CH + 32 * ib + 8 * k + 4 * hh]);
-                    const float ev[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                    for (int r = 0; r < 4; r++) Y[ib][4 * k + r] *= ev[r];
+                    const float4 e = *reinterpret_cast<const float4 *>(&vec[V_F][32 * ib + 8 * k + 4 * hh]);
+                    Y[ib][4 * k] *= e.x, Y[ib][4 * k + 1] *= e.y, Y[ib][4 * k + 2] *= e.z, Y[ib][4 * k + 3] *= e.w;
                 }
-            // ---- Y += M X, block by block
+        };
+        if (!far) decay_state();
+        if constexpr (!STATE) {
 #pragma unroll
-            for (int b = 0; b < 3; b++) {
-                const int jb = b == 2, ib = b > 0;
-                const bool diag = b != 1;
-                const float ci = vec[(diag ? V_CS : V_VE) * CH + 32 * ib + c];
+            for (int r = 0; r < 16; r++) Y[0][r] = Y[1][r] = 0.0f;
 #pragma unroll
-                for (int tt = 0; tt < 2; tt++) {
-                    float m[8];
+            for (int s = 0; s < DK / 16; s++) {
+                const bf16x8 ca = *reinterpret_cast<const bf16x8 *>(&L.c[c * G::SC + 16 * s + 8 * hh]);
+                const bf16x8 cb = *reinterpret_cast<const bf16x8 *>(&L.c[(32 + c) * G::SC + 16 * s + 8 * hh]);
+                float sv[8];
+                uint32_t part[2][4];
 #pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const int j0 = 32 * jb + 16 * tt + 8 * k + 4 * hh;
-                        const float4 dj = *reinterpret_cast<const float4 *>(&vec[(diag ? V_D : V_VE) * CH + j0]);
-                        const float dv[4] = {dj.x, dj.y, dj.z, dj.w};
-                        float cj[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if (diag) {
-                            const float4 cv = *reinterpret_cast<const float4 *>(&vec[V_CS * CH + j0]);
-                            cj[0] = cv.x, cj[1] = cv.y, cj[2] = cv.z, cj[3] = cv.w;
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; r++) {
-                            const float gv = Gt[b][8 * tt + 4 * k + r] * dv[r];
-                            if (diag)
-                                m[4 * k + r] = j0 + r <= 32 * ib + c
-                                                   ? gv * __builtin_amdgcn_exp2f(ci - cj[r]) : 0.0f;
-                            else
-                                m[4 * k + r] = gv * ci;
-                        }
-                    }
-                    bf16x8 mh, ml;
-                    split2(m, mh, ml);
-                    Y[ib] = mma(mh, xf[2 * jb + tt], Y[ib]);
-                    Y[ib] = mma(ml, xf[2 * jb + tt], Y[ib]);
-                }
+                for (int e = 0; e < 8; e++) sv[e] = S[s / 2][8 * (s & 1) + e];
+                split<2, 8>(sv, part);
+                Y[0] = mma(ca, operand(part[0]), Y[0]);
+                Y[1] = mma(cb, operand(part[0]), Y[1]);
+                Y[0] = mma(ca, operand(part[1]), Y[0]);
+                Y[1] = mma(cb, operand(part[1]), Y[1]);
             }
-            // ---- y = Y + D x; neighbouring lanes trade halves so that each stores two columns of one row
-            const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
-            uint16_t *const yp = reinterpret_cast<uint16_t *>(io.y) + (size_t)head * DV + slice * 32 + (c & ~1);
+            if (far) {
+                scale_rows();
 #pragma unroll
-            for (int ib = 0; ib < 2; ib++)
+                for (int fr = 0; fr < 6; fr++) {
+                    const int ib = fr >= 2, f = ib ? fr - 2 : fr;
+                    const u32x4 gh = *reinterpret_cast<const u32x4 *>(&L.g[fr][0][lane * 8]);
+                    const u32x4 gl = *reinterpret_cast<const u32x4 *>(&L.g[fr][1][lane * 8]);
+                    const float ci = vec[V_CS][32 * ib + c];
+                    float m[8];
+                    uint32_t part[2][4];
 #pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-                    const bf16x8 &xr = xf[2 * ib + r / 8];
-                    const float y0 = fmaf(Dh, (float)xr[r % 8], Y[ib][r]);
-                    const float y1 = fmaf(Dh, (float)xr[r % 8 + 1], Y[ib][r + 1]);
-                    const uint32_t u = __builtin_bit_cast(uint32_t, (bf16x2{(__bf16)y0, (__bf16)y1}));
-                    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
-                    const uint32_t w = __builtin_amdgcn_perm(o, u, sel);
-                    const int i = 32 * ib + 8 * (r / 4) + 4 * hh + r % 4 + (lane & 1);
-                    if (i < nv) {
-                        uint16_t *d = yp + (row + i) * io.ldy;
-                        if (A.wide) *reinterpret_cast<uint32_t *>(d) = w;
-                        else d[0] = (uint16_t)w, d[1] = (uint16_t)(w >> 16);
+                    for (int e = 0; e < 8; e++) {
+                        const int j = 16 * f + 8 * (e / 4) + 4 * hh + e % 4;
+                        const float gv = (e & 1) ? high_of(gh[e / 2]) + high_of(gl[e / 2])
+                                                 : low_of(gh[e / 2]) + low_of(gl[e / 2]);
+                        // above the diagonal gv is zero, and the exponent is kept from overflowing
+                        m[e] = gv * (vec[V_D][j] * __builtin_amdgcn_exp2f(fminf(ci - vec[V_CS][j], 0.0f)));
                     }
+                    split<2, 8>(m, part);
+                    Y[ib] = mma(operand(part[0]), xf[f], Y[ib]);
+                    Y[ib] = mma(operand(part[1]), xf[f], Y[ib]);
                 }
+                decay_state();
+            }
         }
-
-        // ---- S <- e^{cs_63} S + B^T (w x)
-        const float tot = L.tot[hw];
-#pragma unroll
-        for (int nb = 0; nb < G::NBLK; nb++)
-#pragma unroll
-            for (int r = 0; r < 16; r++) S[nb][r] *= tot;
+        // ---- S' + B^T (w x), and tril(C B^T) (w x)
 #pragma unroll
         for (int f = 0; f < 4; f++) {
+            const u32x4 xr = __builtin_bit_cast(u32x4, xf[f]);
             float wx[8];
+            uint32_t part[3][4];
 #pragma unroll
             for (int k = 0; k < 2; k++) {
-                const float4 w = *reinterpret_cast<const float4 *>(&vec[V_W * CH + 16 * f + 8 * k + 4 * hh]);
-                const float wv4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int r = 0; r < 4; r++) wx[4 * k + r] = wv4[r] * (float)xf[f][4 * k + r];
+                const float4 w = *reinterpret_cast<const float4 *>(&vec[V_W][16 * f + 8 * k + 4 * hh]);
+                wx[4 * k] = w.x * low_of(xr[2 * k]);
+                wx[4 * k + 1] = w.y * high_of(xr[2 * k]);
+                wx[4 * k + 2] = w.z * low_of(xr[2 * k + 1]);
+                wx[4 * k + 3] = w.w * high_of(xr[2 * k + 1]);
             }
-            bf16x8 xh, xm, xl;
-            split3(wx, xh, xm, xl);
+            split<3, 8>(wx, part);
+            const bf16x8 xh = operand(part[0]), xm = operand(part[1]), xl = operand(part[2]);
+            if constexpr (!STATE) {
+                if (!far)
+#pragma unroll
+                    for (int ib = f / 2; ib < 2; ib++) {
+                        const int fr = ib ? 2 + f : f;
+                        const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[fr][0][lane * 8]);
+                        const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[fr][1][lane * 8]);
+                        Y[ib] = mma(gh, xh, Y[ib]);
+                        Y[ib] = mma(gl, xh, Y[ib]);
+                        Y[ib] = mma(gh, xm, Y[ib]);
+                    }
+            }
 #pragma unroll
             for (int nb = 0; nb < G::NBLK; nb++) {
                 const bf16x8 bt = ld_cols(&L.b[(16 * f + tr_r) * G::SB + 32 * nb + tr_c], G::SB);
                 S[nb] = mma(bt, xh, S[nb]);
                 S[nb] = mma(bt, xm, S[nb]);
                 S[nb] = mma(bt, xl, S[nb]);
+            }
+        }
+        if constexpr (!STATE) {
+            if (!far) scale_rows();
+            // ---- y = Y + D x, through the wave's own columns of the x tile: neighbouring lanes trade
+            // halves so that each writes two columns of a row, and rows leave in 16-byte pieces
+            const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
+            __bf16 *const yt = &L.x[hw * DV + slice * 32];
+            wave_lds_sync();
+#pragma unroll
+            for (int ib = 0; ib < 2; ib++)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    const uint32_t xr = __builtin_bit_cast(u32x4, xf[2 * ib + r / 8])[r % 8 / 2];
+                    const uint32_t u = pack2(fmaf(Dh, low_of(xr), Y[ib][r]), fmaf(Dh, high_of(xr), Y[ib][r + 1]));
+                    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
+                    const int i = 32 * ib + 8 * (r / 4) + r % 4 + 4 * hh + (lane & 1);
+                    *reinterpret_cast<uint32_t *>(&yt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
+                }
+            wave_lds_sync();
+#pragma unroll
+            for (int n = 0; n < 4; n++) {
+                const int i = 16 * n + lane / 4, k8 = lane % 4 * 8;
+                if (i < nv)
+                    st_global8<WIDE>(io.y, (row + i) * io.ldy + (size_t)head * DV + slice * 32 + k8,
+                                     *reinterpret_cast<const u32x4 *>(&yt[i * G::SX + k8]));
             }
         }
     }
@@ -415,11 +531,14 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart
     }
 }
 
-int heads_per_group(const gdnq_ssm_desc &d)
+// Heads per workgroup: as many as share B and C and fit its 8 waves, a power
+// of two; rows that need narrow accesses take one.
+int heads_per_group(const gdnq_ssm_desc &d, bool wide)
 {
-    const int per = d.hk ? d.H / d.hk : 1, most = d.dv == 64 ? 4 : 2;
-    for (int n = most; n > 1; n /= 2)
-        if (per % n == 0) return n;
+    const int per = d.hk ? d.H / d.hk : 1;
+    if (wide)
+        for (int n = d.dv == 64 ? 4 : 2; n > 1; n /= 2)
+            if (per % n == 0) return n;
     return 1;
 }
 
@@ -446,31 +565,33 @@ size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T)
 
 hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStream_t st)
 {
-    const int hk = d.hk ? d.hk : d.H, hpw = heads_per_group(d), sh = segment_shift(d, c.T);
-    const unsigned ids = segment_ids(c.n, c.T, sh), blocks = (unsigned)(d.H / hpw);
     const gdnq_ssm_io &io = c.io;
     const bool wide = wide_rows(io.x, io.ldx, 2) && wide_rows(io.B, io.ldb, 2) && wide_rows(io.C, io.ldc, 2) &&
                       wide_rows(io.y, io.ldy, 2);
-    const SsmArgs A{c, d.H, hk, sh, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0, wide,
+    const int hk = d.hk ? d.hk : d.H, hpw = heads_per_group(d, wide), sh = segment_shift(d, c.T);
+    const unsigned ids = segment_ids(c.n, c.T, sh), blocks = (unsigned)(d.H / hpw);
+    const SsmArgs A{c, d.H, hk, sh, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
                     make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
     return with_dims(d.dk, d.dv, [&](auto DK, auto DV) {
-        const auto go = [&](auto HPW) {
+        const auto go = [&](auto HPW, auto WIDE) {
             using G = SsmGeom<DK.value, DV.value, HPW.value>;
+            constexpr bool W = decltype(WIDE)::value;
             if (c.T > 1 << sh) {
-                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true>), dim3(ids * blocks),
+                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, W>), dim3(ids * blocks),
                                    dim3(G::NT), 0, st, A);
                 constexpr unsigned parts = DK.value * DV.value / 1024;
                 hipLaunchKernelGGL((ssm_join_kernel<DK.value * DV.value>), dim3((unsigned)c.n * d.H * parts), dim3(256),
                                    0, st, A, make_divisor(parts), make_divisor((unsigned)d.H));
             }
-            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false>), dim3(ids * blocks),
+            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, W>), dim3(ids * blocks),
                                dim3(G::NT), 0, st, A);
             return hipGetLastError();
         };
+        if (!wide) return go(std::integral_constant<int, 1>{}, std::false_type{});
         if constexpr (DV.value == 64)
-            if (hpw == 4) return go(std::integral_constant<int, 4>{});
-        if (hpw >= 2) return go(std::integral_constant<int, 2>{});
-        return go(std::integral_constant<int, 1>{});
+            if (hpw == 4) return go(std::integral_constant<int, 4>{}, std::true_type{});
+        if (hpw >= 2) return go(std::integral_constant<int, 2>{}, std::true_type{});
+        return go(std::integral_constant<int, 1>{}, std::true_type{});
     });
 }
 
