@@ -11,12 +11,13 @@
 //   Y = diag(e^{cs_i - cs_63}) (tril(C B^T) (w X) + C S') + D X,
 //   S <- S' + B^T (w X).
 // tril(C B^T) is the same for all heads that share B and C, so a workgroup
-// forms it once, and w X serves both lines.  A head whose chunk decays by
-// more than 2^-RANGE takes the first line as
-//   Y = (tril(C B^T) . e^{cs_i - cs_j} delta_j) X + diag(e^{cs_i}) C S + D X
-// instead, whose factors are all at most one.  Exponents are in base 2;
-// cs_63 - cs_j is summed over the tokens behind j, which keeps it exact where
-// it is small.
+// forms it once, and w X serves both lines.  With exponents in base 2 and
+// cs_63 > -RANGE every factor is in range; cs_63 - cs_j is summed over the
+// tokens behind j, which keeps it exact where it is small.  A head whose
+// chunk decays further, to -2 RANGE, counts the exponents from cs_63 / 2
+// instead of cs_63 and decays S by 2^{cs_63 / 2} before and after; beyond
+// that its outputs are formed from factors that are all at most one:
+//   Y = (tril(C B^T) . e^{cs_i - cs_j} delta_j) X + diag(e^{cs_i}) C S + D X.
 //
 // Precision: the products run on the bf16 matrix instructions with fp32
 // sums.  B, C and x are bf16, so C B^T is exact up to the sum.  The fp32
@@ -29,8 +30,13 @@
 // when the contraction index is taken in the accumulators' row order (slots
 // 0..3 of lane half h are rows 16t + 4h .. + 3, slots 4..7 rows 16t + 8 + 4h
 // .. + 3).  x and B are read by columns with the transposing LDS read.  A
-// workgroup holds up to 8 waves: HPW heads that share B and C.  The next
-// chunk's rows are loaded into registers while a chunk is computed.
+// workgroup holds up to 8 waves: HPW heads that share B and C.
+//
+// While chunk c is computed, the rows of B and C of chunk c+2 and of x of
+// chunk c+1 are on their way into registers, those of B and C of chunk c+1
+// go to the other half of their LDS buffers, and the waves form chunk c+1's
+// decays and, after a barrier in the middle, its tril(C B^T); a second
+// barrier ends the chunk.  x and y pass through LDS within each wave.
 //
 // Long sequences are cut into segments of 2^SH tokens (launch_ssm_prefill
 // says when): a first kernel forms each segment's own state and decay from
@@ -67,27 +73,29 @@ __device__ __forceinline__ floatx16 mma(bf16x8 a, bf16x8 b, floatx16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Inclusive prefix sum over the 64 lanes of a wave: shifts within rows of 16
-// lanes, then the last lane of rows 0 and 2 into rows 1 and 3, then lane 31
-// into rows 2 and 3.
-__device__ __forceinline__ float scan64(float x)
-{
-#define GDNQ_DPP(x, ctrl, rmask) \
-    __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, rmask, 0xf, true))
-    x += GDNQ_DPP(x, 0x111, 0xf);
-    x += GDNQ_DPP(x, 0x112, 0xf);
-    x += GDNQ_DPP(x, 0x114, 0xf);
-    x += GDNQ_DPP(x, 0x118, 0xf);
-    x += GDNQ_DPP(x, 0x142, 0xa);
-    x += GDNQ_DPP(x, 0x143, 0xc);
-#undef GDNQ_DPP
-    return x;
-}
-
 __device__ __forceinline__ float lane_of(float x, int lane)
 {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
 }
+
+// Sum over the lanes behind this one (exclusive), and over all: shifts down
+// within rows of 16 lanes, then the totals of the rows behind.
+__device__ __forceinline__ float suffix64(float x, int lane, float &total)
+{
+#define GDNQ_DPP(x, ctrl) \
+    __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xf, 0xf, true))
+    float s = GDNQ_DPP(x, 0x101);   // row_shl:1
+    s += GDNQ_DPP(s, 0x101);
+    s += GDNQ_DPP(s, 0x102);
+    s += GDNQ_DPP(s, 0x104);
+    s += GDNQ_DPP(s, 0x108);
+#undef GDNQ_DPP
+    const float t = s + x;   // lane 16 r: the total of row r
+    const float t3 = lane_of(t, 48), t2 = lane_of(t, 32) + t3, t1 = lane_of(t, 16) + t2;
+    total = lane_of(t, 0) + t1;
+    return s + (lane < 32 ? (lane < 16 ? t1 : t2) : (lane < 48 ? t3 : 0.0f));
+}
+
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
@@ -141,12 +149,13 @@ __device__ __forceinline__ bf16x8 ld_rows(const __bf16 *p)
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// 8 consecutive bf16 values of a token row, in one load where rows are WIDE
+// 8 consecutive bf16 values `off` bytes behind a uniform base, in one access
+// where rows are WIDE
 template <bool WIDE>
-__device__ __forceinline__ u32x4 ld_global8(const void *base, size_t off)
+__device__ __forceinline__ u32x4 ld_global8(const char *base, uint32_t off)
 {
-    const uint16_t *p = reinterpret_cast<const uint16_t *>(base) + off;
-    if constexpr (WIDE) return *reinterpret_cast<const u32x4 *>(p);
+    if constexpr (WIDE) return *reinterpret_cast<const u32x4 *>(base + off);
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(base + off);
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; i++) r[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
@@ -154,27 +163,28 @@ __device__ __forceinline__ u32x4 ld_global8(const void *base, size_t off)
 }
 
 template <bool WIDE>
-__device__ __forceinline__ void st_global8(void *base, size_t off, u32x4 v)
+__device__ __forceinline__ void st_global8(char *base, uint32_t off, u32x4 v)
 {
-    uint16_t *p = reinterpret_cast<uint16_t *>(base) + off;
-    if constexpr (WIDE) *reinterpret_cast<u32x4 *>(p) = v;
-    else
+    if constexpr (WIDE) *reinterpret_cast<u32x4 *>(base + off) = v;
+    else {
+        uint16_t *p = reinterpret_cast<uint16_t *>(base + off);
 #pragma unroll
         for (int i = 0; i < 4; i++) p[2 * i] = (uint16_t)v[i], p[2 * i + 1] = (uint16_t)(v[i] >> 16);
+    }
 }
 
 // Row strides in elements.  B is read by rows (C B^T) and by columns (the
 // state's update): a stride of 20 banks more than a multiple of 64 keeps the
 // row reads at two lanes per bank and the column reads below that.  C is
-// read by rows in 16-byte pieces (4 banks more), x by columns only (16 more).
+// read by rows in 16-byte pieces (4 banks more).  A wave's x tile has rows of
+// 16 banks, which its column reads cover without a pad.
 template <int DK, int DV, int HPW>
 struct SsmGeom {
     static constexpr int SL = DV / 32;           // waves per head
     static constexpr int NW = HPW * SL;
     static constexpr int NT = NW * 64;
-    static constexpr int SB = DK + 40, SC = DK + 8, SX = HPW * DV + (HPW * DV == 64 ? 40 : 32);
-    static constexpr int NB = CH * DK / 8 / NT;         // 16-byte pieces of B (and of C) per thread
-    static constexpr int NX = CH * HPW * DV / 8 / NT;   // and of x
+    static constexpr int SB = DK + 40, SC = DK + 8, SX = 32;
+    static constexpr int NB = CH * DK / 8 / NT;  // 16-byte pieces of B (and of C) per thread
     static constexpr int NBLK = DK / 32;
 };
 
@@ -182,28 +192,23 @@ struct SsmGeom {
 // other form cs and delta.
 enum { V_F, V_W, V_CS, V_D, V_N };
 
-// Chunks that decay to 2^-RANGE or less take the second form: 2^RANGE and
-// 2^-RANGE times any usual value, and its second bf16 part, are normal numbers.
+// 2^RANGE and 2^-RANGE times any usual value, and its second bf16 part, are
+// normal numbers.
 constexpr float RANGE = 80.0f;
+enum { NEAR, FAR, APART };   // cs_63 above -RANGE, above -2 RANGE, below
 
-template <class G>
+template <class G, bool STATE>
 struct SsmLds {
     static constexpr int HEADS = G::NW / G::SL;
-    __bf16 b[CH * G::SB];
-    __bf16 c[CH * G::SC];
-    __bf16 x[CH * G::SX];
+    __bf16 b[2][CH * G::SB];
+    __bf16 c[STATE ? 1 : 2][STATE ? 8 : CH * G::SC];
+    __bf16 x[G::NW][CH * G::SX];
     // tril(C B^T) as operands: rows 0..31 by tokens 0..15, 16..31, rows 32..63
     // by tokens 0..15, .., 48..63; each in two parts of 8 values per lane
-    alignas(16) __bf16 g[6][2][64 * 8];
+    alignas(16) __bf16 g[STATE ? 1 : 2][STATE ? 1 : 6][2][STATE ? 8 : 64 * 8];
     alignas(16) float v[2][HEADS][V_N][CH];
-    float tot[2][HEADS];
-    int far[2][HEADS];
-};
-
-// One chunk's rows on their way from memory to LDS.
-template <class G, bool STATE>
-struct SsmRows {
-    u32x4 b[G::NB], c[STATE ? 1 : G::NB], x[G::NX];
+    float tot[2][HEADS];   // the decay of S before the chunk's products (of FAR: also behind them)
+    int mode[2][HEADS];
 };
 
 // STATE: only the segment's own state and decay, from zero.
@@ -211,13 +216,16 @@ template <int DK, int DV, int HPW, bool STATE, bool WIDE>
 __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(SsmArgs A)
 {
     using G = SsmGeom<DK, DV, HPW>;
-    __shared__ SsmLds<G> L;
+    __shared__ SsmLds<G, STATE> L;
     const int t = (int)__builtin_amdgcn_workitem_id_x(), lane = t & 63;
     const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int hw = wv / G::SL, slice = wv % G::SL;
+    const int hw = wv % HPW, slice = wv / HPW;   // a head's first wave on each SIMD
+    // workgroups go to the 8 XCDs by turns: all head blocks of a segment are
+    // given numbers of one XCD, so that they read B and C from one L2
     const unsigned g = __builtin_amdgcn_workgroup_id_x();
-    const unsigned id = __builtin_amdgcn_readfirstlane(div_by(g, A.byHB));
-    const int h0 = (int)(g - id * A.byHB.d) * HPW, head = h0 + hw;
+    const unsigned round = __builtin_amdgcn_readfirstlane(div_by(g >> 3, A.byHB)), id = round * 8u + (g & 7u);
+    if (id >= A.ids) return;
+    const int h0 = (int)((g >> 3) - round * A.byHB.d) * HPW, head = h0 + hw;
     const int hb = h0 / (A.H / A.hk);
     const gdnq_ssm_io &io = A.c.io;
     SeqTile q;
@@ -245,23 +253,56 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
     const float Dh = io.D ? io.D[head] : 0.0f;
     float seglog = 0.0f;
 
-    // rows behind the segment's end repeat its last one; their weights are zero
-    SsmRows<G, STATE> R;
-    const auto fetch = [&](int c0) {
-        const int nv = min(CH, ntok - c0);
-        const size_t row = row0 + c0;
+    // the thread's 16-byte pieces of a chunk's rows, B and C dealt out over
+    // the workgroup, x's 32 columns over the wave, as byte offsets from the
+    // chunk's first row; rows behind the segment's end repeat its last one,
+    // with weights of zero
+    u32x4 rb[G::NB], rc[G::NB], rx[4];
+    constexpr int PK = DK / 8, RPI = G::NT / PK;   // pieces per row, rows per turn
+    const int br = t / PK;
+    uint32_t ob[G::NB], oc[G::NB], ox[4];
+    const uint32_t bcol = (uint32_t)(hb * DK + t % PK * 8), xcol = (uint32_t)(head * DV + slice * 32 + lane % 4 * 8);
+    const auto offsets_bc = [&](int nv) {
 #pragma unroll
         for (int i = 0; i < G::NB; i++) {
-            const int p = t + i * G::NT, k8 = p % (DK / 8);
-            const size_t src = row + min(p / (DK / 8), nv - 1), col = (size_t)hb * DK + k8 * 8;
-            R.b[i] = ld_global8<WIDE>(io.B, src * io.ldb + col);
-            if constexpr (!STATE) R.c[i] = ld_global8<WIDE>(io.C, src * io.ldc + col);
+            const uint32_t r = (uint32_t)min(br + i * RPI, nv - 1);
+            ob[i] = (r * (uint32_t)io.ldb + bcol) * 2u;
+            oc[i] = (r * (uint32_t)io.ldc + bcol) * 2u;
         }
+    };
+    const auto offsets_x = [&](int nv) {
 #pragma unroll
-        for (int i = 0; i < G::NX; i++) {
-            constexpr int PR = HPW * DV / 8;
-            const int p = t + i * G::NT;
-            R.x[i] = ld_global8<WIDE>(io.x, (row + min(p / PR, nv - 1)) * io.ldx + (size_t)h0 * DV + p % PR * 8);
+        for (int i = 0; i < 4; i++) ox[i] = ((uint32_t)min(16 * i + lane / 4, nv - 1) * (uint32_t)io.ldx + xcol) * 2u;
+    };
+    offsets_bc(min(CH, ntok));
+    offsets_x(min(CH, ntok));
+    const auto fetch = [&](int c0) {
+        if (ntok - c0 < CH) offsets_bc(ntok - c0);
+        const char *const pb = reinterpret_cast<const char *>(io.B) + (row0 + c0) * io.ldb * 2;
+        const char *const pc = reinterpret_cast<const char *>(io.C) + (row0 + c0) * io.ldc * 2;
+#pragma unroll
+        for (int i = 0; i < G::NB; i++) {
+            rb[i] = ld_global8<WIDE>(pb, ob[i]);
+            if constexpr (!STATE) rc[i] = ld_global8<WIDE>(pc, oc[i]);
+        }
+    };
+    const auto fetch_x = [&](int c0) {
+        if (ntok - c0 < CH) offsets_x(ntok - c0);
+        const char *const px = reinterpret_cast<const char *>(io.x) + (row0 + c0) * io.ldx * 2;
+#pragma unroll
+        for (int i = 0; i < 4; i++) rx[i] = ld_global8<WIDE>(px, ox[i]);
+    };
+    const auto stage = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < G::NB; i++) {
+            const int r = br + i * RPI, k8 = t % PK;
+            *reinterpret_cast<u32x4 *>(&L.b[buf][r * G::SB + k8 * 8]) = rb[i];
+            if constexpr (!STATE) {
+                // columns of each 16 in the order 0-3, 8-11, 4-7, 12-15
+                __bf16 *d = &L.c[buf][r * G::SC + (k8 & ~1) * 8 + (k8 & 1) * 4];
+                *reinterpret_cast<uint2 *>(d) = make_uint2(rc[i][0], rc[i][1]);
+                *reinterpret_cast<uint2 *>(d + 8) = make_uint2(rc[i][2], rc[i][3]);
+            }
         }
     };
     float dt_in = 0.0f;
@@ -274,97 +315,94 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         if (A.sp) d = softplus(d);
         d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
         const float la = d * Ah;
-        const float suf = __shfl(scan64(__shfl(la, 63 - lane)), 63 - lane) - la;   // the tokens behind this one
-        const float cs = scan64(la), tot = lane_of(cs, 63);
-        const bool far = !(tot > -RANGE);
+        float tot;
+        const float suf = suffix64(la, lane, tot);   // cs_63 - cs
+        const int mode = STATE || tot > -RANGE ? NEAR : tot > -2.0f * RANGE ? FAR : APART;
+        const float half = 0.5f * tot;
         float(&v)[V_N][CH] = L.v[buf][hw];
-        v[V_W][lane] = __builtin_amdgcn_exp2f(suf) * d;
+        v[V_W][lane] = __builtin_amdgcn_exp2f(mode == FAR ? suf - half : suf) * d;
         if constexpr (!STATE) {
-            v[V_F][lane] = __builtin_amdgcn_exp2f(far ? cs : -suf);
-            v[V_CS][lane] = cs;
+            v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : (mode == FAR ? half : tot) - suf);
+            v[V_CS][lane] = tot - suf;
             v[V_D][lane] = d;
         }
         seglog += tot;
         if (lane == 0) {
-            L.tot[buf][hw] = __builtin_amdgcn_exp2f(tot);
-            L.far[buf][hw] = far;
+            L.tot[buf][hw] = __builtin_amdgcn_exp2f(mode == FAR ? half : tot);
+            L.mode[buf][hw] = mode;
+        }
+    };
+
+    // tril(C B^T) of the chunk in buf: the 10 blocks of 16 x 16 tokens on and below the diagonal, by turns
+    const auto triangle = [&](int buf) {
+        const int l16 = lane & 15, qd = lane >> 4;
+        for (int n = G::NW - 1 - wv; n < 10; n += G::NW) {
+            const int I = (int)((0x3333222110ull >> (4 * n)) & 15u), J = (int)((0x3210210100ull >> (4 * n)) & 15u);
+            floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < DK / 32; s++) {
+                const bf16x8 bj = ld_rows(&L.b[buf][(16 * J + l16) * G::SB + 32 * s + 16 * (qd / 2) + 4 * (qd & 1)]);
+                const bf16x8 ci = *reinterpret_cast<const bf16x8 *>(&L.c[buf][(16 * I + l16) * G::SC + 32 * s + 8 * qd]);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bj, ci, acc, 0, 0, 0);
+            }
+            // row 4 qd + r of the block is token j, lane l16 token i
+            float m[4];
+            uint32_t part[2][2];
+#pragma unroll
+            for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
+            split<2, 4>(m, part);
+            const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
+#pragma unroll
+            for (int p = 0; p < 2; p++)
+                *reinterpret_cast<uint2 *>(&L.g[buf][f][p][at]) = make_uint2(part[p][0], part[p][1]);
         }
     };
 
     if constexpr (!STATE) {   // the blocks above the diagonal stay zero
-        for (int i = t; i < 6 * 2 * 64; i += G::NT) *reinterpret_cast<uint4 *>(&L.g[0][0][i * 8]) = make_uint4(0, 0, 0, 0);
+        for (int i = t; i < 2 * 6 * 2 * 64; i += G::NT)
+            *reinterpret_cast<uint4 *>(&L.g[0][0][0][i * 8]) = make_uint4(0, 0, 0, 0);
     }
     fetch_dt(0);
     fetch(0);
-    if (slice == 0) decays(min(CH, ntok), 0);
-    if (CH < ntok) fetch_dt(CH);
+    fetch_x(0);
+    if (slice == 0) {
+        decays(min(CH, ntok), 0);
+        if (CH < ntok) fetch_dt(CH);
+    }
+    stage(0);
+    if (CH < ntok) fetch(CH);
+    if constexpr (!STATE) {
+        __syncthreads();
+        triangle(0);
+    }
     int buf = 0;
     for (int c0 = 0; c0 < ntok; c0 += CH, buf ^= 1) {
         const int nv = min(CH, ntok - c0);
         const size_t row = row0 + c0;
-        __syncthreads();   // the previous chunk's reads are done
-#pragma unroll
-        for (int i = 0; i < G::NB; i++) {
-            const int p = t + i * G::NT, r = p / (DK / 8), k8 = p % (DK / 8);
-            *reinterpret_cast<u32x4 *>(&L.b[r * G::SB + k8 * 8]) = R.b[i];
-            if constexpr (!STATE) {
-                // columns of each 16 in the order 0-3, 8-11, 4-7, 12-15
-                __bf16 *d = &L.c[r * G::SC + (k8 & ~1) * 8 + (k8 & 1) * 4];
-                *reinterpret_cast<uint2 *>(d) = make_uint2(R.c[i][0], R.c[i][1]);
-                *reinterpret_cast<uint2 *>(d + 8) = make_uint2(R.c[i][2], R.c[i][3]);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < G::NX; i++) {
-            constexpr int PR = HPW * DV / 8;
-            const int p = t + i * G::NT;
-            *reinterpret_cast<u32x4 *>(&L.x[p / PR * G::SX + p % PR * 8]) = R.x[i];
-        }
-        __syncthreads();
         const bool more = c0 + CH < ntok;
-        if (more) fetch(c0 + CH);
-
-        // ---- the first wave of a head forms the next chunk's decays, the others
-        // tril(C B^T): the 10 blocks of 16 x 16 tokens on and below the diagonal, by turns
-        if (slice == 0) {
-            if (more) {
-                decays(min(CH, ntok - c0 - CH), buf ^ 1);
-                if (c0 + 2 * CH < ntok) fetch_dt(c0 + 2 * CH);
-            }
-        } else if constexpr (!STATE) {
-            const int l16 = lane & 15, qd = lane >> 4;
-            for (int n = hw * (G::SL - 1) + slice - 1; n < 10; n += HPW * (G::SL - 1)) {
-                const int I = (int)((0x3333222110ull >> (4 * n)) & 15u), J = (int)((0x3210210100ull >> (4 * n)) & 15u);
-                floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();   // chunk c0 is staged, and the previous one's buffers are free
+        if (more) stage(buf ^ 1);
+        if (c0 + 2 * CH < ntok) fetch(c0 + 2 * CH);
+        __bf16 *const xt = L.x[wv];
 #pragma unroll
-                for (int s = 0; s < DK / 32; s++) {
-                    const bf16x8 bj = ld_rows(&L.b[(16 * J + l16) * G::SB + 32 * s + 16 * (qd / 2) + 4 * (qd & 1)]);
-                    const bf16x8 ci = *reinterpret_cast<const bf16x8 *>(&L.c[(16 * I + l16) * G::SC + 32 * s + 8 * qd]);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bj, ci, acc, 0, 0, 0);
-                }
-                // row 4 qd + r of the block is token j, lane l16 token i
-                float m[4];
-                uint32_t part[2][2];
-#pragma unroll
-                for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
-                split<2, 4>(m, part);
-                const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
-#pragma unroll
-                for (int p = 0; p < 2; p++)
-                    *reinterpret_cast<uint2 *>(&L.g[f][p][at]) = make_uint2(part[p][0], part[p][1]);
-            }
+        for (int i = 0; i < 4; i++) *reinterpret_cast<u32x4 *>(&xt[(64 * i + lane) * 8]) = rx[i];
+        if (more) fetch_x(c0 + CH);
+        if (slice == 0 && more) {
+            decays(min(CH, ntok - c0 - CH), buf ^ 1);
+            if (c0 + 2 * CH < ntok) fetch_dt(c0 + 2 * CH);
         }
-        if constexpr (!STATE) __syncthreads();
+        wave_lds_sync();
 
         const int l16 = lane & 15;
         const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
         const float(&vec)[V_N][CH] = L.v[buf][hw];
         const float tot = L.tot[buf][hw];
-        const bool far = !STATE && __builtin_amdgcn_readfirstlane(L.far[buf][hw]);
+        const int mode = STATE ? NEAR : __builtin_amdgcn_readfirstlane(L.mode[buf][hw]);
+        const bool apart = mode == APART;
         bf16x8 xf[4];   // x rows 16 f .. + 15, the wave's columns
 #pragma unroll
         for (int f = 0; f < 4; f++)
-            xf[f] = ld_cols(&L.x[(16 * f + tr_r) * G::SX + hw * DV + slice * 32 + tr_c], G::SX);
+            xf[f] = ld_cols(&xt[(16 * f + tr_r) * G::SX + tr_c], G::SX);
 
         const auto decay_state = [&] {
 #pragma unroll
@@ -382,14 +420,14 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                     Y[ib][4 * k] *= e.x, Y[ib][4 * k + 1] *= e.y, Y[ib][4 * k + 2] *= e.z, Y[ib][4 * k + 3] *= e.w;
                 }
         };
-        if (!far) decay_state();
+        if (!apart) decay_state();
         if constexpr (!STATE) {
 #pragma unroll
             for (int r = 0; r < 16; r++) Y[0][r] = Y[1][r] = 0.0f;
 #pragma unroll
             for (int s = 0; s < DK / 16; s++) {
-                const bf16x8 ca = *reinterpret_cast<const bf16x8 *>(&L.c[c * G::SC + 16 * s + 8 * hh]);
-                const bf16x8 cb = *reinterpret_cast<const bf16x8 *>(&L.c[(32 + c) * G::SC + 16 * s + 8 * hh]);
+                const bf16x8 ca = *reinterpret_cast<const bf16x8 *>(&L.c[buf][c * G::SC + 16 * s + 8 * hh]);
+                const bf16x8 cb = *reinterpret_cast<const bf16x8 *>(&L.c[buf][(32 + c) * G::SC + 16 * s + 8 * hh]);
                 float sv[8];
                 uint32_t part[2][4];
 #pragma unroll
@@ -400,13 +438,13 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                 Y[0] = mma(ca, operand(part[1]), Y[0]);
                 Y[1] = mma(cb, operand(part[1]), Y[1]);
             }
-            if (far) {
+            if (apart) {
                 scale_rows();
 #pragma unroll
                 for (int fr = 0; fr < 6; fr++) {
                     const int ib = fr >= 2, f = ib ? fr - 2 : fr;
-                    const u32x4 gh = *reinterpret_cast<const u32x4 *>(&L.g[fr][0][lane * 8]);
-                    const u32x4 gl = *reinterpret_cast<const u32x4 *>(&L.g[fr][1][lane * 8]);
+                    const u32x4 gh = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][0][lane * 8]);
+                    const u32x4 gl = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][1][lane * 8]);
                     const float ci = vec[V_CS][32 * ib + c];
                     float m[8];
                     uint32_t part[2][4];
@@ -425,6 +463,10 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                 decay_state();
             }
         }
+        if constexpr (!STATE) {
+            __syncthreads();   // chunk c0 + CH is staged
+            if (more) triangle(buf ^ 1);
+        }
         // ---- S' + B^T (w x), and tril(C B^T) (w x)
 #pragma unroll
         for (int f = 0; f < 4; f++) {
@@ -442,12 +484,12 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             split<3, 8>(wx, part);
             const bf16x8 xh = operand(part[0]), xm = operand(part[1]), xl = operand(part[2]);
             if constexpr (!STATE) {
-                if (!far)
+                if (!apart)
 #pragma unroll
                     for (int ib = f / 2; ib < 2; ib++) {
                         const int fr = ib ? 2 + f : f;
-                        const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[fr][0][lane * 8]);
-                        const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[fr][1][lane * 8]);
+                        const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][0][lane * 8]);
+                        const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][1][lane * 8]);
                         Y[ib] = mma(gh, xh, Y[ib]);
                         Y[ib] = mma(gl, xh, Y[ib]);
                         Y[ib] = mma(gh, xm, Y[ib]);
@@ -455,18 +497,18 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             }
 #pragma unroll
             for (int nb = 0; nb < G::NBLK; nb++) {
-                const bf16x8 bt = ld_cols(&L.b[(16 * f + tr_r) * G::SB + 32 * nb + tr_c], G::SB);
+                const bf16x8 bt = ld_cols(&L.b[buf][(16 * f + tr_r) * G::SB + 32 * nb + tr_c], G::SB);
                 S[nb] = mma(bt, xh, S[nb]);
                 S[nb] = mma(bt, xm, S[nb]);
                 S[nb] = mma(bt, xl, S[nb]);
             }
         }
+        if (mode == FAR) decay_state();
         if constexpr (!STATE) {
-            if (!far) scale_rows();
-            // ---- y = Y + D x, through the wave's own columns of the x tile: neighbouring lanes trade
+            if (!apart) scale_rows();
+            // ---- y = Y + D x, through the wave's x tile: neighbouring lanes trade
             // halves so that each writes two columns of a row, and rows leave in 16-byte pieces
             const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
-            __bf16 *const yt = &L.x[hw * DV + slice * 32];
             wave_lds_sync();
 #pragma unroll
             for (int ib = 0; ib < 2; ib++)
@@ -476,15 +518,16 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                     const uint32_t u = pack2(fmaf(Dh, low_of(xr), Y[ib][r]), fmaf(Dh, high_of(xr), Y[ib][r + 1]));
                     const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
                     const int i = 32 * ib + 8 * (r / 4) + r % 4 + 4 * hh + (lane & 1);
-                    *reinterpret_cast<uint32_t *>(&yt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
+                    *reinterpret_cast<uint32_t *>(&xt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
                 }
             wave_lds_sync();
+            char *const py = reinterpret_cast<char *>(io.y) + row * io.ldy * 2;
 #pragma unroll
             for (int n = 0; n < 4; n++) {
-                const int i = 16 * n + lane / 4, k8 = lane % 4 * 8;
+                const int i = 16 * n + lane / 4;
                 if (i < nv)
-                    st_global8<WIDE>(io.y, (row + i) * io.ldy + (size_t)head * DV + slice * 32 + k8,
-                                     *reinterpret_cast<const u32x4 *>(&yt[i * G::SX + k8]));
+                    st_global8<WIDE>(py, ((uint32_t)i * (uint32_t)io.ldy + xcol) * 2u,
+                                     *reinterpret_cast<const u32x4 *>(&xt[(64 * n + lane) * 8]));
             }
         }
     }
@@ -577,13 +620,13 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
             using G = SsmGeom<DK.value, DV.value, HPW.value>;
             constexpr bool W = decltype(WIDE)::value;
             if (c.T > 1 << sh) {
-                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, W>), dim3(ids * blocks),
+                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, W>), dim3((ids + 7) / 8 * 8 * blocks),
                                    dim3(G::NT), 0, st, A);
                 constexpr unsigned parts = DK.value * DV.value / 1024;
                 hipLaunchKernelGGL((ssm_join_kernel<DK.value * DV.value>), dim3((unsigned)c.n * d.H * parts), dim3(256),
                                    0, st, A, make_divisor(parts), make_divisor((unsigned)d.H));
             }
-            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, W>), dim3(ids * blocks),
+            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, W>), dim3((ids + 7) / 8 * 8 * blocks),
                                dim3(G::NT), 0, st, A);
             return hipGetLastError();
         };
