@@ -127,7 +127,7 @@ int gdnq_ssm_workspace(const gdnq_ssm_desc *desc, int32_t n_seqs, int32_t T, siz
  * Packed prompts.  S: device fp32 [n_slots,H,dk,dv], the pool of states (the
  * layout of gdnq.h's fp32 states); each sequence's slot is replaced by its
  * state after the last token.  io_dtype must be GDNQ_IO_BF16
- * and rows at most 2^23 elements apart (GDNQ_EUNSUPPORTED otherwise).  Runs
+ * and rows at most 2^22 elements apart (GDNQ_EUNSUPPORTED otherwise).  Runs
  * chunk by chunk on the matrix cores,
  * fp32 operands split into bf16 parts (two for outputs, three for states).
  * workspace: device, 16-byte aligned, at least gdnq_ssm_workspace bytes

@@ -250,9 +250,9 @@ int gdnq_ssm_prefill(const gdnq_ssm_desc *desc, const gdnq_ssm_io *io, float *S,
     Spans sp;
     TRY(check_packed(cont, cu_seqlens, n_seqs, sp));
     TRY(check_ssm_call(*desc, c, T, sp));
-    const int64_t far = 1 << 23;   // a chunk's rows are addressed by 32-bit offsets
-    if (c.io.ldx > far || c.io.ldb > far || c.io.ldc > far || c.io.ldy > far)
-        return fail(GDNQ_EUNSUPPORTED, "gdnq_ssm_prefill takes rows at most 2^23 elements apart");
+    const int64_t far = 1 << 22;   // a chunk's rows are addressed by 32-bit offsets
+    if (c.io.ldx > far || c.io.ldb > far || c.io.ldc > far || c.io.ldy > far || c.io.lddt > far)
+        return fail(GDNQ_EUNSUPPORTED, "gdnq_ssm_prefill takes rows at most 2^22 elements apart");
     const size_t need = gdnq::ssm_workspace(*desc, n_seqs, T);
     if (workspace_bytes < need)
         return fail(GDNQ_EINVAL, "workspace of %zu bytes is too small (%zu are needed)", workspace_bytes, need);

@@ -32,11 +32,11 @@
 // .. + 3).  x and B are read by columns with the transposing LDS read.  A
 // workgroup holds up to 8 waves: HPW heads that share B and C.
 //
-// While chunk c is computed, the rows of B and C of chunk c+2 and of x of
-// chunk c+1 are on their way into registers, those of B and C of chunk c+1
-// go to the other half of their LDS buffers, and the waves form chunk c+1's
-// decays and, after a barrier in the middle, its tril(C B^T); a second
-// barrier ends the chunk.  x and y pass through LDS within each wave.
+// While chunk c is computed, the next one is prepared: its rows of B and C are
+// on their way into registers in the first half (C S) and go to the other
+// half of their LDS buffers before a barrier in the middle, behind which the
+// waves form its tril(C B^T) and load its x; the heads' first waves form its
+// decays.  x and y pass through LDS within each wave.
 //
 // Long sequences are cut into segments of 2^SH tokens (launch_ssm_prefill
 // says when): a first kernel forms each segment's own state and decay from
@@ -76,6 +76,16 @@ __device__ __forceinline__ floatx16 mma(bf16x8 a, bf16x8 b, floatx16 c)
 __device__ __forceinline__ float lane_of(float x, int lane)
 {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+}
+
+// A row of a chunk times a distance below 2^24 bytes; the masks tell the
+// compiler that the 24-bit multiplier does.
+__device__ __forceinline__ uint32_t row_bytes(uint32_t row, uint32_t ld) { return (row & 63u) * (ld & 0xFFFFFFu); }
+
+// a value that is the same in every lane, in a scalar register
+__device__ __forceinline__ float uniform(float x)
+{
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
 }
 
 // Sum over the lanes behind this one (exclusive), and over all: shifts down
@@ -249,48 +259,47 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
 #pragma unroll
             for (int r = 0; r < 16; r++) S[nb][r] = load ? from[(size_t)(32 * nb + 8 * (r / 4) + r % 4) * DV] : 0.0f;
     }
-    const float Ah = io.A[head] * 1.44269504f, bias = io.dt_bias ? io.dt_bias[head] : 0.0f;
-    const float Dh = io.D ? io.D[head] : 0.0f;
+    const float Ah = uniform(io.A[head] * 1.44269504f), bias = uniform(io.dt_bias ? io.dt_bias[head] : 0.0f);
+    const float Dh = uniform(io.D ? io.D[head] : 0.0f);
     float seglog = 0.0f;
 
     // the thread's 16-byte pieces of a chunk's rows, B and C dealt out over
-    // the workgroup, x's 32 columns over the wave, as byte offsets from the
-    // chunk's first row; rows behind the segment's end repeat its last one,
-    // with weights of zero
+    // the workgroup, x's 32 columns over the wave; rows behind the segment's
+    // end repeat its last one, with weights of zero.  Byte offsets from the
+    // chunk's first row: a row number below 64 times a distance below 2^24.
     u32x4 rb[G::NB], rc[G::NB], rx[4];
     constexpr int PK = DK / 8, RPI = G::NT / PK;   // pieces per row, rows per turn
     const int br = t / PK;
-    uint32_t ob[G::NB], oc[G::NB], ox[4];
-    const uint32_t bcol = (uint32_t)(hb * DK + t % PK * 8), xcol = (uint32_t)(head * DV + slice * 32 + lane % 4 * 8);
-    const auto offsets_bc = [&](int nv) {
+    const uint32_t bcol = (uint32_t)(hb * DK + t % PK * 8) * 2u;
+    const uint32_t xcol = (uint32_t)(head * DV + slice * 32 + lane % 4 * 8) * 2u;
+    // each of these advances by a chunk with every call
+    const uint32_t ldb = (uint32_t)io.ldb * 2u, ldc = (uint32_t)io.ldc * 2u, ldx = (uint32_t)io.ldx * 2u,
+                   ldy = (uint32_t)io.ldy * 2u, ldt = (uint32_t)io.lddt * 2u;
+    const char *pb = reinterpret_cast<const char *>(io.B) + row0 * ldb;
+    const char *pc = reinterpret_cast<const char *>(io.C) + row0 * ldc;
+    const char *px = reinterpret_cast<const char *>(io.x) + row0 * ldx;
+    const char *pt = reinterpret_cast<const char *>(io.dt) + row0 * ldt + (size_t)head * 2;
+    char *py = reinterpret_cast<char *>(io.y) + row0 * ldy;
+    const auto fetch = [&](int nv) {
 #pragma unroll
         for (int i = 0; i < G::NB; i++) {
             const uint32_t r = (uint32_t)min(br + i * RPI, nv - 1);
-            ob[i] = (r * (uint32_t)io.ldb + bcol) * 2u;
-            oc[i] = (r * (uint32_t)io.ldc + bcol) * 2u;
+            rb[i] = ld_global8<WIDE>(pb, row_bytes(r, ldb) + bcol);
+            if constexpr (!STATE) rc[i] = ld_global8<WIDE>(pc, row_bytes(r, ldc) + bcol);
         }
+        pb += (size_t)CH * ldb;
+        pc += (size_t)CH * ldc;
     };
-    const auto offsets_x = [&](int nv) {
+    const auto fetch_x = [&](int nv) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) ox[i] = ((uint32_t)min(16 * i + lane / 4, nv - 1) * (uint32_t)io.ldx + xcol) * 2u;
+        for (int i = 0; i < 4; i++)
+            rx[i] = ld_global8<WIDE>(px, row_bytes((uint32_t)min(16 * i + lane / 4, nv - 1), ldx) + xcol);
+        px += (size_t)CH * ldx;
     };
-    offsets_bc(min(CH, ntok));
-    offsets_x(min(CH, ntok));
-    const auto fetch = [&](int c0) {
-        if (ntok - c0 < CH) offsets_bc(ntok - c0);
-        const char *const pb = reinterpret_cast<const char *>(io.B) + (row0 + c0) * io.ldb * 2;
-        const char *const pc = reinterpret_cast<const char *>(io.C) + (row0 + c0) * io.ldc * 2;
-#pragma unroll
-        for (int i = 0; i < G::NB; i++) {
-            rb[i] = ld_global8<WIDE>(pb, ob[i]);
-            if constexpr (!STATE) rc[i] = ld_global8<WIDE>(pc, oc[i]);
-        }
-    };
-    const auto fetch_x = [&](int c0) {
-        if (ntok - c0 < CH) offsets_x(ntok - c0);
-        const char *const px = reinterpret_cast<const char *>(io.x) + (row0 + c0) * io.ldx * 2;
-#pragma unroll
-        for (int i = 0; i < 4; i++) rx[i] = ld_global8<WIDE>(px, ox[i]);
+    uint32_t dt_in = 0;
+    const auto fetch_dt = [&](int nv) {   // widened at its use, or it would be waited for here
+        if (slice == 0) dt_in = *reinterpret_cast<const uint16_t *>(pt + row_bytes((uint32_t)min(lane, nv - 1), ldt));
+        pt += (size_t)CH * ldt;
     };
     const auto stage = [&](int buf) {
 #pragma unroll
@@ -305,13 +314,9 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             }
         }
     };
-    float dt_in = 0.0f;
-    const auto fetch_dt = [&](int c0) {
-        if (slice == 0) dt_in = load1<true>(io.dt, (row0 + c0 + min(lane, ntok - c0 - 1)) * io.lddt + head);
-    };
     // decays of a chunk: one wave per head, one token per lane
-    const auto decays = [&](int nv, int buf) {
-        float d = dt_in + bias;
+    const auto decays = [&](uint32_t dt, int nv, int buf) {
+        float d = low_of(dt) + bias;
         if (A.sp) d = softplus(d);
         d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
         const float la = d * Ah;
@@ -333,70 +338,82 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         }
     };
 
-    // tril(C B^T) of the chunk in buf: the 10 blocks of 16 x 16 tokens on and below the diagonal, by turns
-    const auto triangle = [&](int buf) {
-        const int l16 = lane & 15, qd = lane >> 4;
-        for (int n = G::NW - 1 - wv; n < 10; n += G::NW) {
-            const int I = (int)((0x3333222110ull >> (4 * n)) & 15u), J = (int)((0x3210210100ull >> (4 * n)) & 15u);
-            floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    // tril(C B^T) of the chunk in buf: block n of the 10 blocks of 16 x 16 tokens
+    // on and below the diagonal, transposed, and its way into the operands
+    const int l16 = lane & 15, qd = lane >> 4;
+    const auto tri_i = [](int n) { return (int)((0x3333222110ull >> (4 * n)) & 15u); };
+    const auto tri_j = [](int n) { return (int)((0x3210210100ull >> (4 * n)) & 15u); };
+    const auto triangle = [&](int buf, int n) {
+        const __bf16 *pb = &L.b[buf][(16 * tri_j(n) + l16) * G::SB + 16 * (qd / 2) + 4 * (qd & 1)];
+        const __bf16 *pc = &L.c[buf][(16 * tri_i(n) + l16) * G::SC + 8 * qd];
+        floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int s = 0; s < DK / 32; s++) {
-                const bf16x8 bj = ld_rows(&L.b[buf][(16 * J + l16) * G::SB + 32 * s + 16 * (qd / 2) + 4 * (qd & 1)]);
-                const bf16x8 ci = *reinterpret_cast<const bf16x8 *>(&L.c[buf][(16 * I + l16) * G::SC + 32 * s + 8 * qd]);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bj, ci, acc, 0, 0, 0);
-            }
-            // row 4 qd + r of the block is token j, lane l16 token i
-            float m[4];
-            uint32_t part[2][2];
-#pragma unroll
-            for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
-            split<2, 4>(m, part);
-            const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
-#pragma unroll
-            for (int p = 0; p < 2; p++)
-                *reinterpret_cast<uint2 *>(&L.g[buf][f][p][at]) = make_uint2(part[p][0], part[p][1]);
-        }
+        for (int s = 0; s < DK / 32; s++)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ld_rows(pb + 32 * s),
+                                                          *reinterpret_cast<const bf16x8 *>(pc + 32 * s), acc, 0, 0, 0);
+        return acc;
     };
+    const auto put_triangle = [&](int buf, int n, floatx4 acc) {
+        const int I = tri_i(n), J = tri_j(n);   // row 4 qd + r of the block is token j, lane l16 token i
+        float m[4];
+        uint32_t part[2][2];
+#pragma unroll
+        for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
+        split<2, 4>(m, part);
+        const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
+#pragma unroll
+        for (int p = 0; p < 2; p++)
+            *reinterpret_cast<uint2 *>(&L.g[buf][f][p][at]) = make_uint2(part[p][0], part[p][1]);
+    };
+    const int n0 = G::NW - 1 - wv;   // the wave's first block; the others follow NW apart
 
     if constexpr (!STATE) {   // the blocks above the diagonal stay zero
         for (int i = t; i < 2 * 6 * 2 * 64; i += G::NT)
             *reinterpret_cast<uint4 *>(&L.g[0][0][0][i * 8]) = make_uint4(0, 0, 0, 0);
     }
-    fetch_dt(0);
-    fetch(0);
-    fetch_x(0);
-    if (slice == 0) {
-        decays(min(CH, ntok), 0);
-        if (CH < ntok) fetch_dt(CH);
-    }
+    fetch_dt(min(CH, ntok));
+    fetch(min(CH, ntok));
+    fetch_x(min(CH, ntok));
+    if (slice == 0) decays(dt_in, min(CH, ntok), 0);
     stage(0);
-    if (CH < ntok) fetch(CH);
+    if (CH < ntok) fetch_dt(min(CH, ntok - CH));
     if constexpr (!STATE) {
         __syncthreads();
-        triangle(0);
+        for (int n = n0; n < 10; n += G::NW) put_triangle(0, n, triangle(0, n));
     }
+    // a chunk's outputs wait in the wave's x tile until the next chunk begins:
+    // there the loads of a chunk ago have long arrived, so that nothing waits for the stores
+    __bf16 *const xt = L.x[wv];
+    u32x4 yo[4];
+    const auto load_y = [&] {
+#pragma unroll
+        for (int n = 0; n < 4; n++) yo[n] = *reinterpret_cast<const u32x4 *>(&xt[(64 * n + lane) * 8]);
+    };
+    const auto store_y = [&](int nv) {
+#pragma unroll
+        for (int n = 0; n < 4; n++)
+            if (nv == CH || 16 * n + lane / 4 < nv)
+                st_global8<WIDE>(py, row_bytes((uint32_t)(16 * n + lane / 4), ldy) + xcol, yo[n]);
+        py += (size_t)CH * ldy;
+    };
     int buf = 0;
-    for (int c0 = 0; c0 < ntok; c0 += CH, buf ^= 1) {
-        const int nv = min(CH, ntok - c0);
-        const size_t row = row0 + c0;
-        const bool more = c0 + CH < ntok;
-        __syncthreads();   // chunk c0 is staged, and the previous one's buffers are free
-        if (more) stage(buf ^ 1);
-        if (c0 + 2 * CH < ntok) fetch(c0 + 2 * CH);
-        __bf16 *const xt = L.x[wv];
+    for (int left = ntok; left > 0; left -= CH, buf ^= 1) {
+        const bool more = left > CH;
+        __syncthreads();   // the chunk is staged, and the previous one's buffers are free
+        if constexpr (!STATE) load_y();
+        wave_lds_sync();
 #pragma unroll
         for (int i = 0; i < 4; i++) *reinterpret_cast<u32x4 *>(&xt[(64 * i + lane) * 8]) = rx[i];
-        if (more) fetch_x(c0 + CH);
-        if (slice == 0 && more) {
-            decays(min(CH, ntok - c0 - CH), buf ^ 1);
-            if (c0 + 2 * CH < ntok) fetch_dt(c0 + 2 * CH);
-        }
+        uint32_t dt_now = dt_in;
+        asm volatile("" : "+v"(dt_now));   // arrived as well, before stores and new loads are on their way
+        if (!STATE && left < ntok) store_y(CH);
+        if (more) fetch(min(CH, left - CH));
+        if (slice == 0 && more) decays(dt_now, min(CH, left - CH), buf ^ 1);
         wave_lds_sync();
 
-        const int l16 = lane & 15;
         const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
         const float(&vec)[V_N][CH] = L.v[buf][hw];
-        const float tot = L.tot[buf][hw];
+        const float tot = uniform(L.tot[buf][hw]);
         const int mode = STATE ? NEAR : __builtin_amdgcn_readfirstlane(L.mode[buf][hw]);
         const bool apart = mode == APART;
         bf16x8 xf[4];   // x rows 16 f .. + 15, the wave's columns
@@ -418,6 +435,22 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                 for (int k = 0; k < 4; k++) {
                     const float4 e = *reinterpret_cast<const float4 *>(&vec[V_F][32 * ib + 8 * k + 4 * hh]);
                     Y[ib][4 * k] *= e.x, Y[ib][4 * k + 1] *= e.y, Y[ib][4 * k + 2] *= e.z, Y[ib][4 * k + 3] *= e.w;
+                }
+        };
+        const auto output = [&] {
+            // y = Y + D x to the wave's x tile; neighbouring lanes trade halves so
+            // that each writes two columns of a row
+            const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
+            wave_lds_sync();
+#pragma unroll
+            for (int ib = 0; ib < 2; ib++)
+#pragma unroll
+                for (int r = 0; r < 16; r += 2) {
+                    const uint32_t xr = __builtin_bit_cast(u32x4, xf[2 * ib + r / 8])[r % 8 / 2];
+                    const uint32_t u = pack2(fmaf(Dh, low_of(xr), Y[ib][r]), fmaf(Dh, high_of(xr), Y[ib][r + 1]));
+                    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
+                    const int i = 32 * ib + 8 * (r / 4) + r % 4 + 4 * hh + (lane & 1);
+                    *reinterpret_cast<uint32_t *>(&xt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
                 }
         };
         if (!apart) decay_state();
@@ -460,14 +493,19 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                     Y[ib] = mma(operand(part[0]), xf[f], Y[ib]);
                     Y[ib] = mma(operand(part[1]), xf[f], Y[ib]);
                 }
+                output();
                 decay_state();
             }
         }
+        floatx4 tri = {};
         if constexpr (!STATE) {
-            __syncthreads();   // chunk c0 + CH is staged
-            if (more) triangle(buf ^ 1);
+            if (more) stage(buf ^ 1);
+            __syncthreads();   // the next chunk is staged (if there is one: the blocks of a chunk behind the last are not used)
         }
-        // ---- S' + B^T (w x), and tril(C B^T) (w x)
+        if (left > 2 * CH) fetch_dt(min(CH, left - 2 * CH));
+        if (more) fetch_x(min(CH, left - CH));
+        if constexpr (!STATE) tri = triangle(buf ^ 1, n0);
+        // ---- S' + B^T (w x), and tril(C B^T) (w x) (not used of a chunk set APART)
 #pragma unroll
         for (int f = 0; f < 4; f++) {
             const u32x4 xr = __builtin_bit_cast(u32x4, xf[f]);
@@ -484,16 +522,15 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             split<3, 8>(wx, part);
             const bf16x8 xh = operand(part[0]), xm = operand(part[1]), xl = operand(part[2]);
             if constexpr (!STATE) {
-                if (!apart)
 #pragma unroll
-                    for (int ib = f / 2; ib < 2; ib++) {
-                        const int fr = ib ? 2 + f : f;
-                        const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][0][lane * 8]);
-                        const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][1][lane * 8]);
-                        Y[ib] = mma(gh, xh, Y[ib]);
-                        Y[ib] = mma(gl, xh, Y[ib]);
-                        Y[ib] = mma(gh, xm, Y[ib]);
-                    }
+                for (int ib = f / 2; ib < 2; ib++) {
+                    const int fr = ib ? 2 + f : f;
+                    const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][0][lane * 8]);
+                    const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][1][lane * 8]);
+                    Y[ib] = mma(gh, xh, Y[ib]);
+                    Y[ib] = mma(gl, xh, Y[ib]);
+                    Y[ib] = mma(gh, xm, Y[ib]);
+                }
             }
 #pragma unroll
             for (int nb = 0; nb < G::NBLK; nb++) {
@@ -503,33 +540,22 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                 S[nb] = mma(bt, xl, S[nb]);
             }
         }
-        if (mode == FAR) decay_state();
+        if (STATE && more) stage(buf ^ 1);
         if constexpr (!STATE) {
-            if (!apart) scale_rows();
-            // ---- y = Y + D x, through the wave's x tile: neighbouring lanes trade
-            // halves so that each writes two columns of a row, and rows leave in 16-byte pieces
-            const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
-            wave_lds_sync();
-#pragma unroll
-            for (int ib = 0; ib < 2; ib++)
-#pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    const uint32_t xr = __builtin_bit_cast(u32x4, xf[2 * ib + r / 8])[r % 8 / 2];
-                    const uint32_t u = pack2(fmaf(Dh, low_of(xr), Y[ib][r]), fmaf(Dh, high_of(xr), Y[ib][r + 1]));
-                    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
-                    const int i = 32 * ib + 8 * (r / 4) + r % 4 + 4 * hh + (lane & 1);
-                    *reinterpret_cast<uint32_t *>(&xt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
-                }
-            wave_lds_sync();
-            char *const py = reinterpret_cast<char *>(io.y) + row * io.ldy * 2;
-#pragma unroll
-            for (int n = 0; n < 4; n++) {
-                const int i = 16 * n + lane / 4;
-                if (i < nv)
-                    st_global8<WIDE>(py, ((uint32_t)i * (uint32_t)io.ldy + xcol) * 2u,
-                                     *reinterpret_cast<const u32x4 *>(&xt[(64 * n + lane) * 8]));
-            }
+            put_triangle(buf ^ 1, n0, tri);
+            for (int n = n0 + G::NW; n < 10; n += G::NW) put_triangle(buf ^ 1, n, triangle(buf ^ 1, n));
         }
+        if (mode == FAR) decay_state();
+        if constexpr (!STATE)
+            if (!apart) {
+                scale_rows();
+                output();
+            }
+    }
+    if constexpr (!STATE) {
+        wave_lds_sync();
+        load_y();
+        store_y((ntok - 1) % CH + 1);
     }
     if (STATE || last) {
         float *to = STATE ? seg : pool;

@@ -212,3 +212,34 @@ def test_bounds_that_break_the_rules_touch_nothing_outside():
         for i in range(2):
             if not 0 <= cu[i] < cu[i + 1] <= T:
                 assert np.array_equal(d["S"][i].cpu().numpy(), p["S"][i]), cu
+
+
+@pytest.mark.parametrize("resets", [False, True])
+def test_prompts_over_decays(resets):
+    """Heads whose chunks decay by 2^-0 to 2^-5000, on every side of the
+    kernel's two borders (2^-80 and 2^-160 over 64 tokens), evenly or by a few
+    tokens that forget nearly everything before them."""
+    torch = torch_cuda()
+    g = lib()
+    say("ssm decays", resets)
+    bits = np.array([0, 1e-3, 20, 70, 79, 81, 100, 140, 158, 162, 400, 5000], np.float64)
+    H, dk, dv, T = len(bits), 128, 64, 300
+    p = _problem(77, T, H, dk, dv, 1, "bf16", 1)
+    step = np.full((T, H), 0.25)
+    if resets:
+        step[:] = 1e-3
+        step[np.random.default_rng(3).integers(0, T, 14)] = 4.0
+    p["dt"] = torch.from_numpy(np.log(np.expm1(step)).astype(np.float32)).bfloat16()
+    p["dt_bias"] = np.zeros(H, np.float32)
+    per = 64 * 0.25 if not resets else 3 * 4.0
+    p["A"] = (-bits * np.log(2.0) / per).astype(np.float32)
+    d = _dev(p)
+    y = torch.full_like(d["x"], 7.0)
+    desc = g.SsmDesc(H=H, dk=dk, dv=dv, hk=1)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    nb = g.gdnq_ssm_workspace(desc, 1, T)
+    g.gdnq_ssm_prefill(desc, d["x"], d["B"], d["C"], d["dt"], d["A"], d["D"], d["dt_bias"], y, d["S"], 1, i32(0), i32(1),
+                       i32(0, T), 1, T, torch.empty(nb, dtype=torch.uint8, device="cuda") if nb else None)
+    torch.cuda.synchronize()
+    _check_prompts(p, y.double().cpu().numpy().reshape(T, H, dv), d["S"].double().cpu().numpy(), [0], [1], [0, T], 1, H,
+                   dk, dv, 1)
