@@ -22,8 +22,9 @@
 // Precision: the products run on the bf16 matrix instructions with fp32
 // sums.  B, C and x are bf16, so C B^T is exact up to the sum.  The fp32
 // operands of the outputs, tril(C B^T), S' and w X, are taken in two bf16
-// parts (off by 2^-18); the state's update takes w X in three (2^-26), so
-// that states stay as exact as fp32.
+// parts (off by at most 2^-16 of an operand); the state's update takes w X in
+// three (2^-24), so that states stay as exact as fp32 (with two they measured
+// 1.7e-6 off in norm, and the call took 0.86 of the time).
 //
 // A wave owns 32 value columns of one head for the whole segment: its state
 // (dk x 32) stays in accumulators, which feed C S directly as the B operand
@@ -118,7 +119,7 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
 __device__ __forceinline__ float low_of(uint32_t p) { return __uint_as_float(p << 16); }
 __device__ __forceinline__ float high_of(uint32_t p) { return __uint_as_float(p & 0xFFFF0000u); }
 
-// x[0..N) as the sum of P bf16 parts, off by 2^-(9 P) of x
+// x[0..N) as the sum of P bf16 parts, off by at most 2^-(8 P) of x
 template <int P, int N>
 __device__ __forceinline__ void split(float (&x)[N], uint32_t (&part)[P][N / 2])
 {

@@ -7,8 +7,9 @@ absolute values, ym and Sm) as the measure:
   |delta A| and a few ulps, B (delta x)^T carries e_d, the sum over dk rows
   dk u; states then round once, outputs once to their type.
   prompts: chunks of 64 tokens or fewer.  An operand in two bf16 parts is off
-  by 2^-18, in three by 2^-26; outputs have at most two such operands in a
-  product's path (2^-17), sums of at most dk and 64 terms, and a decay between
+  by at most 2^-16 of itself (2^-8 a part), in three by 2^-24.  An output
+  takes C B^T and w x in two parts each and leaves out the product of their
+  second parts: 3 2^-16.  Sums have at most dk and 64 terms, and a decay between
   two tokens of a chunk comes from a difference of running sums of at most K
   (the largest sum of |delta A| over 64 tokens), each off by at most 8 u K, so
   by a relative 16 u K; every chunk that a state passes through adds a
@@ -151,9 +152,9 @@ def _check_prompts(p, got, gS, slots, cont, cu, n_slots, H, dk, dv, hk):
         K = max((c[min(t + 64, m)] - c[t]).max() for t in range(m))
         e_d = L.delta_bound(v).max() * (1 + min(K, 64))
         tau = e_d + (dk + 2 * 64 + 16 * K + 16 * (m // 32 + 1)) * L.U
-        dS = np.abs(gS[slots[i]] - S) - Sm * (tau + 2.0 ** -25)
+        dS = np.abs(gS[slots[i]] - S) - Sm * (tau + 2.0 ** -24)
         assert not (dS > 2.0 ** -120).any(), (i, dS.max(), "state")
-        b = ym * (tau + 2.0 ** -17 + dk * L.U)
+        b = ym * (tau + 3 * 2.0 ** -16 + dk * L.U)
         dy = np.abs(got[lo:hi] - ref) - (b + (np.abs(ref) + b) * L.ROUND["bf16"])
         assert not (dy > 2.0 ** -120).any(), (i, dy.max(), np.argwhere(dy > 0)[:4].tolist())
         want[slots[i]] = gS[slots[i]]
