@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 
-from . import EINVAL, IO_BF16, GdnqError, _check, _stream, lib
+from . import EINVAL, IO_BF16, IO_F32, GdnqError, _check, _stream, lib
 
 CONV_SILU = 1
 SSM_SOFTPLUS = 1
@@ -113,30 +113,50 @@ def _bad(msg):
     raise GdnqError(EINVAL, msg)
 
 
-def _io_name(io):
-    return "torch.bfloat16" if io == IO_BF16 else "torch.float32"
+_torch = None
+_dtypes = {}
+_raw_stream = None
 
 
-def _device(t, name):
-    import torch
-    if t.device.type != "cuda":
+def _begin(stream):
+    """(current device, stream handle) of a call.  Loads torch on first use;
+    device -2 as long as no GPU is in use (no tensor is on it then)."""
+    global _torch, _raw_stream
+    if _torch is None:
+        import torch
+        _dtypes.update({IO_F32: torch.float32, IO_BF16: torch.bfloat16})
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _torch = torch
+    cuda = _torch.cuda
+    cur = cuda.current_device() if cuda.is_initialized() else -2
+    if stream is None:
+        return cur, (_raw_stream(cur) if _raw_stream and cur >= 0 else _stream(None))
+    return cur, _stream(stream)
+
+
+def _refuse(t, dtype, cur, name):
+    where = t.get_device()
+    if where < 0:
         _bad(f"{name} is on {t.device}, not on a GPU")
-    if t.device.index != torch.cuda.current_device():
-        _bad(f"{name} is on {t.device}, not on the current device {torch.cuda.current_device()}")
-
-
-def _rows(t, n, width, dtype, name):
-    """(pointer, row distance) of n rows of `width` values."""
-    if t is None or isinstance(t, int):
-        return t, 0
-    _device(t, name)
-    if str(t.dtype) != dtype:
+    if where != cur:
+        _bad(f"{name} is on {t.device}, not on the current device {cur}")
+    if dtype is not None and t.dtype is not dtype:
         _bad(f"{name} is {t.dtype}, not {dtype}")
+
+
+def _rows(t, n, width, dtype, cur, name):
+    """(pointer, row distance) of n rows of `width` values."""
+    if t is None or type(t) is int:
+        return t, 0
     shape, st = t.shape, t.stride()
-    if t.dim() == 3:
+    if len(shape) == 2 and shape[1] == width and shape[0] >= n and t.dtype is dtype and t.get_device() == cur \
+            and st[1] == 1 and st[0] >= width:
+        return t.data_ptr(), st[0]
+    _refuse(t, dtype, cur, name)
+    if len(shape) == 3:
         flat = shape[1] * shape[2] == width and st[2] == 1 and (st[1] == shape[2] or shape[1] == 1)
     else:
-        flat = t.dim() == 2 and shape[1] == width and (st[1] == 1 or width == 1)
+        flat = len(shape) == 2 and shape[1] == width and (st[1] == 1 or width == 1)
     if not flat:
         _bad(f"{name} must have rows of {width} consecutive values (got shape {tuple(shape)}, strides {st})")
     if shape[0] < n:
@@ -147,44 +167,52 @@ def _rows(t, n, width, dtype, name):
     return t.data_ptr(), (st[0] if shape[0] > 1 else width)
 
 
-def _flat(t, n, dtype, name):
+def _flat(t, n, dtype, cur, name):
     """Pointer of at least n contiguous values."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
-    _device(t, name)
-    if str(t.dtype) != dtype:
-        _bad(f"{name} is {t.dtype}, not {dtype}")
+    if t.dtype is dtype and t.get_device() == cur and t.is_contiguous() and t.numel() >= n:
+        return t.data_ptr()
+    _refuse(t, dtype, cur, name)
     if not t.is_contiguous():
         _bad(f"{name} must be contiguous")
-    if t.numel() < n:
-        _bad(f"{name} has {t.numel()} values, {n} are needed")
-    return t.data_ptr()
+    _bad(f"{name} has {t.numel()} values, {n} are needed")
 
 
-_F, _I = "torch.float32", "torch.int32"
+def _types(d):
+    """The io, fp32 and int32 types of a call (an unknown io_dtype is the library's to refuse)."""
+    return _dtypes.get(d.io_dtype, _torch.float32), _torch.float32, _torch.int32
 
 
 def gdnq_conv_prefill(desc, x, w, bias, state, n_slots, slots, cont, cu_seqlens, n_seqs, T, y, stream=None):
     d = _desc(desc)
-    io = _io_name(d.io_dtype)
-    xp, ldx = _rows(x, T, d.C, io, "x")
-    yp, ldy = _rows(y, T, d.C, io, "y")
-    _check(lib.gdnq_conv_prefill(
-        d, xp, ldx, _flat(w, d.width * d.C, _F, "w"), _flat(bias, d.C, _F, "bias"),
-        _flat(state, n_slots * (d.width - 1) * d.C, io, "state"), n_slots, _flat(slots, n_seqs, _I, "slots"),
-        _flat(cont, n_seqs, _I, "cont"), _flat(cu_seqlens, n_seqs + 1, _I, "cu_seqlens"), n_seqs, T, yp, ldy,
-        _stream(stream)))
+    cur, st = _begin(stream)
+    io, f32, i32 = _types(d)
+    C, width = d.C, d.width
+    xp, ldx = _rows(x, T, C, io, cur, "x")
+    yp, ldy = _rows(y, T, C, io, cur, "y")
+    rc = lib.gdnq_conv_prefill(
+        d, xp, ldx, _flat(w, width * C, f32, cur, "w"), _flat(bias, C, f32, cur, "bias"),
+        _flat(state, n_slots * (width - 1) * C, io, cur, "state"), n_slots, _flat(slots, n_seqs, i32, cur, "slots"),
+        _flat(cont, n_seqs, i32, cur, "cont"), _flat(cu_seqlens, n_seqs + 1, i32, cur, "cu_seqlens"), n_seqs, T, yp,
+        ldy, st)
+    if rc:
+        _check(rc)
 
 
 def gdnq_conv_step(desc, x, w, bias, state, n_slots, slots, n, y, stream=None):
     d = _desc(desc)
-    io = _io_name(d.io_dtype)
-    xp, ldx = _rows(x, n, d.C, io, "x")
-    yp, ldy = _rows(y, n, d.C, io, "y")
-    _check(lib.gdnq_conv_step(
-        d, xp, ldx, _flat(w, d.width * d.C, _F, "w"), _flat(bias, d.C, _F, "bias"),
-        _flat(state, n_slots * (d.width - 1) * d.C, io, "state"), n_slots, _flat(slots, n, _I, "slots"), n, yp, ldy,
-        _stream(stream)))
+    cur, st = _begin(stream)
+    io, f32, i32 = _types(d)
+    C, width = d.C, d.width
+    xp, ldx = _rows(x, n, C, io, cur, "x")
+    yp, ldy = _rows(y, n, C, io, cur, "y")
+    rc = lib.gdnq_conv_step(
+        d, xp, ldx, _flat(w, width * C, f32, cur, "w"), _flat(bias, C, f32, cur, "bias"),
+        _flat(state, n_slots * (width - 1) * C, io, cur, "state"), n_slots, _flat(slots, n, i32, cur, "slots"), n, yp,
+        ldy, st)
+    if rc:
+        _check(rc)
 
 
 def gdnq_ssm_workspace(desc, n_seqs, T) -> int:
@@ -194,60 +222,77 @@ def gdnq_ssm_workspace(desc, n_seqs, T) -> int:
     return out.value
 
 
-def _ssm_io(d, n, x, B, C, dt, A, D, dt_bias, y):
-    io = _io_name(d.io_dtype)
-    nb = (d.hk or d.H) * d.dk
-    xp, ldx = _rows(x, n, d.H * d.dv, io, "x")
-    bp, ldb = _rows(B, n, nb, io, "B")
-    cp, ldc = _rows(C, n, nb, io, "C")
-    tp, lddt = _rows(dt, n, d.H, io, "dt")
-    yp, ldy = _rows(y, n, d.H * d.dv, io, "y")
-    return _SsmIo(xp, bp, cp, tp, yp, _flat(A, d.H, _F, "A"), _flat(D, d.H, _F, "D"),
-                  _flat(dt_bias, d.H, _F, "dt_bias"), ldx, ldb, ldc, lddt, ldy)
+def _ssm_io(d, cur, n, x, B, C, dt, A, D, dt_bias, y):
+    io, f32, _ = _types(d)
+    H = d.H
+    nb, nx = (d.hk or H) * d.dk, H * d.dv
+    xp, ldx = _rows(x, n, nx, io, cur, "x")
+    bp, ldb = _rows(B, n, nb, io, cur, "B")
+    cp, ldc = _rows(C, n, nb, io, cur, "C")
+    tp, lddt = _rows(dt, n, H, io, cur, "dt")
+    yp, ldy = _rows(y, n, nx, io, cur, "y")
+    return _SsmIo(xp, bp, cp, tp, yp, _flat(A, H, f32, cur, "A"), _flat(D, H, f32, cur, "D"),
+                  _flat(dt_bias, H, f32, cur, "dt_bias"), ldx, ldb, ldc, lddt, ldy)
 
 
 def gdnq_ssm_prefill(desc, x, B, C, dt, A, D, dt_bias, y, S, n_slots, slots, cont, cu_seqlens, n_seqs, T,
                      workspace=None, stream=None):
     d = _desc(desc)
+    cur, st = _begin(stream)
+    _, f32, i32 = _types(d)
     nb = 0
-    if workspace is not None and not isinstance(workspace, int):
-        _device(workspace, "workspace")
+    if type(workspace) is int:
+        nb = gdnq_ssm_workspace(d, n_seqs, T)
+    elif workspace is not None:
+        _refuse(workspace, None, cur, "workspace")
         if not workspace.is_contiguous():
             _bad("workspace must be contiguous")
         nb = workspace.numel() * workspace.element_size()
         workspace = workspace.data_ptr()
-    elif workspace is not None:
-        nb = gdnq_ssm_workspace(d, n_seqs, T)
-    _check(lib.gdnq_ssm_prefill(
-        d, _ssm_io(d, T, x, B, C, dt, A, D, dt_bias, y), _flat(S, n_slots * d.H * d.dk * d.dv, _F, "S"), n_slots,
-        _flat(slots, n_seqs, _I, "slots"), _flat(cont, n_seqs, _I, "cont"),
-        _flat(cu_seqlens, n_seqs + 1, _I, "cu_seqlens"), n_seqs, T, workspace, nb, _stream(stream)))
+    rc = lib.gdnq_ssm_prefill(
+        d, _ssm_io(d, cur, T, x, B, C, dt, A, D, dt_bias, y), _flat(S, n_slots * d.H * d.dk * d.dv, f32, cur, "S"),
+        n_slots, _flat(slots, n_seqs, i32, cur, "slots"), _flat(cont, n_seqs, i32, cur, "cont"),
+        _flat(cu_seqlens, n_seqs + 1, i32, cur, "cu_seqlens"), n_seqs, T, workspace, nb, st)
+    if rc:
+        _check(rc)
 
 
 def gdnq_ssm_step(desc, x, B, C, dt, A, D, dt_bias, y, S, n_slots, slots, n, stream=None):
     d = _desc(desc)
-    _check(lib.gdnq_ssm_step(
-        d, _ssm_io(d, n, x, B, C, dt, A, D, dt_bias, y), _flat(S, n_slots * d.H * d.dk * d.dv, _F, "S"), n_slots,
-        _flat(slots, n, _I, "slots"), n, _stream(stream)))
+    cur, st = _begin(stream)
+    _, f32, i32 = _types(d)
+    rc = lib.gdnq_ssm_step(
+        d, _ssm_io(d, cur, n, x, B, C, dt, A, D, dt_bias, y), _flat(S, n_slots * d.H * d.dk * d.dv, f32, cur, "S"),
+        n_slots, _flat(slots, n, i32, cur, "slots"), n, st)
+    if rc:
+        _check(rc)
 
 
 def gdnq_norm_gated(desc, x, z, w, y, rows, stream=None):
     d = _desc(desc)
-    io = _io_name(d.io_dtype)
-    xp, ldx = _rows(x, rows, d.D, io, "x")
-    zp, ldz = _rows(z, rows, d.D, io, "z")
-    yp, ldy = _rows(y, rows, d.D, io, "y")
-    nw = (d.group or d.D) if d.flags & NORM_GROUP_WEIGHT else d.D
-    _check(lib.gdnq_norm_gated(d, xp, ldx, zp, ldz, _flat(w, nw, _F, "w"), yp, ldy, rows, _stream(stream)))
+    cur, st = _begin(stream)
+    io, f32, _ = _types(d)
+    D = d.D
+    xp, ldx = _rows(x, rows, D, io, cur, "x")
+    zp, ldz = _rows(z, rows, D, io, cur, "z")
+    yp, ldy = _rows(y, rows, D, io, cur, "y")
+    nw = (d.group or D) if d.flags & NORM_GROUP_WEIGHT else D
+    rc = lib.gdnq_norm_gated(d, xp, ldx, zp, ldz, _flat(w, nw, f32, cur, "w"), yp, ldy, rows, st)
+    if rc:
+        _check(rc)
 
 
 def gdnq_norm_residual(desc, x, post_w, scale, res, res_out, w, y, rows, stream=None):
     d = _desc(desc)
-    io = _io_name(d.io_dtype)
-    rio = _F if d.flags & NORM_RES_F32 else io
-    xp, ldx = _rows(x, rows, d.D, io, "x")
-    rp, ldr = _rows(res, rows, d.D, rio, "res")
-    op, ldro = _rows(res_out, rows, d.D, rio, "res_out")
-    yp, ldy = _rows(y, rows, d.D, io, "y")
-    _check(lib.gdnq_norm_residual(d, xp, ldx, _flat(post_w, d.D, _F, "post_w"), scale, rp, ldr, op, ldro,
-                                  _flat(w, d.D, _F, "w"), yp, ldy, rows, _stream(stream)))
+    cur, st = _begin(stream)
+    io, f32, _ = _types(d)
+    rio = f32 if d.flags & NORM_RES_F32 else io
+    D = d.D
+    xp, ldx = _rows(x, rows, D, io, cur, "x")
+    rp, ldr = _rows(res, rows, D, rio, cur, "res")
+    op, ldro = (rp, ldr) if res_out is res else _rows(res_out, rows, D, rio, cur, "res_out")
+    yp, ldy = _rows(y, rows, D, io, cur, "y")
+    rc = lib.gdnq_norm_residual(d, xp, ldx, _flat(post_w, D, f32, cur, "post_w"), scale, rp, ldr, op, ldro,
+                                _flat(w, D, f32, cur, "w"), yp, ldy, rows, st)
+    if rc:
+        _check(rc)

@@ -257,32 +257,29 @@ def test_binding_refuses_host_tensors_and_other_types(g):
         g.gdnq_conv_step(g.ConvDesc(C=64), x, BASE, None, BASE, 4, None, 4, BASE, stream=0)
     from recurrent_state_quantization_amd import layer
 
-    class OnGpu:   # a tensor's face, as the binding sees one on the current device
-        def __init__(self, t):
-            self.t, self.device = t, type("D", (), {"type": "cuda", "index": 0})()
+    class OnGpu:   # a tensor's face, as the binding sees one on device `index`
+        def __init__(self, t, index=0):
+            self.t, self.index = t, index
+
+        def get_device(self):
+            return self.index
 
         def __getattr__(self, k):
             return getattr(self.t, k)
 
-    cur = torch.cuda.current_device
-    torch.cuda.current_device = lambda: 0
-    try:
-        ok = layer._rows(OnGpu(x), 4, 64, "torch.bfloat16", "x")
-        assert ok == (x.data_ptr(), 64)
-        assert layer._rows(OnGpu(x[:, 8:40]), 4, 32, "torch.bfloat16", "x")[1] == 64
-        assert layer._rows(OnGpu(x.view(4, 2, 32)), 4, 64, "torch.bfloat16", "x")[1] == 64
-        for t, n, w, msg in ((x, 5, 64, "4 rows"), (x, 4, 32, "rows of 32"), (x.float(), 4, 64, "float32"),
-                             (x.t(), 4, 4, "consecutive"), (x[:1].expand(4, 64), 4, 64, "overlap"),
-                             (x.view(4, 2, 32).transpose(0, 1), 2, 128, "consecutive")):
-            with pytest.raises(g.GdnqError, match=msg):
-                layer._rows(OnGpu(t), n, w, "torch.bfloat16", "x")
-        with pytest.raises(g.GdnqError, match="contiguous"):
-            layer._flat(OnGpu(x[:, ::2]), 4, "torch.bfloat16", "w")
-        with pytest.raises(g.GdnqError, match="values"):
-            layer._flat(OnGpu(x), 257, "torch.bfloat16", "w")
-        other = OnGpu(x)
-        other.device.index = 1
+    bf = torch.bfloat16
+    assert layer._rows(OnGpu(x), 4, 64, bf, 0, "x") == (x.data_ptr(), 64)
+    assert layer._rows(OnGpu(x[:, 8:40]), 4, 32, bf, 0, "x")[1] == 64
+    assert layer._rows(OnGpu(x.view(4, 2, 32)), 4, 64, bf, 0, "x")[1] == 64
+    assert layer._rows(OnGpu(x[:1, :8]), 1, 8, bf, 0, "x")[1] >= 8
+    for t, n, w, msg in ((x, 5, 64, "4 rows"), (x, 4, 32, "rows of 32"), (x.float(), 4, 64, "float32"),
+                         (x.t(), 4, 4, "consecutive"), (x[:1].expand(4, 64), 4, 64, "overlap"),
+                         (x.view(4, 2, 32).transpose(0, 1), 2, 128, "consecutive")):
+        with pytest.raises(g.GdnqError, match=msg):
+            layer._rows(OnGpu(t), n, w, bf, 0, "x")
+    for t, n, msg in ((x[:, ::2], 4, "contiguous"), (x, 257, "values"), (x.float(), 4, "float32")):
+        with pytest.raises(g.GdnqError, match=msg):
+            layer._flat(OnGpu(t), n, bf, 0, "w")
+    for f in (lambda t: layer._flat(t, 4, bf, 0, "w"), lambda t: layer._rows(t, 4, 64, bf, 0, "w")):
         with pytest.raises(g.GdnqError, match="current device"):
-            layer._flat(other, 4, "torch.bfloat16", "w")
-    finally:
-        torch.cuda.current_device = cur
+            f(OnGpu(x, 1))
