@@ -199,9 +199,9 @@ struct SsmGeom {
     static constexpr int NBLK = DK / 32;
 };
 
-// Per-token vectors of a head in LDS: the outputs' row factor, w, and for the
+// Per-token vectors of a head in LDS: w, the outputs' row factor, and for the
 // other form cs and delta.
-enum { V_F, V_W, V_CS, V_D, V_N };
+enum { V_W, V_F, V_CS, V_D, V_N };
 
 // 2^RANGE and 2^-RANGE times any usual value, and its second bf16 part, are
 // normal numbers.
@@ -217,7 +217,8 @@ struct SsmLds {
     // tril(C B^T) as operands: rows 0..31 by tokens 0..15, 16..31, rows 32..63
     // by tokens 0..15, .., 48..63; each in two parts of 8 values per lane
     alignas(16) __bf16 g[STATE ? 1 : 2][STATE ? 1 : 6][2][STATE ? 8 : 64 * 8];
-    alignas(16) float v[2][HEADS][V_N][CH];
+    static constexpr int VN = STATE ? 1 : V_N;
+    alignas(16) float v[2][HEADS][VN][CH];
     float tot[2][HEADS];   // the decay of S before the chunk's products (of FAR: also behind them)
     int mode[2][HEADS];
 };
@@ -228,6 +229,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
 {
     using G = SsmGeom<DK, DV, HPW>;
     __shared__ SsmLds<G, STATE> L;
+    using Vectors = float[SsmLds<G, STATE>::VN][CH];
     const int t = (int)__builtin_amdgcn_workitem_id_x(), lane = t & 63;
     const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
     const int hw = wv % HPW, slice = wv / HPW;   // a head's first wave on each SIMD
@@ -325,7 +327,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         const float suf = suffix64(la, lane, tot);   // cs_63 - cs
         const int mode = STATE || tot > -RANGE ? NEAR : tot > -2.0f * RANGE ? FAR : APART;
         const float half = 0.5f * tot;
-        float(&v)[V_N][CH] = L.v[buf][hw];
+        Vectors &v = L.v[buf][hw];
         v[V_W][lane] = __builtin_amdgcn_exp2f(mode == FAR ? suf - half : suf) * d;
         if constexpr (!STATE) {
             v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : (mode == FAR ? half : tot) - suf);
@@ -413,7 +415,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         wave_lds_sync();
 
         const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
-        const float(&vec)[V_N][CH] = L.v[buf][hw];
+        const Vectors &vec = L.v[buf][hw];
         const float tot = uniform(L.tot[buf][hw]);
         const int mode = STATE ? NEAR : __builtin_amdgcn_readfirstlane(L.mode[buf][hw]);
         const bool apart = mode == APART;
@@ -612,13 +614,20 @@ int heads_per_group(const gdnq_ssm_desc &d, bool wide)
     return 1;
 }
 
-// log2 of a segment's tokens: the longest that still gives the chip 2048
-// waves of 32 columns each, if the T tokens were one sequence; from 256 tokens.
-int segment_shift(const gdnq_ssm_desc &d, int T)
+// log2 of a segment's tokens.  Up to 384 tokens take one segment: the two
+// other kernels cost more than they save (300 tokens of 64 heads of 128 x 64:
+// 36 us, 39 in segments of 128; 512 tokens: 56, 47).  Above, from 128 tokens on
+// the longest that still gives the chip 2048 waves of 32 columns (8 per
+// compute unit) and is no longer than the average sequence: 2048 tokens, 64
+// heads: 53, 60, 89 us in segments of 128, 256, 512; 6000 tokens in 20
+// sequences of 24 heads: 76, 64, 83; 16384 tokens, 64 heads: 280, 223, 195,
+// 293 in segments of 256 to 2048.
+int segment_shift(const gdnq_ssm_desc &d, int n, int T)
 {
+    if (T <= 384) return 9;
     const long long per = (long long)d.H * (d.dv / 32);
-    int sh = 8;
-    while (sh < 30 && ((long long)T >> (sh + 1)) * per >= 2048) sh++;
+    int sh = 7;
+    while (((T >> (sh + 1)) + (long long)n) * per >= 2048 && ((long long)n << (sh + 1)) <= T) sh++;
     return sh;
 }
 
@@ -628,7 +637,7 @@ unsigned segment_ids(int n, int T, int sh) { return (unsigned)(T >> sh) + (unsig
 
 size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T)
 {
-    const int sh = segment_shift(d, T);
+    const int sh = segment_shift(d, n, T);
     if (T <= 1 << sh) return 0;
     return (size_t)segment_ids(n, T, sh) * (size_t)d.H * ((size_t)d.dk * d.dv + 1) * 4;
 }
@@ -638,7 +647,7 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
     const gdnq_ssm_io &io = c.io;
     const bool wide = wide_rows(io.x, io.ldx, 2) && wide_rows(io.B, io.ldb, 2) && wide_rows(io.C, io.ldc, 2) &&
                       wide_rows(io.y, io.ldy, 2);
-    const int hk = d.hk ? d.hk : d.H, hpw = heads_per_group(d, wide), sh = segment_shift(d, c.T);
+    const int hk = d.hk ? d.hk : d.H, hpw = heads_per_group(d, wide), sh = segment_shift(d, c.n, c.T);
     const unsigned ids = segment_ids(c.n, c.T, sh), blocks = (unsigned)(d.H / hpw);
     const SsmArgs A{c, d.H, hk, sh, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
                     make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
