@@ -211,7 +211,7 @@ int gdnq_conv_prefill(const gdnq_conv_desc *desc, const void *x, int64_t ldx, co
     Spans sp;
     TRY(check_packed(cont, cu_seqlens, n_seqs, sp));
     TRY(check_conv_call(*desc, c, T, sp));
-    TRY(check_grid(((unsigned long long)T / 8 + n_seqs) * (((unsigned long long)desc->C + 63) / 64), "T*C"));
+    TRY(check_grid(((unsigned long long)T / 16 + n_seqs) * (((unsigned long long)desc->C + 63) / 64), "T*C"));
     return launched(gdnq::launch_conv_prefill(*desc, c, stream_of(stream)));
 }
 
@@ -257,7 +257,7 @@ int gdnq_ssm_prefill(const gdnq_ssm_desc *desc, const gdnq_ssm_io *io, float *S,
     if (workspace_bytes < need)
         return fail(GDNQ_EINVAL, "workspace of %zu bytes is too small (%zu are needed)", workspace_bytes, need);
     if (need) TRY(flat(sp, workspace, need, "workspace", WRITE));
-    TRY(check_grid(((unsigned long long)T / 64 + n_seqs) * desc->H * 4, "T*H"));
+    TRY(check_grid(((unsigned long long)T / 128 + n_seqs + 8) * desc->H * 16, "T*H"));
     return launched(gdnq::launch_ssm_prefill(*desc, c, stream_of(stream)));
 }
 

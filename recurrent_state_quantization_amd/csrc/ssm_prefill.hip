@@ -322,7 +322,9 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         float d = low_of(dt) + bias;
         if (A.sp) d = softplus(d);
         d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
-        const float la = d * Ah;
+        // 2^-256 is zero in fp32; the bound keeps the sums behind a token that
+        // forgets everything from losing the digits of its neighbours' decays
+        const float la = fmaxf(d * Ah, -256.0f);
         float tot;
         const float suf = suffix64(la, lane, tot);   // cs_63 - cs
         const int mode = STATE || tot > -RANGE ? NEAR : tot > -2.0f * RANGE ? FAR : APART;
