@@ -43,6 +43,8 @@
 // says when): a first kernel forms each segment's own state and decay from
 // zero, a second runs along the segments of each sequence and leaves the
 // state at every segment's start, and the main kernel starts from those.
+#include <cmath>
+
 #include "layer_launchers.hpp"
 #include "rows.hpp"
 
@@ -233,12 +235,12 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
     const int t = (int)__builtin_amdgcn_workitem_id_x(), lane = t & 63;
     const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
     const int hw = wv % HPW, slice = wv / HPW;   // a head's first wave on each SIMD
-    // workgroups go to the 8 XCDs by turns: all head blocks of a segment are
-    // given numbers of one XCD, so that they read B and C from one L2
+    // head blocks of a segment are neighbours (and so on all XCDs: giving them
+    // one XCD's numbers spread the segments unevenly and was no faster)
     const unsigned g = __builtin_amdgcn_workgroup_id_x();
-    const unsigned round = __builtin_amdgcn_readfirstlane(div_by(g >> 3, A.byHB)), id = round * 8u + (g & 7u);
+    const unsigned id = __builtin_amdgcn_readfirstlane(div_by(g, A.byHB));
     if (id >= A.ids) return;
-    const int h0 = (int)((g >> 3) - round * A.byHB.d) * HPW, head = h0 + hw;
+    const int h0 = (int)(g - id * A.byHB.d) * HPW, head = h0 + hw;
     const int hb = h0 / (A.H / A.hk);
     const gdnq_ssm_io &io = A.c.io;
     SeqTile q;
@@ -607,30 +609,44 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart
 
 // Heads per workgroup: as many as share B and C and fit its 8 waves, a power
 // of two; rows that need narrow accesses take one.
-int heads_per_group(const gdnq_ssm_desc &d, bool wide)
+int heads_per_group(const gdnq_ssm_desc &d)
 {
     const int per = d.hk ? d.H / d.hk : 1;
-    if (wide)
-        for (int n = d.dv == 64 ? 4 : 2; n > 1; n /= 2)
-            if (per % n == 0) return n;
+    for (int n = d.dv == 64 ? 4 : 2; n > 1; n /= 2)
+        if (per % n == 0) return n;
     return 1;
 }
 
 // log2 of a segment's tokens.  Up to 384 tokens take one segment: the two
 // other kernels cost more than they save (300 tokens of 64 heads of 128 x 64:
-// 36 us, 39 in segments of 128; 512 tokens: 56, 47).  Above, from 128 tokens on
-// the longest that still gives the chip 2048 waves of 32 columns (8 per
-// compute unit) and is no longer than the average sequence: 2048 tokens, 64
-// heads: 53, 60, 89 us in segments of 128, 256, 512; 6000 tokens in 20
-// sequences of 24 heads: 76, 64, 83; 16384 tokens, 64 heads: 280, 223, 195,
-// 293 in segments of 256 to 2048.
-int segment_shift(const gdnq_ssm_desc &d, int n, int T)
+// 36 us, 39 in segments of 128; 512 tokens: 56, 47).  Above, the length from
+// 128 on with the least estimated time: a workgroup per compute unit and round,
+// 6.0 us a chunk and half as much again per segment in the main kernel, 3.4 us
+// a chunk and one more per segment in the states' kernel, and the joined states
+// at 5 TB/s (dk = 128; with dk = 64 all three are about half).  Measured in us
+// for segments of 256, 512, 1024, 2048: 16384 tokens of 64 heads of 128 x 64
+// 275, 218, 193, 293; 32731 tokens in 9 sequences of 32 heads of 128 x 128 -,
+// 465, 454, 505; 32768 tokens in 4 sequences of 80 heads of 128 x 64 -, 588,
+// 530, 610; 6000 tokens in 20 sequences of 24 heads 57, 83 (128: 72).
+int segment_shift(const gdnq_ssm_desc &d, int hpw, int n, int T)
 {
     if (T <= 384) return 9;
-    const long long per = (long long)d.H * (d.dv / 32);
-    int sh = 7;
-    while (((T >> (sh + 1)) + (long long)n) * per >= 2048 && ((long long)n << (sh + 1)) <= T) sh++;
-    return sh;
+    const double blocks = d.H / hpw, join = (double)d.H * 128 * d.dv * 8 / 5e6;
+    const auto rounds = [&](double segs) { return std::ceil(segs * blocks / 256.0); };
+    int best = 7;
+    double least = 0.0;
+    for (int sh = 7; sh <= 20; sh++) {
+        const double len = (double)(1 << sh), chunks = len / CH;
+        // segments of sequences that are long against them, half of one lost to each one's end
+        const double all = n == 1 ? std::ceil(T / len) : std::fmax((double)n, T / len + 0.5 * n);
+        const double us = rounds(all) * (chunks + 1.5) * 6.0 + rounds(all - n) * (chunks + 1.0) * 3.4 + all * join;
+        if (sh == 7 || us < least) {
+            best = sh;
+            least = us;
+        }
+        if (len >= T) break;
+    }
+    return best;
 }
 
 unsigned segment_ids(int n, int T, int sh) { return (unsigned)(T >> sh) + (unsigned)n; }
@@ -639,7 +655,7 @@ unsigned segment_ids(int n, int T, int sh) { return (unsigned)(T >> sh) + (unsig
 
 size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T)
 {
-    const int sh = segment_shift(d, n, T);
+    const int sh = segment_shift(d, heads_per_group(d), n, T);
     if (T <= 1 << sh) return 0;
     return (size_t)segment_ids(n, T, sh) * (size_t)d.H * ((size_t)d.dk * d.dv + 1) * 4;
 }
@@ -649,7 +665,7 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
     const gdnq_ssm_io &io = c.io;
     const bool wide = wide_rows(io.x, io.ldx, 2) && wide_rows(io.B, io.ldb, 2) && wide_rows(io.C, io.ldc, 2) &&
                       wide_rows(io.y, io.ldy, 2);
-    const int hk = d.hk ? d.hk : d.H, hpw = heads_per_group(d, wide), sh = segment_shift(d, c.n, c.T);
+    const int hk = d.hk ? d.hk : d.H, hpw = wide ? heads_per_group(d) : 1, sh = segment_shift(d, heads_per_group(d), c.n, c.T);
     const unsigned ids = segment_ids(c.n, c.T, sh), blocks = (unsigned)(d.H / hpw);
     const SsmArgs A{c, d.H, hk, sh, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
                     make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
@@ -658,13 +674,13 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
             using G = SsmGeom<DK.value, DV.value, HPW.value>;
             constexpr bool W = decltype(WIDE)::value;
             if (c.T > 1 << sh) {
-                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, W>), dim3((ids + 7) / 8 * 8 * blocks),
+                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, W>), dim3(ids * blocks),
                                    dim3(G::NT), 0, st, A);
                 constexpr unsigned parts = DK.value * DV.value / 1024;
                 hipLaunchKernelGGL((ssm_join_kernel<DK.value * DV.value>), dim3((unsigned)c.n * d.H * parts), dim3(256),
                                    0, st, A, make_divisor(parts), make_divisor((unsigned)d.H));
             }
-            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, W>), dim3((ids + 7) / 8 * 8 * blocks),
+            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, W>), dim3(ids * blocks),
                                dim3(G::NT), 0, st, A);
             return hipGetLastError();
         };
