@@ -23,8 +23,8 @@
  *    call reads its columns straight out of a projection's wider output.
  *    These pointers need their element's alignment only; rows whose pointers
  *    and distances are all multiples of 16 bytes take wide loads.
- *    Weights, states, slots and workspaces are contiguous and 16-byte
- *    aligned.
+ *    Weights, states, per-entry arrays (slots, cont, cu_seqlens) and
+ *    workspaces are contiguous and 16-byte aligned.
  *  - Outputs and states must not overlap any input (the address range from
  *    the first to the last row counts) or each other.
  *  - Packed sequences: T token rows hold n_seqs sequences, sequence i in rows
@@ -126,10 +126,10 @@ int gdnq_ssm_workspace(const gdnq_ssm_desc *desc, int32_t n_seqs, int32_t T, siz
 /*
  * Packed prompts.  S: device fp32 [n_slots,H,dk,dv], the pool of states (the
  * layout of gdnq.h's fp32 states); each sequence's slot is replaced by its
- * state after the last token.  io_dtype must be GDNQ_IO_BF16
- * and rows at most 2^22 elements apart (GDNQ_EUNSUPPORTED otherwise).  Runs
- * chunk by chunk on the matrix cores,
- * fp32 operands split into bf16 parts (two for outputs, three for states).
+ * state after the last token.  io_dtype must be GDNQ_IO_BF16 and rows at most
+ * 2^22 elements apart (GDNQ_EUNSUPPORTED otherwise).  Runs chunk by chunk on
+ * the matrix cores, fp32 operands split into bf16 parts (two for outputs, three
+ * for states).
  * workspace: device, 16-byte aligned, at least gdnq_ssm_workspace bytes
  * (NULL where that is 0), free for other use once the call has run; calls
  * that may run at the same time need one each.

@@ -372,7 +372,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         for (int p = 0; p < 2; p++)
             *reinterpret_cast<uint2 *>(&L.g[buf][f][p][at]) = make_uint2(part[p][0], part[p][1]);
     };
-    const int n0 = G::NW - 1 - wv;   // the wave's first block; the others follow NW apart
+    const int n0 = wv;   // the wave's first block; the others follow NW apart
 
     if constexpr (!STATE) {   // the blocks above the diagonal stay zero
         for (int i = t; i < 2 * 6 * 2 * 64; i += G::NT)
@@ -436,13 +436,16 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         };
         floatx16 Y[2];
         const auto scale_rows = [&] {   // Y rows by V_F
+            float4 e[8];
 #pragma unroll
-            for (int ib = 0; ib < 2; ib++)
+            for (int k = 0; k < 8; k++) e[k] = *reinterpret_cast<const float4 *>(&vec[V_F][8 * k + 4 * hh]);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float4 e = *reinterpret_cast<const float4 *>(&vec[V_F][32 * ib + 8 * k + 4 * hh]);
-                    Y[ib][4 * k] *= e.x, Y[ib][4 * k + 1] *= e.y, Y[ib][4 * k + 2] *= e.z, Y[ib][4 * k + 3] *= e.w;
-                }
+            for (int k = 0; k < 8; k++) {
+                floatx16 &y = Y[k / 4];
+                const int r = 4 * (k % 4);
+                y[r] *= e[k].x, y[r + 1] *= e[k].y, y[r + 2] *= e[k].z, y[r + 3] *= e[k].w;
+            }
         };
         const auto output = [&] {
             // y = Y + D x to the wave's x tile; neighbouring lanes trade halves so
