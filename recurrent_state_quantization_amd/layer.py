@@ -115,22 +115,25 @@ def _bad(msg):
 
 _torch = None
 _dtypes = {}
-_raw_stream = None
+_device = _raw_stream = None   # torch's own queries, without their Python wrappers where it has them
 
 
 def _begin(stream):
     """(current device, stream handle) of a call.  Loads torch on first use;
     device -2 as long as no GPU is in use (no tensor is on it then)."""
-    global _torch, _raw_stream
-    if _torch is None:
-        import torch
-        _dtypes.update({IO_F32: torch.float32, IO_BF16: torch.bfloat16})
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _torch = torch
-    cuda = _torch.cuda
-    cur = cuda.current_device() if cuda.is_initialized() else -2
+    global _torch, _device, _raw_stream
+    if _device is None:
+        if _torch is None:
+            import torch
+            _dtypes.update({IO_F32: torch.float32, IO_BF16: torch.bfloat16})
+            _torch = torch
+        if not _torch.cuda.is_initialized():
+            return -2, _stream(stream)
+        _raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+        _device = getattr(_torch._C, "_cuda_getDevice", _torch.cuda.current_device)
+    cur = _device()
     if stream is None:
-        return cur, (_raw_stream(cur) if _raw_stream and cur >= 0 else _stream(None))
+        return cur, (_raw_stream(cur) if _raw_stream else _stream(None))
     return cur, _stream(stream)
 
 
