@@ -26,8 +26,8 @@
 // three (2^-24), so that states stay as exact as fp32 (with two they measured
 // 1.7e-6 off in norm, and the call took 0.86 of the time).
 //
-// A wave owns 32 value columns of one head for the whole segment: its state
-// (dk x 32) stays in accumulators, which feed C S directly as the B operand
+// A wave owns 32 value columns of one head for a whole piece of a sequence: its
+// state (dk x 32) stays in accumulators, which feed C S directly as the B operand
 // when the contraction index is taken in the accumulators' row order (slots
 // 0..3 of lane half h are rows 16t + 4h .. + 3, slots 4..7 rows 16t + 8 + 4h
 // .. + 3).  x and B are read by columns with the transposing LDS read.  A
@@ -39,10 +39,13 @@
 // waves form its tril(C B^T) and load its x; the heads' first waves form its
 // decays.  x and y pass through LDS within each wave.
 //
-// Long sequences are cut into segments of 2^SH tokens (launch_ssm_prefill
-// says when): a first kernel forms each segment's own state and decay from
-// zero, a second runs along the segments of each sequence and leaves the
-// state at every segment's start, and the main kernel starts from those.
+// The packed tokens are dealt out in equal shares over the compute units
+// (shares() says how many), wherever that cuts a sequence: a first kernel forms
+// the state and decay of each share's last piece, if its sequence goes on in
+// the next, from the sequence's own start or from zero, a second runs along
+// the shares of each sequence and leaves the state at every later one's start,
+// and the main kernel starts from those.
+#include <algorithm>
 #include <cmath>
 
 #include "layer_launchers.hpp"
@@ -60,15 +63,25 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int CH = 64;   // tokens per chunk
 
+// Places of the packed axis that is dealt out in shares: sequence b holds its
+// tokens' places from cu[b] + PAD b on and PAD more, the price of beginning a
+// sequence (a chunk and a half, and half a chunk at its end) and of many in
+// one share. 9 sequences, 32731 tokens of 32 heads of 128 x 128: 372 us with
+// 96, 367 with 128, 364 with 192.
+constexpr long long PAD = 192;
+
 struct SsmArgs {
     SsmCall c;
     int H, hk;
-    int sh;              // log2 of a segment's tokens
-    unsigned ids;        // segment numbers
+    long long len;       // places of a share; 0: one share per sequence, its whole length
+    unsigned ids;        // shares
     float dt_min, dt_max;
     bool sp;
-    Divisor byHB;        // head blocks per segment
-    float *ws;           // [ids][H][dk*dv] states, then [ids][H] base-2 decay exponents
+    Divisor byHB;        // head blocks per share
+    // [ids][H][dk*dv] states where a share begins inside a sequence (at first
+    // that of the piece before), as many where a share's last sequence begins
+    // inside it and does not end there, then [ids][H] base-2 decay exponents
+    float *ws;
 };
 
 __device__ __forceinline__ floatx16 mma(bf16x8 a, bf16x8 b, floatx16 c)
@@ -225,8 +238,31 @@ struct SsmLds {
     int mode[2][HEADS];
 };
 
-// STATE: only the segment's own state and decay, from zero.
-template <int DK, int DV, int HPW, bool STATE, bool WIDE>
+// The last sequence that begins at place `at` or before it (sequence b begins
+// at cu[b] + PAD b): a probe per lane, 64 sequences a round, in [0, n) also
+// with bounds that break the rules.
+__device__ __forceinline__ int seq_at(const int32_t *cu, int n, long long at)
+{
+    const int lane = (int)(__builtin_amdgcn_workitem_id_x() & 63u);
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 63) / 64;
+        const long long p = lo + (long long)lane * step;
+        bool in = lane == 0;
+        if (p < hi && lane) in = (long long)cu[p] + PAD * p <= at;
+        const int k = __popcll(__ballot(in));
+        lo += (k - 1) * step;
+        if (lo + step < hi) hi = lo + step;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// A share: the pieces of sequences on its A.len places, one after another.
+// STATE: only the state and decay of its last piece, if that piece's sequence
+// goes on behind it.  MANY: a share may hold more than one piece; one alone
+// spares the loop's registers (16384 tokens of 64 heads of 128 x 64 191 us,
+// 195 with it, 300 tokens 32, 34).
+template <int DK, int DV, int HPW, bool STATE, bool MANY, bool WIDE>
 __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(SsmArgs A)
 {
     using G = SsmGeom<DK, DV, HPW>;
@@ -235,350 +271,373 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
     const int t = (int)__builtin_amdgcn_workitem_id_x(), lane = t & 63;
     const int wv = __builtin_amdgcn_readfirstlane(t >> 6);
     const int hw = wv % HPW, slice = wv / HPW;   // a head's first wave on each SIMD
-    // head blocks of a segment are neighbours (and so on all XCDs: giving them
-    // one XCD's numbers spread the segments unevenly and was no faster)
+    // head blocks of a share are neighbours (and so on all XCDs: giving them
+    // one XCD's numbers spread the work unevenly and was no faster)
     const unsigned g = __builtin_amdgcn_workgroup_id_x();
     const unsigned id = __builtin_amdgcn_readfirstlane(div_by(g, A.byHB));
-    if (id >= A.ids) return;
+    if (id + (STATE ? 1 : 0) >= A.ids) return;
     const int h0 = (int)(g - id * A.byHB.d) * HPW, head = h0 + hw;
     const int hb = h0 / (A.H / A.hk);
     const gdnq_ssm_io &io = A.c.io;
-    SeqTile q;
-    if (!seq_tile(A.c.cu, A.c.slots, A.c.n, (int)id, A.sh, A.c.T, A.c.n_slots, q)) return;
-    const bool multi = q.len > (1 << A.sh), last = ((long long)(q.k + 1) << A.sh) >= q.len;
-    if (STATE && last) return;
-    const size_t row0 = (size_t)q.start + ((size_t)q.k << A.sh);
-    const int ntok = min(1 << A.sh, q.len - (q.k << A.sh));
-
     const int c = lane & 31, hh = lane >> 5;
-    // the wave's state: accumulator r of block nb is row 32 nb + 8 (r/4) + 4 hh + r % 4, column 32 slice + c
-    floatx16 S[G::NBLK];
+    // accumulator r of the state's block nb is row 32 nb + 8 (r/4) + 4 hh + r % 4, column 32 slice + c
     const size_t soff = (size_t)(4 * hh) * DV + slice * 32 + c;
-    float *const pool = A.c.S + ((size_t)q.slot * A.H + head) * DK * DV + soff;
-    float *const seg = A.ws + ((size_t)id * A.H + head) * DK * DV + soff;   // touched only if multi
-    {
-        const float *from = multi ? seg : pool;
-        const bool load = !STATE && (multi || (A.c.cont && A.c.cont[q.seq]));
-#pragma unroll
-        for (int nb = 0; nb < G::NBLK; nb++)
-#pragma unroll
-            for (int r = 0; r < 16; r++) S[nb][r] = load ? from[(size_t)(32 * nb + 8 * (r / 4) + r % 4) * DV] : 0.0f;
-    }
     const float Ah = uniform(io.A[head] * 1.44269504f), bias = uniform(io.dt_bias ? io.dt_bias[head] : 0.0f);
     const float Dh = uniform(io.D ? io.D[head] : 0.0f);
-    float seglog = 0.0f;
-
-    // the thread's 16-byte pieces of a chunk's rows, B and C dealt out over
-    // the workgroup, x's 32 columns over the wave; rows behind the segment's
-    // end repeat its last one, with weights of zero.  Byte offsets from the
-    // chunk's first row: a row number below 64 times a distance below 2^24.
-    u32x4 rb[G::NB], rc[G::NB], rx[4];
-    constexpr int PK = DK / 8, RPI = G::NT / PK;   // pieces per row, rows per turn
-    const int br = t / PK;
-    const uint32_t bcol = (uint32_t)(hb * DK + t % PK * 8) * 2u;
-    const uint32_t xcol = (uint32_t)(head * DV + slice * 32 + lane % 4 * 8) * 2u;
-    // each of these advances by a chunk with every call
-    const uint32_t ldb = (uint32_t)io.ldb * 2u, ldc = (uint32_t)io.ldc * 2u, ldx = (uint32_t)io.ldx * 2u,
-                   ldy = (uint32_t)io.ldy * 2u, ldt = (uint32_t)io.lddt * 2u;
-    const char *pb = reinterpret_cast<const char *>(io.B) + row0 * ldb;
-    const char *pc = reinterpret_cast<const char *>(io.C) + row0 * ldc;
-    const char *px = reinterpret_cast<const char *>(io.x) + row0 * ldx;
-    const char *pt = reinterpret_cast<const char *>(io.dt) + row0 * ldt + (size_t)head * 2;
-    char *py = reinterpret_cast<char *>(io.y) + row0 * ldy;
-    const auto fetch = [&](int nv) {
-#pragma unroll
-        for (int i = 0; i < G::NB; i++) {
-            const uint32_t r = (uint32_t)min(br + i * RPI, nv - 1);
-            rb[i] = ld_global8<WIDE>(pb, row_bytes(r, ldb) + bcol);
-            if constexpr (!STATE) rc[i] = ld_global8<WIDE>(pc, row_bytes(r, ldc) + bcol);
-        }
-        pb += (size_t)CH * ldb;
-        pc += (size_t)CH * ldc;
-    };
-    const auto fetch_x = [&](int nv) {
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            rx[i] = ld_global8<WIDE>(px, row_bytes((uint32_t)min(16 * i + lane / 4, nv - 1), ldx) + xcol);
-        px += (size_t)CH * ldx;
-    };
-    uint32_t dt_in = 0;
-    const auto fetch_dt = [&](int nv) {   // widened at its use, or it would be waited for here
-        if (slice == 0) dt_in = *reinterpret_cast<const uint16_t *>(pt + row_bytes((uint32_t)min(lane, nv - 1), ldt));
-        pt += (size_t)CH * ldt;
-    };
-    const auto stage = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < G::NB; i++) {
-            const int r = br + i * RPI, k8 = t % PK;
-            *reinterpret_cast<u32x4 *>(&L.b[buf][r * G::SB + k8 * 8]) = rb[i];
-            if constexpr (!STATE) {
-                // columns of each 16 in the order 0-3, 8-11, 4-7, 12-15
-                __bf16 *d = &L.c[buf][r * G::SC + (k8 & ~1) * 8 + (k8 & 1) * 4];
-                *reinterpret_cast<uint2 *>(d) = make_uint2(rc[i][0], rc[i][1]);
-                *reinterpret_cast<uint2 *>(d + 8) = make_uint2(rc[i][2], rc[i][3]);
-            }
-        }
-    };
-    // decays of a chunk: one wave per head, one token per lane
-    const auto decays = [&](uint32_t dt, int nv, int buf) {
-        float d = low_of(dt) + bias;
-        if (A.sp) d = softplus(d);
-        d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
-        // 2^-256 is zero in fp32; the bound keeps the sums behind a token that
-        // forgets everything from losing the digits of its neighbours' decays
-        const float la = fmaxf(d * Ah, -256.0f);
-        float tot;
-        const float suf = suffix64(la, lane, tot);   // cs_63 - cs
-        const int mode = STATE || tot > -RANGE ? NEAR : tot > -2.0f * RANGE ? FAR : APART;
-        const float half = 0.5f * tot;
-        Vectors &v = L.v[buf][hw];
-        v[V_W][lane] = __builtin_amdgcn_exp2f(mode == FAR ? suf - half : suf) * d;
-        if constexpr (!STATE) {
-            v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : (mode == FAR ? half : tot) - suf);
-            v[V_CS][lane] = tot - suf;
-            v[V_D][lane] = d;
-        }
-        seglog += tot;
-        if (lane == 0) {
-            L.tot[buf][hw] = __builtin_amdgcn_exp2f(mode == FAR ? half : tot);
-            L.mode[buf][hw] = mode;
-        }
-    };
-
-    // tril(C B^T) of the chunk in buf: block n of the 10 blocks of 16 x 16 tokens
-    // on and below the diagonal, transposed, and its way into the operands
-    const int l16 = lane & 15, qd = lane >> 4;
-    const auto tri_i = [](int n) { return (int)((0x3333222110ull >> (4 * n)) & 15u); };
-    const auto tri_j = [](int n) { return (int)((0x3210210100ull >> (4 * n)) & 15u); };
-    const auto triangle = [&](int buf, int n) {
-        const __bf16 *pb = &L.b[buf][(16 * tri_j(n) + l16) * G::SB + 16 * (qd / 2) + 4 * (qd & 1)];
-        const __bf16 *pc = &L.c[buf][(16 * tri_i(n) + l16) * G::SC + 8 * qd];
-        floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < DK / 32; s++)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ld_rows(pb + 32 * s),
-                                                          *reinterpret_cast<const bf16x8 *>(pc + 32 * s), acc, 0, 0, 0);
-        return acc;
-    };
-    const auto put_triangle = [&](int buf, int n, floatx4 acc) {
-        const int I = tri_i(n), J = tri_j(n);   // row 4 qd + r of the block is token j, lane l16 token i
-        float m[4];
-        uint32_t part[2][2];
-#pragma unroll
-        for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
-        split<2, 4>(m, part);
-        const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
-#pragma unroll
-        for (int p = 0; p < 2; p++)
-            *reinterpret_cast<uint2 *>(&L.g[buf][f][p][at]) = make_uint2(part[p][0], part[p][1]);
-    };
-    const int n0 = wv;   // the wave's first block; the others follow NW apart
-
     if constexpr (!STATE) {   // the blocks above the diagonal stay zero
         for (int i = t; i < 2 * 6 * 2 * 64; i += G::NT)
             *reinterpret_cast<uint4 *>(&L.g[0][0][0][i * 8]) = make_uint4(0, 0, 0, 0);
     }
-    fetch_dt(min(CH, ntok));
-    fetch(min(CH, ntok));
-    fetch_x(min(CH, ntok));
-    if (slice == 0) decays(dt_in, min(CH, ntok), 0);
-    stage(0);
-    if (CH < ntok) fetch_dt(min(CH, ntok - CH));
-    if constexpr (!STATE) {
-        __syncthreads();
-        for (int n = n0; n < 10; n += G::NW) put_triangle(0, n, triangle(0, n));
-    }
-    // a chunk's outputs wait in the wave's x tile until the next chunk begins:
-    // there the loads of a chunk ago have long arrived, so that nothing waits for the stores
-    __bf16 *const xt = L.x[wv];
-    u32x4 yo[4];
-    const auto load_y = [&] {
-#pragma unroll
-        for (int n = 0; n < 4; n++) yo[n] = *reinterpret_cast<const u32x4 *>(&xt[(64 * n + lane) * 8]);
-    };
-    const auto store_y = [&](int nv) {
-#pragma unroll
-        for (int n = 0; n < 4; n++)
-            if (nv == CH || 16 * n + lane / 4 < nv)
-                st_global8<WIDE>(py, row_bytes((uint32_t)(16 * n + lane / 4), ldy) + xcol, yo[n]);
-        py += (size_t)CH * ldy;
-    };
-    int buf = 0;
-    for (int left = ntok; left > 0; left -= CH, buf ^= 1) {
-        const bool more = left > CH;
-        __syncthreads();   // the chunk is staged, and the previous one's buffers are free
-        if constexpr (!STATE) load_y();
-        wave_lds_sync();
-#pragma unroll
-        for (int i = 0; i < 4; i++) *reinterpret_cast<u32x4 *>(&xt[(64 * i + lane) * 8]) = rx[i];
-        uint32_t dt_now = dt_in;
-        asm volatile("" : "+v"(dt_now));   // arrived as well, before stores and new loads are on their way
-        if (!STATE && left < ntok) store_y(CH);
-        if (more) fetch(min(CH, left - CH));
-        if (slice == 0 && more) decays(dt_now, min(CH, left - CH), buf ^ 1);
-        wave_lds_sync();
-
-        const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
-        const Vectors &vec = L.v[buf][hw];
-        const float tot = uniform(L.tot[buf][hw]);
-        const int mode = STATE ? NEAR : __builtin_amdgcn_readfirstlane(L.mode[buf][hw]);
-        const bool apart = mode == APART;
-        bf16x8 xf[4];   // x rows 16 f .. + 15, the wave's columns
-#pragma unroll
-        for (int f = 0; f < 4; f++)
-            xf[f] = ld_cols(&xt[(16 * f + tr_r) * G::SX + tr_c], G::SX);
-
-        const auto decay_state = [&] {
+    const long long from = A.len * id, to = from + A.len;
+    const int b0 = A.len == 0 ? (int)id : seq_at(A.c.cu, A.c.n, STATE ? to - 1 : from);
+    for (int sq = b0; sq < A.c.n; sq++) {
+        if (MANY && sq > b0) {   // a bound out of range ends nothing: its sequences are skipped below
+            const int at = A.c.cu[sq];
+            if (at >= 0 && at <= A.c.T && at + PAD * sq >= to) return;
+        }
+        SeqTile q{};
+        const bool is = seq_rows(A.c.cu, A.c.slots, sq, A.c.T, A.c.n_slots, q);
+        // the piece's first token and the one behind its last, in the sequence
+        const long long v0 = q.start + PAD * sq;
+        const int t0 = A.len && from > v0 ? (int)min(from - v0, (long long)q.len) : 0;
+        const int t1 = A.len ? (int)max(min(to - v0, (long long)q.len), 0ll) : q.len;
+        const bool last = t1 == q.len;
+        if (!is || t0 >= t1 || (STATE && last)) {
+            if constexpr (MANY) continue;
+            return;
+        }
+        const size_t row0 = (size_t)q.start + t0;
+        const int ntok = t1 - t0;
+        floatx16 S[G::NBLK];   // the wave's state
+        float *const pool = A.c.S + ((size_t)q.slot * A.H + head) * DK * DV + soff;
+        const size_t one = (size_t)A.H * DK * DV, all = A.ids * one;
+        float *const mid = A.ws + id * one + (size_t)head * DK * DV + soff, *const begin = mid + all;   // if it is cut
+        {
+            const bool load = t0 > 0 ? !STATE : A.c.cont && A.c.cont[sq];
+            const float *src = t0 > 0 ? mid : STATE || last ? pool : begin;
 #pragma unroll
             for (int nb = 0; nb < G::NBLK; nb++)
 #pragma unroll
-                for (int r = 0; r < 16; r++) S[nb][r] *= tot;
+                for (int r = 0; r < 16; r++) S[nb][r] = load ? src[(size_t)(32 * nb + 8 * (r / 4) + r % 4) * DV] : 0.0f;
+            if (STATE && load) {   // the main kernel's last piece replaces it while the first is still to read it
+#pragma unroll
+                for (int nb = 0; nb < G::NBLK; nb++)
+#pragma unroll
+                    for (int r = 0; r < 16; r++) begin[(size_t)(32 * nb + 8 * (r / 4) + r % 4) * DV] = S[nb][r];
+            }
+        }
+        float seglog = 0.0f;
+
+        // the thread's 16-byte pieces of a chunk's rows, B and C dealt out over
+        // the workgroup, x's 32 columns over the wave; rows behind the piece's
+        // end repeat its last one, with weights of zero.  Byte offsets from the
+        // chunk's first row: a row number below 64 times a distance below 2^24.
+        u32x4 rb[G::NB], rc[G::NB], rx[4];
+        constexpr int PK = DK / 8, RPI = G::NT / PK;   // pieces per row, rows per turn
+        const int br = t / PK;
+        const uint32_t bcol = (uint32_t)(hb * DK + t % PK * 8) * 2u;
+        const uint32_t xcol = (uint32_t)(head * DV + slice * 32 + lane % 4 * 8) * 2u;
+        // each of these advances by a chunk with every call
+        const uint32_t ldb = (uint32_t)io.ldb * 2u, ldc = (uint32_t)io.ldc * 2u, ldx = (uint32_t)io.ldx * 2u,
+                       ldy = (uint32_t)io.ldy * 2u, ldt = (uint32_t)io.lddt * 2u;
+        const char *pb = reinterpret_cast<const char *>(io.B) + row0 * ldb;
+        const char *pc = reinterpret_cast<const char *>(io.C) + row0 * ldc;
+        const char *px = reinterpret_cast<const char *>(io.x) + row0 * ldx;
+        const char *pt = reinterpret_cast<const char *>(io.dt) + row0 * ldt + (size_t)head * 2;
+        char *py = reinterpret_cast<char *>(io.y) + row0 * ldy;
+        const auto fetch = [&](int nv) {
+#pragma unroll
+            for (int i = 0; i < G::NB; i++) {
+                const uint32_t r = (uint32_t)min(br + i * RPI, nv - 1);
+                rb[i] = ld_global8<WIDE>(pb, row_bytes(r, ldb) + bcol);
+                if constexpr (!STATE) rc[i] = ld_global8<WIDE>(pc, row_bytes(r, ldc) + bcol);
+            }
+            pb += (size_t)CH * ldb;
+            pc += (size_t)CH * ldc;
         };
-        floatx16 Y[2];
-        const auto scale_rows = [&] {   // Y rows by V_F
-            float4 e[8];
+        const auto fetch_x = [&](int nv) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) e[k] = *reinterpret_cast<const float4 *>(&vec[V_F][8 * k + 4 * hh]);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < 4; i++)
+                rx[i] = ld_global8<WIDE>(px, row_bytes((uint32_t)min(16 * i + lane / 4, nv - 1), ldx) + xcol);
+            px += (size_t)CH * ldx;
+        };
+        uint32_t dt_in = 0;
+        const auto fetch_dt = [&](int nv) {   // widened at its use, or it would be waited for here
+            if (slice == 0) dt_in = *reinterpret_cast<const uint16_t *>(pt + row_bytes((uint32_t)min(lane, nv - 1), ldt));
+            pt += (size_t)CH * ldt;
+        };
+        const auto stage = [&](int buf) {
 #pragma unroll
-            for (int k = 0; k < 8; k++) {
-                floatx16 &y = Y[k / 4];
-                const int r = 4 * (k % 4);
-                y[r] *= e[k].x, y[r + 1] *= e[k].y, y[r + 2] *= e[k].z, y[r + 3] *= e[k].w;
+            for (int i = 0; i < G::NB; i++) {
+                const int r = br + i * RPI, k8 = t % PK;
+                *reinterpret_cast<u32x4 *>(&L.b[buf][r * G::SB + k8 * 8]) = rb[i];
+                if constexpr (!STATE) {
+                    // columns of each 16 in the order 0-3, 8-11, 4-7, 12-15
+                    __bf16 *d = &L.c[buf][r * G::SC + (k8 & ~1) * 8 + (k8 & 1) * 4];
+                    *reinterpret_cast<uint2 *>(d) = make_uint2(rc[i][0], rc[i][1]);
+                    *reinterpret_cast<uint2 *>(d + 8) = make_uint2(rc[i][2], rc[i][3]);
+                }
             }
         };
-        const auto output = [&] {
-            // y = Y + D x to the wave's x tile; neighbouring lanes trade halves so
-            // that each writes two columns of a row
-            const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
+        // decays of a chunk: one wave per head, one token per lane
+        const auto decays = [&](uint32_t dt, int nv, int buf) {
+            float d = low_of(dt) + bias;
+            if (A.sp) d = softplus(d);
+            d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
+            // 2^-256 is zero in fp32; the bound keeps the sums behind a token that
+            // forgets everything from losing the digits of its neighbours' decays
+            const float la = fmaxf(d * Ah, -256.0f);
+            float tot;
+            const float suf = suffix64(la, lane, tot);   // cs_63 - cs
+            const int mode = STATE || tot > -RANGE ? NEAR : tot > -2.0f * RANGE ? FAR : APART;
+            const float half = 0.5f * tot;
+            Vectors &v = L.v[buf][hw];
+            v[V_W][lane] = __builtin_amdgcn_exp2f(mode == FAR ? suf - half : suf) * d;
+            if constexpr (!STATE) {
+                v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : (mode == FAR ? half : tot) - suf);
+                v[V_CS][lane] = tot - suf;
+                v[V_D][lane] = d;
+            }
+            seglog += tot;
+            if (lane == 0) {
+                L.tot[buf][hw] = __builtin_amdgcn_exp2f(mode == FAR ? half : tot);
+                L.mode[buf][hw] = mode;
+            }
+        };
+
+        // tril(C B^T) of the chunk in buf: block n of the 10 blocks of 16 x 16 tokens
+        // on and below the diagonal, transposed, and its way into the operands
+        const int l16 = lane & 15, qd = lane >> 4;
+        const auto tri_i = [](int n) { return (int)((0x3333222110ull >> (4 * n)) & 15u); };
+        const auto tri_j = [](int n) { return (int)((0x3210210100ull >> (4 * n)) & 15u); };
+        const auto triangle = [&](int buf, int n) {
+            const __bf16 *pb = &L.b[buf][(16 * tri_j(n) + l16) * G::SB + 16 * (qd / 2) + 4 * (qd & 1)];
+            const __bf16 *pc = &L.c[buf][(16 * tri_i(n) + l16) * G::SC + 8 * qd];
+            floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < DK / 32; s++)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ld_rows(pb + 32 * s),
+                                                              *reinterpret_cast<const bf16x8 *>(pc + 32 * s), acc, 0, 0, 0);
+            return acc;
+        };
+        const auto put_triangle = [&](int buf, int n, floatx4 acc) {
+            const int I = tri_i(n), J = tri_j(n);   // row 4 qd + r of the block is token j, lane l16 token i
+            float m[4];
+            uint32_t part[2][2];
+#pragma unroll
+            for (int r = 0; r < 4; r++) m[r] = I > J || 4 * qd + r <= l16 ? acc[r] : 0.0f;
+            split<2, 4>(m, part);
+            const int f = I < 2 ? J : 2 + J, at = ((qd & 1) * 32 + 16 * (I & 1) + l16) * 8 + 4 * (qd / 2);
+#pragma unroll
+            for (int p = 0; p < 2; p++)
+                *reinterpret_cast<uint2 *>(&L.g[buf][f][p][at]) = make_uint2(part[p][0], part[p][1]);
+        };
+        const int n0 = wv;   // the wave's first block; the others follow NW apart
+
+        fetch_dt(min(CH, ntok));
+        fetch(min(CH, ntok));
+        fetch_x(min(CH, ntok));
+        if (MANY && sq > b0) __syncthreads();   // the buffers of the piece before are free
+        if (slice == 0) decays(dt_in, min(CH, ntok), 0);
+        stage(0);
+        if (CH < ntok) fetch_dt(min(CH, ntok - CH));
+        if constexpr (!STATE) {
+            __syncthreads();
+            for (int n = n0; n < 10; n += G::NW) put_triangle(0, n, triangle(0, n));
+        }
+        // a chunk's outputs wait in the wave's x tile until the next chunk begins:
+        // there the loads of a chunk ago have long arrived, so that nothing waits for the stores
+        __bf16 *const xt = L.x[wv];
+        u32x4 yo[4];
+        const auto load_y = [&] {
+#pragma unroll
+            for (int n = 0; n < 4; n++) yo[n] = *reinterpret_cast<const u32x4 *>(&xt[(64 * n + lane) * 8]);
+        };
+        const auto store_y = [&](int nv) {
+#pragma unroll
+            for (int n = 0; n < 4; n++)
+                if (nv == CH || 16 * n + lane / 4 < nv)
+                    st_global8<WIDE>(py, row_bytes((uint32_t)(16 * n + lane / 4), ldy) + xcol, yo[n]);
+            py += (size_t)CH * ldy;
+        };
+        int buf = 0;
+        for (int left = ntok; left > 0; left -= CH, buf ^= 1) {
+            const bool more = left > CH;
+            __syncthreads();   // the chunk is staged, and the previous one's buffers are free
+            if constexpr (!STATE) load_y();
             wave_lds_sync();
 #pragma unroll
-            for (int ib = 0; ib < 2; ib++)
+            for (int i = 0; i < 4; i++) *reinterpret_cast<u32x4 *>(&xt[(64 * i + lane) * 8]) = rx[i];
+            uint32_t dt_now = dt_in;
+            asm volatile("" : "+v"(dt_now));   // arrived as well, before stores and new loads are on their way
+            if (!STATE && left < ntok) store_y(CH);
+            if (more) fetch(min(CH, left - CH));
+            if (slice == 0 && more) decays(dt_now, min(CH, left - CH), buf ^ 1);
+            wave_lds_sync();
+
+            const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
+            const Vectors &vec = L.v[buf][hw];
+            const float tot = uniform(L.tot[buf][hw]);
+            const int mode = STATE ? NEAR : __builtin_amdgcn_readfirstlane(L.mode[buf][hw]);
+            const bool apart = mode == APART;
+            bf16x8 xf[4];   // x rows 16 f .. + 15, the wave's columns
 #pragma unroll
-                for (int r = 0; r < 16; r += 2) {
-                    const uint32_t xr = __builtin_bit_cast(u32x4, xf[2 * ib + r / 8])[r % 8 / 2];
-                    const uint32_t u = pack2(fmaf(Dh, low_of(xr), Y[ib][r]), fmaf(Dh, high_of(xr), Y[ib][r + 1]));
-                    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
-                    const int i = 32 * ib + 8 * (r / 4) + r % 4 + 4 * hh + (lane & 1);
-                    *reinterpret_cast<uint32_t *>(&xt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
+            for (int f = 0; f < 4; f++)
+                xf[f] = ld_cols(&xt[(16 * f + tr_r) * G::SX + tr_c], G::SX);
+
+            const auto decay_state = [&] {
+#pragma unroll
+                for (int nb = 0; nb < G::NBLK; nb++)
+#pragma unroll
+                    for (int r = 0; r < 16; r++) S[nb][r] *= tot;
+            };
+            floatx16 Y[2];
+            const auto scale_rows = [&] {   // Y rows by V_F
+                float4 e[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++) e[k] = *reinterpret_cast<const float4 *>(&vec[V_F][8 * k + 4 * hh]);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    floatx16 &y = Y[k / 4];
+                    const int r = 4 * (k % 4);
+                    y[r] *= e[k].x, y[r + 1] *= e[k].y, y[r + 2] *= e[k].z, y[r + 3] *= e[k].w;
                 }
-        };
-        if (!apart) decay_state();
-        if constexpr (!STATE) {
+            };
+            const auto output = [&] {
+                // y = Y + D x to the wave's x tile; neighbouring lanes trade halves so
+                // that each writes two columns of a row
+                const uint32_t sel = (lane & 1) ? 0x03020706u : 0x05040100u;
+                wave_lds_sync();
 #pragma unroll
-            for (int r = 0; r < 16; r++) Y[0][r] = Y[1][r] = 0.0f;
+                for (int ib = 0; ib < 2; ib++)
 #pragma unroll
-            for (int s = 0; s < DK / 16; s++) {
-                const bf16x8 ca = *reinterpret_cast<const bf16x8 *>(&L.c[buf][c * G::SC + 16 * s + 8 * hh]);
-                const bf16x8 cb = *reinterpret_cast<const bf16x8 *>(&L.c[buf][(32 + c) * G::SC + 16 * s + 8 * hh]);
-                float sv[8];
-                uint32_t part[2][4];
-#pragma unroll
-                for (int e = 0; e < 8; e++) sv[e] = S[s / 2][8 * (s & 1) + e];
-                split<2, 8>(sv, part);
-                Y[0] = mma(ca, operand(part[0]), Y[0]);
-                Y[1] = mma(cb, operand(part[0]), Y[1]);
-                Y[0] = mma(ca, operand(part[1]), Y[0]);
-                Y[1] = mma(cb, operand(part[1]), Y[1]);
-            }
-            if (apart) {
-                scale_rows();
-#pragma unroll
-                for (int fr = 0; fr < 6; fr++) {
-                    const int ib = fr >= 2, f = ib ? fr - 2 : fr;
-                    const u32x4 gh = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][0][lane * 8]);
-                    const u32x4 gl = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][1][lane * 8]);
-                    const float ci = vec[V_CS][32 * ib + c];
-                    float m[8];
-                    uint32_t part[2][4];
-#pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        const int j = 16 * f + 8 * (e / 4) + 4 * hh + e % 4;
-                        const float gv = (e & 1) ? high_of(gh[e / 2]) + high_of(gl[e / 2])
-                                                 : low_of(gh[e / 2]) + low_of(gl[e / 2]);
-                        // above the diagonal gv is zero, and the exponent is kept from overflowing
-                        m[e] = gv * (vec[V_D][j] * __builtin_amdgcn_exp2f(fminf(ci - vec[V_CS][j], 0.0f)));
+                    for (int r = 0; r < 16; r += 2) {
+                        const uint32_t xr = __builtin_bit_cast(u32x4, xf[2 * ib + r / 8])[r % 8 / 2];
+                        const uint32_t u = pack2(fmaf(Dh, low_of(xr), Y[ib][r]), fmaf(Dh, high_of(xr), Y[ib][r + 1]));
+                        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, DPP_XOR1, 0xF, 0xF, true);
+                        const int i = 32 * ib + 8 * (r / 4) + r % 4 + 4 * hh + (lane & 1);
+                        *reinterpret_cast<uint32_t *>(&xt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
                     }
-                    split<2, 8>(m, part);
-                    Y[ib] = mma(operand(part[0]), xf[f], Y[ib]);
-                    Y[ib] = mma(operand(part[1]), xf[f], Y[ib]);
-                }
-                output();
-                decay_state();
-            }
-        }
-        floatx4 tri = {};
-        if constexpr (!STATE) {
-            if (more) stage(buf ^ 1);
-            __syncthreads();   // the next chunk is staged (if there is one: the blocks of a chunk behind the last are not used)
-        }
-        if (left > 2 * CH) fetch_dt(min(CH, left - 2 * CH));
-        if (more) fetch_x(min(CH, left - CH));
-        if constexpr (!STATE) tri = triangle(buf ^ 1, n0);
-        // ---- S' + B^T (w x), and tril(C B^T) (w x) (not used of a chunk set APART)
-#pragma unroll
-        for (int f = 0; f < 4; f++) {
-            const u32x4 xr = __builtin_bit_cast(u32x4, xf[f]);
-            float wx[8];
-            uint32_t part[3][4];
-#pragma unroll
-            for (int k = 0; k < 2; k++) {
-                const float4 w = *reinterpret_cast<const float4 *>(&vec[V_W][16 * f + 8 * k + 4 * hh]);
-                wx[4 * k] = w.x * low_of(xr[2 * k]);
-                wx[4 * k + 1] = w.y * high_of(xr[2 * k]);
-                wx[4 * k + 2] = w.z * low_of(xr[2 * k + 1]);
-                wx[4 * k + 3] = w.w * high_of(xr[2 * k + 1]);
-            }
-            split<3, 8>(wx, part);
-            const bf16x8 xh = operand(part[0]), xm = operand(part[1]), xl = operand(part[2]);
+            };
+            if (!apart) decay_state();
             if constexpr (!STATE) {
 #pragma unroll
-                for (int ib = f / 2; ib < 2; ib++) {
-                    const int fr = ib ? 2 + f : f;
-                    const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][0][lane * 8]);
-                    const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][1][lane * 8]);
-                    Y[ib] = mma(gh, xh, Y[ib]);
-                    Y[ib] = mma(gl, xh, Y[ib]);
-                    Y[ib] = mma(gh, xm, Y[ib]);
+                for (int r = 0; r < 16; r++) Y[0][r] = Y[1][r] = 0.0f;
+#pragma unroll
+                for (int s = 0; s < DK / 16; s++) {
+                    const bf16x8 ca = *reinterpret_cast<const bf16x8 *>(&L.c[buf][c * G::SC + 16 * s + 8 * hh]);
+                    const bf16x8 cb = *reinterpret_cast<const bf16x8 *>(&L.c[buf][(32 + c) * G::SC + 16 * s + 8 * hh]);
+                    float sv[8];
+                    uint32_t part[2][4];
+#pragma unroll
+                    for (int e = 0; e < 8; e++) sv[e] = S[s / 2][8 * (s & 1) + e];
+                    split<2, 8>(sv, part);
+                    Y[0] = mma(ca, operand(part[0]), Y[0]);
+                    Y[1] = mma(cb, operand(part[0]), Y[1]);
+                    Y[0] = mma(ca, operand(part[1]), Y[0]);
+                    Y[1] = mma(cb, operand(part[1]), Y[1]);
+                }
+                if (apart) {
+                    scale_rows();
+#pragma unroll
+                    for (int fr = 0; fr < 6; fr++) {
+                        const int ib = fr >= 2, f = ib ? fr - 2 : fr;
+                        const u32x4 gh = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][0][lane * 8]);
+                        const u32x4 gl = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][1][lane * 8]);
+                        const float ci = vec[V_CS][32 * ib + c];
+                        float m[8];
+                        uint32_t part[2][4];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const int j = 16 * f + 8 * (e / 4) + 4 * hh + e % 4;
+                            const float gv = (e & 1) ? high_of(gh[e / 2]) + high_of(gl[e / 2])
+                                                     : low_of(gh[e / 2]) + low_of(gl[e / 2]);
+                            // above the diagonal gv is zero, and the exponent is kept from overflowing
+                            m[e] = gv * (vec[V_D][j] * __builtin_amdgcn_exp2f(fminf(ci - vec[V_CS][j], 0.0f)));
+                        }
+                        split<2, 8>(m, part);
+                        Y[ib] = mma(operand(part[0]), xf[f], Y[ib]);
+                        Y[ib] = mma(operand(part[1]), xf[f], Y[ib]);
+                    }
+                    output();
+                    decay_state();
                 }
             }
-#pragma unroll
-            for (int nb = 0; nb < G::NBLK; nb++) {
-                const bf16x8 bt = ld_cols(&L.b[buf][(16 * f + tr_r) * G::SB + 32 * nb + tr_c], G::SB);
-                S[nb] = mma(bt, xh, S[nb]);
-                S[nb] = mma(bt, xm, S[nb]);
-                S[nb] = mma(bt, xl, S[nb]);
+            floatx4 tri = {};
+            if constexpr (!STATE) {
+                if (more) stage(buf ^ 1);
+                __syncthreads();   // the next chunk is staged (if there is one: the blocks of a chunk behind the last are not used)
             }
+            if (left > 2 * CH) fetch_dt(min(CH, left - 2 * CH));
+            if (more) fetch_x(min(CH, left - CH));
+            if constexpr (!STATE) tri = triangle(buf ^ 1, n0);
+            // ---- S' + B^T (w x), and tril(C B^T) (w x) (not used of a chunk set APART)
+#pragma unroll
+            for (int f = 0; f < 4; f++) {
+                const u32x4 xr = __builtin_bit_cast(u32x4, xf[f]);
+                float wx[8];
+                uint32_t part[3][4];
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const float4 w = *reinterpret_cast<const float4 *>(&vec[V_W][16 * f + 8 * k + 4 * hh]);
+                    wx[4 * k] = w.x * low_of(xr[2 * k]);
+                    wx[4 * k + 1] = w.y * high_of(xr[2 * k]);
+                    wx[4 * k + 2] = w.z * low_of(xr[2 * k + 1]);
+                    wx[4 * k + 3] = w.w * high_of(xr[2 * k + 1]);
+                }
+                split<3, 8>(wx, part);
+                const bf16x8 xh = operand(part[0]), xm = operand(part[1]), xl = operand(part[2]);
+                if constexpr (!STATE) {
+#pragma unroll
+                    for (int ib = f / 2; ib < 2; ib++) {
+                        const int fr = ib ? 2 + f : f;
+                        const bf16x8 gh = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][0][lane * 8]);
+                        const bf16x8 gl = *reinterpret_cast<const bf16x8 *>(&L.g[buf][fr][1][lane * 8]);
+                        Y[ib] = mma(gh, xh, Y[ib]);
+                        Y[ib] = mma(gl, xh, Y[ib]);
+                        Y[ib] = mma(gh, xm, Y[ib]);
+                    }
+                }
+#pragma unroll
+                for (int nb = 0; nb < G::NBLK; nb++) {
+                    const bf16x8 bt = ld_cols(&L.b[buf][(16 * f + tr_r) * G::SB + 32 * nb + tr_c], G::SB);
+                    S[nb] = mma(bt, xh, S[nb]);
+                    S[nb] = mma(bt, xm, S[nb]);
+                    S[nb] = mma(bt, xl, S[nb]);
+                }
+            }
+            if (STATE && more) stage(buf ^ 1);
+            if constexpr (!STATE) {
+                put_triangle(buf ^ 1, n0, tri);
+                for (int n = n0 + G::NW; n < 10; n += G::NW) put_triangle(buf ^ 1, n, triangle(buf ^ 1, n));
+            }
+            if (mode == FAR) decay_state();
+            if constexpr (!STATE)
+                if (!apart) {
+                    scale_rows();
+                    output();
+                }
         }
-        if (STATE && more) stage(buf ^ 1);
         if constexpr (!STATE) {
-            put_triangle(buf ^ 1, n0, tri);
-            for (int n = n0 + G::NW; n < 10; n += G::NW) put_triangle(buf ^ 1, n, triangle(buf ^ 1, n));
+            wave_lds_sync();
+            load_y();
+            store_y((ntok - 1) % CH + 1);
         }
-        if (mode == FAR) decay_state();
-        if constexpr (!STATE)
-            if (!apart) {
-                scale_rows();
-                output();
-            }
-    }
-    if constexpr (!STATE) {
-        wave_lds_sync();
-        load_y();
-        store_y((ntok - 1) % CH + 1);
-    }
-    if (STATE || last) {
-        float *to = STATE ? seg : pool;
+        if (STATE || last) {
+            float *end = STATE ? mid + one : pool;   // STATE: in the next share's place, whose start it leads to
 #pragma unroll
-        for (int nb = 0; nb < G::NBLK; nb++)
+            for (int nb = 0; nb < G::NBLK; nb++)
 #pragma unroll
-            for (int r = 0; r < 16; r++) to[(size_t)(32 * nb + 8 * (r / 4) + r % 4) * DV] = S[nb][r];
+                for (int r = 0; r < 16; r++) end[(size_t)(32 * nb + 8 * (r / 4) + r % 4) * DV] = S[nb][r];
+        }
+        if (STATE && slice == 0 && lane == 0) A.ws[2 * all + (size_t)id * A.H + head] = seglog;
+        if constexpr (!MANY) return;
     }
-    if (STATE && slice == 0 && lane == 0) A.ws[(size_t)A.ids * A.H * DK * DV + (size_t)id * A.H + head] = seglog;
 }
 
-// Along each sequence of several segments: the state at every segment's
-// start, in the place of the segment's own state.  One thread per 4 values.
+// Along each sequence of several pieces: the state at every later piece's
+// start, in the place of the state of the piece before.  One thread per 4 values.
 template <int E>
 __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart, Divisor byH)
 {
@@ -587,26 +646,21 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart
     const unsigned b = div_by(bh, byH), h = bh - b * byH.d;
     SeqTile q;
     if (!seq_rows(A.c.cu, A.c.slots, (int)b, A.c.T, A.c.n_slots, q)) return;
-    const int n = (int)(((long long)q.len + (1 << A.sh) - 1) >> A.sh);
-    if (n < 2) return;
-    const size_t at = (size_t)part * 256 + __builtin_amdgcn_workitem_id_x();
-    const size_t id0 = (size_t)(q.start >> A.sh) + b, step = (size_t)A.H * E / 4;
-    float4 *ws = reinterpret_cast<float4 *>(A.ws) + (id0 * A.H + h) * (E / 4) + at;
-    const float *lg = A.ws + (size_t)A.ids * A.H * E + id0 * A.H + h;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (A.c.cont && A.c.cont[b]) v = reinterpret_cast<const float4 *>(A.c.S)[((size_t)q.slot * A.H + h) * (E / 4) + at];
-    for (int k = 0; k < n; k++) {
-        const size_t o = (size_t)k * step;
-        if (k + 1 < n) {
-            const float4 l = ws[o];
-            const float a = exp2f(lg[(size_t)k * A.H]);
-            ws[o] = v;
-            v.x = fmaf(a, v.x, l.x);
-            v.y = fmaf(a, v.y, l.y);
-            v.z = fmaf(a, v.z, l.z);
-            v.w = fmaf(a, v.w, l.w);
-        } else
-            ws[o] = v;
+    const long long v0 = q.start + PAD * b;
+    const size_t first = (size_t)(v0 / A.len), end = (size_t)((v0 + q.len - 1) / A.len);   // the shares it is in
+    if (first == end) return;
+    const size_t at = (size_t)part * 256 + __builtin_amdgcn_workitem_id_x(), step = (size_t)A.H * E / 4;
+    float4 *ws = reinterpret_cast<float4 *>(A.ws) + (size_t)h * (E / 4) + at;
+    const float *lg = A.ws + 2 * (size_t)A.ids * A.H * E + h;
+    float4 v = ws[(first + 1) * step];
+    for (size_t k = first + 2; k <= end; k++) {
+        const float4 l = ws[k * step];
+        const float a = exp2f(lg[(k - 1) * A.H]);
+        v.x = fmaf(a, v.x, l.x);
+        v.y = fmaf(a, v.y, l.y);
+        v.z = fmaf(a, v.z, l.z);
+        v.w = fmaf(a, v.w, l.w);
+        ws[k * step] = v;
     }
 }
 
@@ -620,47 +674,52 @@ int heads_per_group(const gdnq_ssm_desc &d)
     return 1;
 }
 
-// log2 of a segment's tokens.  Up to 384 tokens take one segment: the two
-// other kernels cost more than they save (300 tokens of 64 heads of 128 x 64:
-// 36 us, 39 in segments of 128; 512 tokens: 56, 47).  Above, the length from
-// 128 on with the least estimated time: a workgroup per compute unit and round,
-// 6.0 us a chunk and half as much again per segment in the main kernel, 3.4 us
-// a chunk and one more per segment in the states' kernel, and the joined states
-// at 5 TB/s (dk = 128; with dk = 64 all three are about half).  Measured in us
-// for segments of 256, 512, 1024, 2048: 16384 tokens of 64 heads of 128 x 64
-// 275, 218, 193, 293; 32731 tokens in 9 sequences of 32 heads of 128 x 128 -,
-// 465, 454, 505; 32768 tokens in 4 sequences of 80 heads of 128 x 64 -, 588,
-// 530, 610; 6000 tokens in 20 sequences of 24 heads 57, 83 (128: 72).
-int segment_shift(const gdnq_ssm_desc &d, int hpw, int n, int T)
+struct Shares {
+    long long len;   // SsmArgs::len
+    unsigned ids;
+};
+
+// How a call is dealt out.  Up to 384 tokens a share is a whole sequence: the
+// two other kernels cost more than they save (300 tokens of 64 heads of
+// 128 x 64: 32 us; 39 when cut at 128).  Above, equal shares of the places for
+// about one to six rounds of one workgroup per compute unit, or for an eighth
+// to half of one, or one share for all, whichever has the least estimated time: 6.0 us
+// a chunk and half as much again to begin in the main kernel, 3.4 us a chunk
+// and one more in the states' kernel, and the joined states at 5 TB/s (dk =
+// 128; with dk = 64 all three are about half).  Measured in us for half a
+// round, one, two, three: 16384 tokens of 64 heads of 128 x 64 290, 194, 224,
+// 257; 32731 tokens in 9 sequences of 32 heads of 128 x 128 566, 368, 404, 423;
+// 32768 in 4 of 80 heads of 128 x 64 1196, 635, 634, 633; 6000 in 20 of 24
+// heads 79, 63, 78, 79.
+Shares shares(const gdnq_ssm_desc &d, int n, int T)
 {
-    if (T <= 384) return 9;
-    const double blocks = d.H / hpw, join = (double)d.H * 128 * d.dv * 8 / 5e6;
-    const auto rounds = [&](double segs) { return std::ceil(segs * blocks / 256.0); };
-    int best = 7;
-    double least = 0.0;
-    for (int sh = 7; sh <= 20; sh++) {
-        const double len = (double)(1 << sh), chunks = len / CH;
-        // segments of sequences that are long against them, half of one lost to each one's end
-        const double all = n == 1 ? std::ceil(T / len) : std::fmax((double)n, T / len + 0.5 * n);
-        const double us = rounds(all) * (chunks + 1.5) * 6.0 + rounds(all - n) * (chunks + 1.0) * 3.4 + all * join;
-        if (sh == 7 || us < least) {
-            best = sh;
+    if (T <= 384) return {0, (unsigned)n};
+    const double blocks = d.H / heads_per_group(d), join = (double)d.H * 128 * d.dv * 8 / 5e6;
+    const long long places = T + PAD * (n - 1);
+    Shares best{places, 1};
+    double least = std::ceil(blocks / 256.0) * ((double)places / CH + 1.5) * 6.0;
+    for (const double r : {0.125, 0.25, 0.5, 1.0, 2.0, 3.0, 4.0, 6.0}) {
+        const long long want = (long long)(r * 256.0 / blocks);
+        if (want < 2) continue;
+        const long long len = std::max(((places + want - 1) / want + CH - 1) / CH * CH, 2ll * CH);
+        const double ids = (double)((places + len - 1) / len), chunks = (double)len / CH;
+        const double us = std::ceil(ids * blocks / 256.0) * (chunks + 1.5) * 6.0 +
+                          std::ceil((ids - 1.0) * blocks / 256.0) * (chunks + 1.0) * 3.4 + (ids - 1.0) * join;
+        if (us < least) {
+            best = {len, (unsigned)ids};
             least = us;
         }
-        if (len >= T) break;
     }
     return best;
 }
-
-unsigned segment_ids(int n, int T, int sh) { return (unsigned)(T >> sh) + (unsigned)n; }
 
 }  // namespace
 
 size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T)
 {
-    const int sh = segment_shift(d, heads_per_group(d), n, T);
-    if (T <= 1 << sh) return 0;
-    return (size_t)segment_ids(n, T, sh) * (size_t)d.H * ((size_t)d.dk * d.dv + 1) * 4;
+    const unsigned ids = shares(d, n, T).ids;
+    if (T <= 384 || ids == 1) return 0;
+    return (size_t)ids * (size_t)d.H * (2 * (size_t)d.dk * d.dv + 1) * 4;
 }
 
 hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStream_t st)
@@ -668,23 +727,28 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
     const gdnq_ssm_io &io = c.io;
     const bool wide = wide_rows(io.x, io.ldx, 2) && wide_rows(io.B, io.ldb, 2) && wide_rows(io.C, io.ldc, 2) &&
                       wide_rows(io.y, io.ldy, 2);
-    const int hk = d.hk ? d.hk : d.H, hpw = wide ? heads_per_group(d) : 1, sh = segment_shift(d, heads_per_group(d), c.n, c.T);
-    const unsigned ids = segment_ids(c.n, c.T, sh), blocks = (unsigned)(d.H / hpw);
-    const SsmArgs A{c, d.H, hk, sh, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
+    const int hk = d.hk ? d.hk : d.H, hpw = wide ? heads_per_group(d) : 1;
+    const Shares sh = shares(d, c.n, c.T);
+    const unsigned ids = sh.ids, blocks = (unsigned)(d.H / hpw);
+    const SsmArgs A{c, d.H, hk, sh.len, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
                     make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
     return with_dims(d.dk, d.dv, [&](auto DK, auto DV) {
         const auto go = [&](auto HPW, auto WIDE) {
             using G = SsmGeom<DK.value, DV.value, HPW.value>;
             constexpr bool W = decltype(WIDE)::value;
-            if (c.T > 1 << sh) {
-                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, W>), dim3(ids * blocks),
-                                   dim3(G::NT), 0, st, A);
+            if (sh.len && ids > 1) {
+                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, false, W>),
+                                   dim3((ids - 1) * blocks), dim3(G::NT), 0, st, A);
                 constexpr unsigned parts = DK.value * DV.value / 1024;
                 hipLaunchKernelGGL((ssm_join_kernel<DK.value * DV.value>), dim3((unsigned)c.n * d.H * parts), dim3(256),
                                    0, st, A, make_divisor(parts), make_divisor((unsigned)d.H));
             }
-            hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, W>), dim3(ids * blocks),
-                               dim3(G::NT), 0, st, A);
+            if (sh.len && c.n > 1)
+                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, true, W>), dim3(ids * blocks),
+                                   dim3(G::NT), 0, st, A);
+            else
+                hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, false, W>),
+                                   dim3(ids * blocks), dim3(G::NT), 0, st, A);
             return hipGetLastError();
         };
         if (!wide) return go(std::integral_constant<int, 1>{}, std::false_type{});

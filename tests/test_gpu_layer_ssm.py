@@ -194,6 +194,49 @@ def test_prompts(case, mode):
     assert bool((ywide[:, :off] == 7).all()) and bool((ywide[:, off + H * dv:] == 7).all())
 
 
+# more than 384 tokens, many sequences: a workgroup takes several, the last of
+# which may go on in another's (several short ones in a row, a cut just behind
+# a start or before an end, empty ones between, hundreds of head blocks)
+SHARED = [
+    (64, 64, 64, 1, [3] * 60 + [900, 0, 1] + [2] * 30 + [65, 64, 0, 0, 127], 9, 0, False),
+    (48, 128, 64, 1, [130, 120, 140, 1, 128, 64, 192, 500], 0, 0, True),
+    (16, 128, 128, 2, [1, 1, 1, 1200, 1, 1, 300, 0, 450], 4, 8, False),
+    (300, 64, 64, 300, [150, 60, 200], 1, 0, False),
+    (9, 64, 128, 3, [385, 1, 1, 1, 1], 0, 2, False),
+]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=[f"H{c[0]}-{c[1]}x{c[2]}-hk{c[3]}-n{len(c[4])}-T{sum(c[4])}" for c in SHARED])
+@pytest.mark.parametrize("mode", ["mixed", "new"])
+def test_prompts_that_share_workgroups(case, mode):
+    test_prompts(case, mode)
+
+
+@pytest.mark.parametrize("cu", [[0, 400, 1501], [-5, 400, 1000], [0, 2 ** 31 - 1, 1000], [1070, 960, 950],
+                                [0, 900, -2 ** 31], [0, 900, 300], [-2 ** 31, 2 ** 31 - 1, 1500]])
+def test_bounds_that_break_the_rules_of_long_calls(cu):
+    torch = torch_cuda()
+    g = lib()
+    say("ssm long bounds", cu)
+    H, dk, dv, T = 16, 64, 64, 1500
+    p = _problem(1, T, H, dk, dv, 1, "bf16", 2)
+    desc = g.SsmDesc(H=H, dk=dk, dv=dv, hk=1)
+    d = _dev(p)
+    buf = torch.full((T + 128, H * dv), 3.0, dtype=torch.bfloat16, device="cuda")
+    nb = g.gdnq_ssm_workspace(desc, 2, T)
+    assert nb > 0
+    ws = torch.zeros(nb + 64, dtype=torch.uint8, device="cuda")
+    cont = torch.ones(2, dtype=torch.int32, device="cuda")
+    g.gdnq_ssm_prefill(desc, d["x"], d["B"], d["C"], d["dt"], d["A"], None, None, buf[64:64 + T], d["S"], 2, None,
+                       cont, torch.tensor(cu, dtype=torch.int32, device="cuda"), 2, T, ws)
+    torch.cuda.synchronize()
+    assert (buf[:64] == 3).all() and (buf[64 + T:] == 3).all()
+    assert (ws[-64:] == 0).all()
+    for i in range(2):
+        if not 0 <= cu[i] < cu[i + 1] <= T:
+            assert np.array_equal(d["S"][i].cpu().numpy(), p["S"][i])
+
+
 def test_bounds_that_break_the_rules_touch_nothing_outside():
     torch = torch_cuda()
     g = lib()
