@@ -6,7 +6,10 @@
 // bound by HBM; the row (or group) stays in registers between its sum of
 // squares and its output.  NT threads hold one group, K pieces of V values
 // each, piece k of thread t at (k NT + t) V, so every access of a wave is
-// consecutive.  NT and K grow with the group (norm_dispatch).
+// consecutive.  NT and K grow with the group (norm_dispatch).  Measured in
+// bf16: 32768 rows of 4096 gated in groups of 512 135 us (6.0 TB/s; a large
+// copy reaches 5.0), 32768 x 4096 on an fp32 residual stream with a norm
+// behind the block 297 us (5.4 TB/s).
 #include "layer_launchers.hpp"
 #include "rows.hpp"
 

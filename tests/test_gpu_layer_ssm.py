@@ -212,6 +212,32 @@ def test_prompts_that_share_workgroups(case, mode):
     test_prompts(case, mode)
 
 
+def test_sequences_between_skipped_ones_of_long_calls():
+    """Sequences with bounds before the first row, behind the last, or with a
+    slot outside the pool are left out; those between them are whole."""
+    torch = torch_cuda()
+    g = lib()
+    say("ssm long skips")
+    H, dk, dv, T = 32, 64, 64, 1400
+    cu = np.array([-3, 5, 300, 302, 500, 1290, 1390, 1401, 5000], np.int32)
+    slots = np.array([0, 1, 2, 9, 4, 5, 6, 7], np.int32)
+    cont = np.array([1, 1, 0, 1, 1, 0, 1, 1], np.int32)
+    p = _problem(4, T, H, dk, dv, 1, "bf16", 8)
+    d = _dev(p)
+    y = torch.full_like(d["x"], 7.0)
+    desc = g.SsmDesc(H=H, dk=dk, dv=dv, hk=1)
+    nb = g.gdnq_ssm_workspace(desc, 8, T)
+    assert nb > 0
+    up = lambda v: torch.from_numpy(v).cuda()  # noqa: E731
+    g.gdnq_ssm_prefill(desc, d["x"], d["B"], d["C"], d["dt"], d["A"], d["D"], d["dt_bias"], y, d["S"], 8, up(slots),
+                       up(cont), up(cu), 8, T, torch.full((nb,), 0x7F, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    for i in (0, 6, 7):
+        slots[i] = -1
+    _check_prompts(p, y.double().cpu().numpy().reshape(T, H, dv), d["S"].double().cpu().numpy(), slots, cont, cu, 8,
+                   H, dk, dv, 1)
+
+
 @pytest.mark.parametrize("cu", [[0, 400, 1501], [-5, 400, 1000], [0, 2 ** 31 - 1, 1000], [1070, 960, 950],
                                 [0, 900, -2 ** 31], [0, 900, 300], [-2 ** 31, 2 ** 31 - 1, 1500]])
 def test_bounds_that_break_the_rules_of_long_calls(cu):

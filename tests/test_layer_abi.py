@@ -283,3 +283,22 @@ def test_binding_refuses_host_tensors_and_other_types(g):
     for f in (lambda t: layer._flat(t, 4, bf, 0, "w"), lambda t: layer._rows(t, 4, 64, bf, 0, "w")):
         with pytest.raises(g.GdnqError, match="current device"):
             f(OnGpu(x, 1))
+
+
+@pytest.mark.parametrize("name", ["ldx", "ldb", "ldc", "lddt", "ldy"])
+def test_ssm_prompt_rows_far_apart(g, name):
+    rc, m = _ssm(g, T=2, ld={name: (1 << 22) + 1})
+    assert rc == 2 and "2^22" in m
+
+
+@pytest.mark.parametrize("H,dk,dv,hk", [(1, 64, 64, 1), (64, 128, 64, 1), (32, 128, 128, 8), (600, 64, 128, 600)])
+def test_ssm_workspace_bounds(g, H, dk, dv, hk):
+    """None for a call of few tokens; never more than two states and a decay
+    for each 64 tokens of all sequences with 192 more each."""
+    d = g.SsmDesc(H=H, dk=dk, dv=dv, hk=hk)
+    one = H * (2 * dk * dv + 1) * 4
+    for n in (1, 3, 1000, 2 ** 20):
+        assert g.gdnq_ssm_workspace(d, n, 384) == 0
+        for T in (385, 5000, 2 ** 20, 2 ** 31 - 1):
+            nb = g.gdnq_ssm_workspace(d, n, T)
+            assert nb % one == 0 and 0 <= nb // one <= (T + 192 * n) // 64 + 1 and nb // one <= 6 * 256
