@@ -637,18 +637,21 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
 }
 
 // Along each sequence of several pieces: the state at every later piece's
-// start, in the place of the state of the piece before.  One thread per 4 values.
+// start, in the place of the state of the piece before.  One thread per 4
+// values of a sequence, or of a share that a sequence of several pieces begins
+// in (`shared`), whichever are fewer.
 template <int E>
-__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart, Divisor byH)
+__global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart, Divisor byH, bool shared)
 {
     const unsigned g = __builtin_amdgcn_workgroup_id_x();
     const unsigned bh = div_by(g, byPart), part = g - bh * byPart.d;
-    const unsigned b = div_by(bh, byH), h = bh - b * byH.d;
+    const unsigned nr = __builtin_amdgcn_readfirstlane(div_by(bh, byH)), h = bh - nr * byH.d;
+    const int b = shared ? seq_at(A.c.cu, A.c.n, A.len * (nr + 1) - 1) : (int)nr;
     SeqTile q;
-    if (!seq_rows(A.c.cu, A.c.slots, (int)b, A.c.T, A.c.n_slots, q)) return;
+    if (!seq_rows(A.c.cu, A.c.slots, b, A.c.T, A.c.n_slots, q)) return;
     const long long v0 = q.start + PAD * b;
     const size_t first = (size_t)(v0 / A.len), end = (size_t)((v0 + q.len - 1) / A.len);   // the shares it is in
-    if (first == end) return;
+    if (first == end || (shared && first != nr)) return;
     const size_t at = (size_t)part * 256 + __builtin_amdgcn_workitem_id_x(), step = (size_t)A.H * E / 4;
     float4 *ws = reinterpret_cast<float4 *>(A.ws) + (size_t)h * (E / 4) + at;
     const float *lg = A.ws + 2 * (size_t)A.ids * A.H * E + h;
@@ -740,8 +743,9 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
                 hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, true, false, W>),
                                    dim3((ids - 1) * blocks), dim3(G::NT), 0, st, A);
                 constexpr unsigned parts = DK.value * DV.value / 1024;
-                hipLaunchKernelGGL((ssm_join_kernel<DK.value * DV.value>), dim3((unsigned)c.n * d.H * parts), dim3(256),
-                                   0, st, A, make_divisor(parts), make_divisor((unsigned)d.H));
+                const unsigned nr = std::min((unsigned)c.n, ids - 1);
+                hipLaunchKernelGGL((ssm_join_kernel<DK.value * DV.value>), dim3(nr * d.H * parts), dim3(256), 0, st, A,
+                                   make_divisor(parts), make_divisor((unsigned)d.H), nr < (unsigned)c.n);
             }
             if (sh.len && c.n > 1)
                 hipLaunchKernelGGL((ssm_chunk_kernel<DK.value, DV.value, HPW.value, false, true, W>), dim3(ids * blocks),
