@@ -89,9 +89,10 @@ __device__ __forceinline__ floatx16 mma(bf16x8 a, bf16x8 b, floatx16 c)
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ float lane_of(float x, int lane)
+template <class T>
+__device__ __forceinline__ T lane_of(T x, int lane)
 {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), lane));
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
 }
 
 // A row of a chunk times a distance below 2^24 bytes; the masks tell the
@@ -106,22 +107,22 @@ __device__ __forceinline__ float uniform(float x)
 
 // Sum over the lanes behind this one (exclusive), and over all: shifts down
 // within rows of 16 lanes, then the totals of the rows behind.
-__device__ __forceinline__ float suffix64(float x, int lane, float &total)
+template <class T>
+__device__ __forceinline__ T suffix64(T x, int lane, T &total)
 {
 #define GDNQ_DPP(x, ctrl) \
-    __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xf, 0xf, true))
-    float s = GDNQ_DPP(x, 0x101);   // row_shl:1
+    __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), ctrl, 0xf, 0xf, true))
+    T s = GDNQ_DPP(x, 0x101);   // row_shl:1
     s += GDNQ_DPP(s, 0x101);
     s += GDNQ_DPP(s, 0x102);
     s += GDNQ_DPP(s, 0x104);
     s += GDNQ_DPP(s, 0x108);
 #undef GDNQ_DPP
-    const float t = s + x;   // lane 16 r: the total of row r
-    const float t3 = lane_of(t, 48), t2 = lane_of(t, 32) + t3, t1 = lane_of(t, 16) + t2;
+    const T t = s + x;   // lane 16 r: the total of row r
+    const T t3 = lane_of(t, 48), t2 = lane_of(t, 32) + t3, t1 = lane_of(t, 16) + t2;
     total = lane_of(t, 0) + t1;
-    return s + (lane < 32 ? (lane < 16 ? t1 : t2) : (lane < 48 ? t3 : 0.0f));
+    return s + (lane < 32 ? (lane < 16 ? t1 : t2) : (lane < 48 ? t3 : T(0)));
 }
-
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
@@ -215,8 +216,21 @@ struct SsmGeom {
 };
 
 // Per-token vectors of a head in LDS: w, the outputs' row factor, and for the
-// other form cs and delta.
-enum { V_W, V_F, V_CS, V_D, V_N };
+// other form delta, cs, and cs as a whole number of 2^-23, modulo 2^32.
+//
+// Between two tokens that are close, cs_i - cs_j is small while both may be as
+// far as -2^14 (64 tokens that forget everything), where fp32 sums are off by
+// 2^-10.  Whole numbers add exactly: the difference is right as long as it is
+// less than 2^8, off by the rounding of each token's exponent (2^-24) only.
+// The sums in fp32 tell where it is not; there the factor is zero.
+enum { V_W, V_F, V_D, V_CS, V_Q, V_N };
+constexpr float QUANTUM = 1.0f / (1 << 23), GONE = -200.0f;   // 2^-200 is zero in fp32
+
+// 2^(cs_i - cs_j) from the difference in fp32 and the one in whole numbers
+__device__ __forceinline__ float decay_between(float far, uint32_t q)
+{
+    return far < GONE ? 0.0f : __builtin_amdgcn_exp2f(fminf((float)(int)q * QUANTUM, 0.0f));
+}
 
 // 2^RANGE and 2^-RANGE times any usual value, and its second bf16 part, are
 // normal numbers.
@@ -384,8 +398,8 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             float d = low_of(dt) + bias;
             if (A.sp) d = softplus(d);
             d = lane < nv ? fminf(fmaxf(d, A.dt_min), A.dt_max) : 0.0f;
-            // 2^-256 is zero in fp32; the bound keeps the sums behind a token that
-            // forgets everything from losing the digits of its neighbours' decays
+            // 2^-256 is zero in fp32; the bound keeps the sums over tokens that forget
+            // everything from growing without end
             const float la = fmaxf(d * Ah, -256.0f);
             float tot;
             const float suf = suffix64(la, lane, tot);   // cs_63 - cs
@@ -394,9 +408,15 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             Vectors &v = L.v[buf][hw];
             v[V_W][lane] = __builtin_amdgcn_exp2f(mode == FAR ? suf - half : suf) * d;
             if constexpr (!STATE) {
-                v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : (mode == FAR ? half : tot) - suf);
-                v[V_CS][lane] = tot - suf;
+                v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : half - suf);   // of APART: below
                 v[V_D][lane] = d;
+                if (mode == APART) {
+                    uint32_t qtot;
+                    const uint32_t qs = suffix64((uint32_t)(int)rintf(la * (1.0f / QUANTUM)), lane, qtot);
+                    v[V_F][lane] = decay_between(tot - suf, qtot - qs);
+                    v[V_CS][lane] = tot - suf;
+                    v[V_Q][lane] = __uint_as_float(qtot - qs);
+                }
             }
             seglog += tot;
             if (lane == 0) {
@@ -543,9 +563,11 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
 #pragma unroll
                     for (int fr = 0; fr < 6; fr++) {
                         const int ib = fr >= 2, f = ib ? fr - 2 : fr;
+                        __builtin_amdgcn_sched_barrier(0);   // one operand's values at a time: registers
                         const u32x4 gh = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][0][lane * 8]);
                         const u32x4 gl = *reinterpret_cast<const u32x4 *>(&L.g[buf][fr][1][lane * 8]);
                         const float ci = vec[V_CS][32 * ib + c];
+                        const uint32_t qi = __float_as_uint(vec[V_Q][32 * ib + c]);
                         float m[8];
                         uint32_t part[2][4];
 #pragma unroll
@@ -553,8 +575,8 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                             const int j = 16 * f + 8 * (e / 4) + 4 * hh + e % 4;
                             const float gv = (e & 1) ? high_of(gh[e / 2]) + high_of(gl[e / 2])
                                                      : low_of(gh[e / 2]) + low_of(gl[e / 2]);
-                            // above the diagonal gv is zero, and the exponent is kept from overflowing
-                            m[e] = gv * (vec[V_D][j] * __builtin_amdgcn_exp2f(fminf(ci - vec[V_CS][j], 0.0f)));
+                            // above the diagonal gv is zero and the factor at most one
+                            m[e] = gv * (vec[V_D][j] * decay_between(ci - vec[V_CS][j], qi - __float_as_uint(vec[V_Q][j])));
                         }
                         split<2, 8>(m, part);
                         Y[ib] = mma(operand(part[0]), xf[f], Y[ib]);

@@ -1,0 +1,90 @@
+"""The scan's prompts (gdnq_ssm_prefill) head by head: bounds from each head's
+own decays, neighbours in chunks that forget much, states in norm, the
+descriptor's options, magnitudes at the ends of the stated range.  Bounds as
+in test_gpu_layer_ssm.py unless a test derives its own, u = 2^-24."""
+import numpy as np
+import pytest
+
+from tests import _layer as L
+from tests._gpu import lib, say, torch_cuda
+from tests.test_gpu_layer_ssm import _dev, _problem
+
+pytestmark = pytest.mark.gpu
+
+
+def _call(p, lens, H, dk, dv, hk, *, tail=0, cont=None, D=True, bias=True, **desc):
+    """Runs a packed call; y and the states in 64 bits."""
+    torch = torch_cuda()
+    g = lib()
+    n, T = len(lens), sum(lens) + tail
+    d = _dev(p)
+    y = torch.full_like(d["x"], 7.0)
+    de = g.SsmDesc(H=H, dk=dk, dv=dv, hk=hk, **desc)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    nb = g.gdnq_ssm_workspace(de, n, T)
+    ws = torch.full((nb,), 0x7F, dtype=torch.uint8, device="cuda") if nb else None
+    g.gdnq_ssm_prefill(de, d["x"], d["B"], d["C"], d["dt"], d["A"], d["D"] if D else None,
+                       d["dt_bias"] if bias else None, y, d["S"], n, None, None if cont is None else i32(cont),
+                       i32([0] + list(np.cumsum(lens))), n, T, ws)
+    torch.cuda.synchronize()
+    return y.double().cpu().numpy().reshape(T, H, dv), d["S"].double().cpu().numpy()
+
+
+def _ref(p, first, end, S, H, dk, dv, hk, D=True, bias=True, **kw):
+    f = lambda k: p[k][first:end].double().numpy()  # noqa: E731
+    rep = lambda k: np.repeat(f(k).reshape(end - first, hk, dk), H // hk, axis=1)  # noqa: E731
+    return L.ssm_rows(f("x").reshape(end - first, H, dv), rep("B"), rep("C"), f("dt"), p["A"].astype(np.float64),
+                      p["D"].astype(np.float64) if D else None, p["dt_bias"].astype(np.float64) if bias else None,
+                      S.astype(np.float64), **kw)
+
+
+def _check(p, got, gS, lens, cont, H, dk, dv, hk, low=2.0 ** -120, exact_delta=False, **kw):
+    """Every head within the bound of its own decays.  The exponents of a
+    chunk that decays past 2^-160 are exact to 64 u; the running sums of the
+    others reach 111 = 160 log 2 at most."""
+    at = 0
+    for i, m in enumerate(lens):
+        end = at + m
+        if m:
+            ref, S, ym, Sm, delta, v = _ref(p, at, end, p["S"][i] * (cont is not None and cont[i]), H, dk, dv, hk, **kw)
+            c = np.concatenate([np.zeros((1, H)), np.cumsum(np.abs(delta * p["A"]), 0)])
+            K = np.max([c[min(t + 64, m)] - c[t] for t in range(m)], 0)
+            e_d = 2 * L.U if exact_delta else L.delta_bound(v).max(0)
+            tau = e_d * (1 + np.minimum(K, 64)) + (dk + 128 + 16 * np.minimum(K, 111) + 64 + 16 * (m // 32 + 1)) * L.U
+            bad = np.abs(gS[i] - S) > Sm * (tau + 2.0 ** -24)[:, None, None] + low
+            assert not bad.any(), (i, "state", np.unique(np.argwhere(bad)[:, 0]))
+            b = ym * (tau + 3 * 2.0 ** -16 + dk * L.U)[None, :, None] + low
+            bad = np.abs(got[at:end] - ref) > b + (np.abs(ref) + b) * L.ROUND["bf16"]
+            assert not bad.any(), (i, "y", np.unique(np.argwhere(bad)[:, 1]))
+        at = end
+    assert (got[at:] == 7).all()
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128)])
+def test_neighbours_between_tokens_that_forget(dk, dv):
+    """Triples of a token that forgets everything before it (x = 0) and two
+    with x of opposite signs, all B and C positive: the last token's output is
+    C B delta x (e^{delta A} - 1), far below its two terms, so it shows how
+    exact the decay between neighbours is, wherever in a chunk they stand.
+    Steps are given (no softplus), so a term is off by its operands (3 2^-16),
+    the two sums ((dk + 64) u), the exponent (64 u and its roundings: 8 u) and
+    a few roundings (8 u)."""
+    torch = torch_cuda()
+    say("scan neighbours", dk, dv)
+    H, T = 6, 640
+    p = _problem(5, T, H, dk, dv, 1, "bf16", 1)
+    for k in ("B", "C"):
+        p[k] = p[k].abs()
+    x = p["x"].reshape(T, H, dv)
+    x[0::3] = 0
+    x[2::3] = -x[1::3][:len(x[2::3])]
+    dt = torch.full((T, H), 2.0 ** -9)
+    dt[0::3] = torch.tensor([1.0, 5.0, 20.0, 77.0, 120.0, 200.0])
+    p["dt"] = dt.bfloat16()
+    p["A"] = -np.array([11.0, 15.0, 3.0, 2.0, 1.7, 1.1], np.float32)
+    got, gS = _call(p, [T], H, dk, dv, 1, D=False, bias=False, cont=[1], flags=0)
+    ref, S, ym, Sm, _, _ = _ref(p, 0, T, p["S"][0], H, dk, dv, 1, D=False, bias=False, sp=False)
+    b = ym * (3 * 2.0 ** -16 + (dk + 144) * L.U)
+    bad = np.abs(got - ref) > b + (np.abs(ref) + b) * L.ROUND["bf16"] + 2.0 ** -120
+    assert not bad.any(), (bad.sum(), (np.abs(got - ref) / np.maximum(ym, 1e-30)).max())
+    assert not (np.abs(gS[0] - S) > Sm * ((dk + 144) * L.U) + 2.0 ** -120).any()
