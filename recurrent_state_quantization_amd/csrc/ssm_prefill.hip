@@ -14,9 +14,9 @@
 // forms it once, and w X serves both lines.  With exponents in base 2 and
 // cs_63 > -RANGE every factor is in range; cs_63 - cs_j is summed over the
 // tokens behind j, which keeps it exact where it is small.  A head whose
-// chunk decays further, to -2 RANGE, counts the exponents from cs_63 / 2
-// instead of cs_63 and decays S by 2^{cs_63 / 2} before and after; beyond
-// that its outputs are formed from factors that are all at most one:
+// chunk decays further, to -2 RANGE, counts the exponents from a whole number
+// h near cs_63 / 2 instead of 0 and decays S by 2^{cs_63 - h} before and by
+// 2^h after, both as exact as without; beyond that its outputs are formed from factors that are all at most one:
 //   Y = (tril(C B^T) . e^{cs_i - cs_j} delta_j) X + diag(e^{cs_i}) C S + D X.
 //
 // Precision: the products run on the bf16 matrix instructions with fp32
@@ -248,7 +248,7 @@ struct SsmLds {
     alignas(16) __bf16 g[STATE ? 1 : 2][STATE ? 1 : 6][2][STATE ? 8 : 64 * 8];
     static constexpr int VN = STATE ? 1 : V_N;
     alignas(16) float v[2][HEADS][VN][CH];
-    float tot[2][HEADS];   // the decay of S before the chunk's products (of FAR: also behind them)
+    float tot[2][HEADS], after[2][HEADS];   // the decay of S before the chunk's products, and (of FAR) behind them
     int mode[2][HEADS];
 };
 
@@ -404,11 +404,14 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             float tot;
             const float suf = suffix64(la, lane, tot);   // cs_63 - cs
             const int mode = STATE || tot > -RANGE ? NEAR : tot > -2.0f * RANGE ? FAR : APART;
-            const float half = 0.5f * tot;
+            // a whole number, taken out of the exponents' own whole part: suf - h in
+            // fp32 would lose the digits of a small suf (2^-19, 13 times fp32's rounding)
+            const int h = mode == FAR ? (int)rintf(0.5f * tot) : 0;
+            const float whole = rintf(suf), part = suf - whole;
             Vectors &v = L.v[buf][hw];
-            v[V_W][lane] = __builtin_amdgcn_exp2f(mode == FAR ? suf - half : suf) * d;
+            v[V_W][lane] = ldexpf(__builtin_amdgcn_exp2f(part) * d, (int)whole - h);
             if constexpr (!STATE) {
-                v[V_F][lane] = __builtin_amdgcn_exp2f(mode == NEAR ? -suf : half - suf);   // of APART: below
+                v[V_F][lane] = ldexpf(__builtin_amdgcn_exp2f(-part), h - (int)whole);   // of APART: below
                 v[V_D][lane] = d;
                 if (mode == APART) {
                     uint32_t qtot;
@@ -420,7 +423,8 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             }
             seglog += tot;
             if (lane == 0) {
-                L.tot[buf][hw] = __builtin_amdgcn_exp2f(mode == FAR ? half : tot);
+                L.tot[buf][hw] = __builtin_amdgcn_exp2f(tot - (float)h);
+                if constexpr (!STATE) L.after[buf][hw] = ldexpf(1.0f, h);
                 L.mode[buf][hw] = mode;
             }
         };
@@ -497,7 +501,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
 
             const int tr_r = 4 * hh + l16 / 4, tr_c = 16 * (c / 16) + 4 * (l16 & 3);
             const Vectors &vec = L.v[buf][hw];
-            const float tot = uniform(L.tot[buf][hw]);
+            const float tot = uniform(L.tot[buf][hw]), after = STATE ? 1.0f : uniform(L.after[buf][hw]);
             const int mode = STATE ? NEAR : __builtin_amdgcn_readfirstlane(L.mode[buf][hw]);
             const bool apart = mode == APART;
             bf16x8 xf[4];   // x rows 16 f .. + 15, the wave's columns
@@ -505,11 +509,11 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
             for (int f = 0; f < 4; f++)
                 xf[f] = ld_cols(&xt[(16 * f + tr_r) * G::SX + tr_c], G::SX);
 
-            const auto decay_state = [&] {
+            const auto decay_state = [&](float by) {
 #pragma unroll
                 for (int nb = 0; nb < G::NBLK; nb++)
 #pragma unroll
-                    for (int r = 0; r < 16; r++) S[nb][r] *= tot;
+                    for (int r = 0; r < 16; r++) S[nb][r] *= by;
             };
             floatx16 Y[2];
             const auto scale_rows = [&] {   // Y rows by V_F
@@ -540,7 +544,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                         *reinterpret_cast<uint32_t *>(&xt[i * G::SX + (c & ~1)]) = __builtin_amdgcn_perm(o, u, sel);
                     }
             };
-            if (!apart) decay_state();
+            if (!apart) decay_state(tot);
             if constexpr (!STATE) {
 #pragma unroll
                 for (int r = 0; r < 16; r++) Y[0][r] = Y[1][r] = 0.0f;
@@ -583,7 +587,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                         Y[ib] = mma(operand(part[1]), xf[f], Y[ib]);
                     }
                     output();
-                    decay_state();
+                    decay_state(tot);
                 }
             }
             floatx4 tri = {};
@@ -634,7 +638,7 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
                 put_triangle(buf ^ 1, n0, tri);
                 for (int n = n0 + G::NW; n < 10; n += G::NW) put_triangle(buf ^ 1, n, triangle(buf ^ 1, n));
             }
-            if (mode == FAR) decay_state();
+            if (mode == FAR) decay_state(after);
             if constexpr (!STATE)
                 if (!apart) {
                     scale_rows();

@@ -88,3 +88,33 @@ def test_neighbours_between_tokens_that_forget(dk, dv):
     bad = np.abs(got - ref) > b + (np.abs(ref) + b) * L.ROUND["bf16"] + 2.0 ** -120
     assert not bad.any(), (bad.sum(), (np.abs(got - ref) / np.maximum(ym, 1e-30)).max())
     assert not (np.abs(gS[0] - S) > Sm * ((dk + 144) * L.U) + 2.0 ** -120).any()
+
+
+@pytest.mark.parametrize("T", [64, 100, 640])
+def test_states_in_norm(T):
+    """||S - ref|| / ||ref|| per head.  Steps are given and every value is
+    random, so errors add in quadrature: a weight (2 u), its product with x
+    and its three parts (u each) and 12 additions a chunk, each half an ulp of
+    the sum so far, stay below 8 u up to two chunks; ten chunks, with the
+    roundings of their decays on one side, below 16 u.  (w x in two bf16 parts
+    is off by 28 u, an exponent rounded at 2^6 by 13 u.)  In each chunk one
+    token, with x = 0, decays by the head's bits, on every side of the
+    kernel's borders."""
+    torch = torch_cuda()
+    say("scan states in norm", T)
+    bits = np.array([0, 20, 79, 82, 110, 157, 163, 400], np.float64)
+    H, dk, dv = len(bits), 128, 64
+    p = _problem(T, T, H, dk, dv, 1, "bf16", 1)
+    r = np.random.default_rng(T)
+    dt = r.uniform(1e-3, 2e-2, (T, H)).astype(np.float32)
+    p["A"] = np.full(H, -1.0, np.float32)
+    p["A"][0] = 0.0
+    x = p["x"].reshape(T, H, dv)
+    for t in range(9, T, 64):
+        dt[t] = np.maximum(bits * np.log(2.0), 1.0)
+        x[t] = 0
+    p["dt"] = torch.from_numpy(dt).bfloat16()
+    _, gS = _call(p, [T], H, dk, dv, 1, D=False, bias=False, cont=[1], flags=0)
+    _, S, _, _, _, _ = _ref(p, 0, T, p["S"][0], H, dk, dv, 1, D=False, bias=False, sp=False)
+    off = np.sqrt(((gS[0] - S) ** 2).sum((1, 2)) / (S ** 2).sum((1, 2))) / L.U
+    assert off.max() < (8 if T <= 128 else 16), off
