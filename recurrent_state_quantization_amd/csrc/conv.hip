@@ -22,7 +22,7 @@ struct ConvArgs {
 };
 
 // act(bias + taps), one fused multiply-add per tap
-template <int V, int W, bool SILU>
+template <bool BF16, int V, int W, bool SILU>
 __device__ __forceinline__ void conv_taps(const float (&win)[W][V], const float (&w)[W][V], const float (&b)[V],
                                           float (&y)[V])
 {
@@ -31,7 +31,7 @@ __device__ __forceinline__ void conv_taps(const float (&win)[W][V], const float 
         float a = b[v];
 #pragma unroll
         for (int k = 0; k < W; k++) a = fmaf(w[k][v], win[k][v], a);
-        y[v] = SILU ? a * sigmoid(a) : a;
+        y[v] = SILU ? a * sigmoid<!BF16>(a) : a;
     }
 }
 
@@ -101,7 +101,7 @@ __global__ __launch_bounds__(256) void conv_prefill_kernel(ConvArgs A)
     const auto emit = [&](const typename P::raw &in) {
         float y[V];
         P::widen(in, win[W - 1]);
-        conv_taps<V, W, SILU>(win, w, b, y);
+        conv_taps<BF16, V, W, SILU>(win, w, b, y);
         store_vec<BF16, V>(yp, 0, y);
         yp += dy;
 #pragma unroll
@@ -166,7 +166,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs A)
     const size_t hist = (size_t)slot * (W - 1) * A.C + c0;
 #pragma unroll
     for (int j = 0; j < W - 1; j++) load_vec<BF16, V>(A.c.state, hist + (size_t)j * A.C, win[j]);
-    conv_taps<V, W, SILU>(win, w, b, y);
+    conv_taps<BF16, V, W, SILU>(win, w, b, y);
     store_vec<BF16, V>(A.c.y, (size_t)i * A.c.ldy + c0, y);
 #pragma unroll
     for (int j = 0; j < W - 1; j++) store_vec<BF16, V>(A.c.state, hist + (size_t)j * A.C, win[j + 1]);

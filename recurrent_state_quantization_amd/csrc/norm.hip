@@ -81,7 +81,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_gated_kernel(NormArg
 #pragma unroll
             for (int v = 0; v < V; v++) {
                 if (A.c.z) {
-                    const float s = sigmoid(g[k][v]);
+                    const float s = sigmoid<!BF16>(g[k][v]);
                     g[k][v] = (A.flags & GDNQ_NORM_GATE_SIGMOID) ? s : g[k][v] * s;
                 } else
                     g[k][v] = 1.0f;

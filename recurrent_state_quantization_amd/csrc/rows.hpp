@@ -93,10 +93,23 @@ __device__ __forceinline__ void load_weights(const float *p, float (&out)[V])
 }
 
 // 1 / (1 + e^-x) from the hardware exp2 and reciprocal (one ulp each; e^-x
-// overflows to infinity below x = -88, whose reciprocal is the limit, 0).
+// overflows to infinity below x = -88, whose reciprocal is the limit, 0).  The
+// exponent is rounded once, so the result is off by about 2 |x| 2^-24 of
+// itself: 2^-16.5 at the far end, which disappears in a bf16 output.
+// EXACT, for fp32 outputs: from e^-|x|, whose exponent's rounding is applied
+// to first order, a few 2^-24 everywhere: seven operations more, hidden behind
+// HBM at fp32's four values per 16 bytes (16384 x 4096 gated 140 us with and
+// without).
+template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float x)
 {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+    if constexpr (!EXACT) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+    const float y = fmaxf(-fabsf(x), -256.0f), t = y * 1.44269502f;
+    const float r = fmaf(y, 1.44269502f, -t) + y * 1.92596303e-8f;
+    float e = __builtin_amdgcn_exp2f(t);
+    e = fmaf(e, r * 0.693147182f, e);
+    const float q = __builtin_amdgcn_rcpf(1.0f + e);
+    return x < 0.0f ? e * q : q;
 }
 
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1.  The exponent of e
