@@ -115,10 +115,12 @@ __device__ __forceinline__ float sigmoid(float x)
 // log(1 + e^x) = max(x, 0) + log(1 + e), e = e^-|x| <= 1.  The exponent of e
 // is rounded once and the rest of the product applied to first order; then
 // log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by its series to s^15 (the
-// next term is below 2^-28 of the sum).  Relative error a few 2^-24.
+// next term is below 2^-28 of the sum).  Relative error a few 2^-24.  e is
+// zero in fp32 long before |x| = 256; the bound keeps t and r finite at the
+// type's ends.
 __device__ __forceinline__ float softplus(float x)
 {
-    const float y = -fabsf(x), t = y * 1.44269502f;
+    const float y = fmaxf(-fabsf(x), -256.0f), t = y * 1.44269502f;
     const float r = fmaf(y, 1.44269502f, -t) + y * 1.92596303e-8f;
     float e = __builtin_amdgcn_exp2f(t);
     e = fmaf(e, r * 0.693147182f, e);

@@ -97,7 +97,7 @@ def test_states_in_norm(T):
     and its three parts (u each) and 12 additions a chunk, each half an ulp of
     the sum so far, stay below 8 u up to two chunks; ten chunks, with the
     roundings of their decays on one side, below 16 u.  (w x in two bf16 parts
-    is off by 28 u, an exponent rounded at 2^6 by 13 u.)  In each chunk one
+    is off by 28 u or more, an exponent rounded at 2^6 by 13 u.)  In each chunk one
     token, with x = 0, decays by the head's bits, on every side of the
     kernel's borders."""
     torch = torch_cuda()
@@ -118,3 +118,46 @@ def test_states_in_norm(T):
     _, S, _, _, _, _ = _ref(p, 0, T, p["S"][0], H, dk, dv, 1, D=False, bias=False, sp=False)
     off = np.sqrt(((gS[0] - S) ** 2).sum((1, 2)) / (S ** 2).sum((1, 2))) / L.U
     assert off.max() < (8 if T <= 128 else 16), off
+
+
+@pytest.mark.parametrize("lens", [[130], [500, 60]])
+def test_steps_of_the_largest_and_lowest_value(lens):
+    """dt at the ends of its type: a step of dt_max, or of dt_min (a token
+    that leaves the state as it was, where that is 0)."""
+    torch = torch_cuda()
+    say("scan dt ends", lens)
+    H, dk, dv, T = 2, 64, 64, sum(lens)
+    p = _problem(T, T, H, dk, dv, 1, "bf16", len(lens))
+    top = torch.finfo(torch.bfloat16).max
+    p["dt"][3::7] = top
+    p["dt"][5::7] = -top
+    p["dt_bias"] = np.zeros(H, np.float32)
+    kw = dict(lo=0.0, hi=0.25)
+    got, gS = _call(p, lens, H, dk, dv, 1, cont=[1] * len(lens), dt_min=0.0, dt_max=0.25)
+    q = dict(p, dt=p["dt"].float().clamp(-100, 40))   # the same steps: softplus is 0 and above dt_max beyond
+    _check(q, got, gS, lens, [1] * len(lens), H, dk, dv, 1, **kw)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_tokens_with_steps_of_the_largest_and_lowest_value(io):
+    torch = torch_cuda()
+    g = lib()
+    say("scan token dt ends", io)
+    H, dk, dv, n = 2, 64, 64, 4
+    p = _problem(n, n, H, dk, dv, 1, io, n)
+    top = torch.finfo(p["dt"].dtype).max
+    p["dt"][1], p["dt"][2] = top, -top
+    p["dt_bias"] = np.zeros(H, np.float32)
+    d = _dev(p)
+    y = torch.empty_like(d["x"])
+    g.gdnq_ssm_step(g.SsmDesc(H=H, dk=dk, dv=dv, hk=1, io_dtype=g.IO_BF16 if io == "bf16" else g.IO_F32, dt_max=0.25),
+                    d["x"], d["B"], d["C"], d["dt"], d["A"], d["D"], d["dt_bias"], y, d["S"], n, None, n)
+    torch.cuda.synchronize()
+    q = dict(p, dt=p["dt"].float().clamp(-100, 40))
+    for i in range(n):
+        ref, S, ym, Sm, delta, v = _ref(q, i, i + 1, p["S"][i], H, dk, dv, 1, lo=0.0, hi=0.25)
+        e = L.delta_bound(v[0]) * (1 + np.abs(delta[0] * p["A"])) + 8 * L.U
+        assert not (np.abs(d["S"][i].double().cpu().numpy() - S) > Sm * e[:, None, None] + 2.0 ** -120).any()
+        b = ym[0] * (e + (dk + 8) * L.U)[:, None]
+        got = y[i].double().cpu().numpy().reshape(H, dv)
+        assert not (np.abs(got - ref[0]) > b + (np.abs(ref[0]) + b) * L.ROUND[io] + 2.0 ** -120).any()
