@@ -42,10 +42,15 @@ __device__ __forceinline__ float group_sum(float x, float (*part)[16], int slot)
     return x;
 }
 
-// 1 / sqrt(mean square + eps); eps > 0 keeps the argument normal
+// 1 / sqrt(mean square + eps).  The instruction takes normal arguments only;
+// a smaller one (eps below 2^-126 and a row as small) goes through it 2^48
+// times as large.
 __device__ __forceinline__ float inv_rms(float ss, const NormArgs &A)
 {
-    return __builtin_amdgcn_rsqf(fmaf(ss, A.inv_n, A.eps));
+    const float m = fmaf(ss, A.inv_n, A.eps);
+    const bool small = m < 0x1p-126f;
+    const float r = __builtin_amdgcn_rsqf(small ? m * 0x1p48f : m);
+    return small ? r * 0x1p24f : r;
 }
 
 template <bool BF16, int V, int NT, int K>

@@ -79,3 +79,39 @@ def test_norm_gate_in_fp32(first, sig):
     rel = 12 * L.U + (2 * (GATE + L.U) if first else GATE)
     bad = ~(np.abs(got - ref) <= np.abs(ref) * rel + 2.0 ** -120)
     assert not bad.any(), (bad.sum(), (np.abs(got - ref)[bad] / np.abs(ref[bad])).max() / L.U)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("eps", [1e-40, 1e-38, 2e-45])
+def test_smallest_eps(io, eps):
+    """eps below fp32's normal numbers: rows of zeros give zeros, rows whose
+    mean square is as small their own root.  Such an argument is a multiple of
+    2^-149 and off by at most 4 of them (the mean's product and its sum with
+    eps, half each, and 16 squares or sums of their own)."""
+    torch = torch_cuda()
+    g = lib()
+    say("smallest eps", io, eps)
+    D = 64
+    r = np.random.default_rng(2)
+    x = r.standard_normal((5, D)).astype(np.float32)
+    x[0], x[1], x[2], x[3] = 0, x[1] * 2.0 ** -63, x[2] * 2.0 ** -66, x[3] * 2.0 ** -100
+    x = torch.from_numpy(x).to(torch.bfloat16 if io == "bf16" else torch.float32)
+    w = torch.ones(D, device="cuda")
+    d = g.NormDesc(D=D, io_dtype=g.IO_BF16 if io == "bf16" else g.IO_F32, eps=eps)
+    eps = float(np.float32(eps))
+    y, y2, ro = (torch.full((5, D), 7.0, dtype=x.dtype, device="cuda") for _ in range(3))
+    g.gdnq_norm_gated(d, x.cuda(), None, w, y, 5)
+    g.gdnq_norm_residual(d, x.cuda(), w, 1.0, torch.zeros_like(x).cuda(), ro, w, y2, 5)
+    torch.cuda.synchronize()
+    u = x.double().numpy()
+    arg = (u * u).mean(-1, keepdims=True) + eps
+    tiny = 80 * 2.0 ** -149   # 64 squares of half a 2^-149 each, twice over
+    ref = u / np.sqrt(arg)
+    off = 0.5 * (2.0 * tiny / D + 2.0 ** -148) / arg
+    got = y.double().cpu().numpy()
+    assert np.isfinite(got).all() and np.isfinite(y2.double().cpu().numpy()).all()
+    assert (got[0] == 0).all() and (y2[0] == 0).all()
+    ok = off[:, 0] < 0.25   # beyond, the argument has no digits: eps = 2^-149 alone is one unit (row 0: zeros, above)
+    assert ok[4]
+    bad = np.abs(got - ref)[ok] > (np.abs(ref) * (40 * L.U + 2 * off + L.ROUND[io]))[ok]
+    assert not bad.any(), np.abs(got / np.where(ref == 0, 1, ref) - 1).max(1)
