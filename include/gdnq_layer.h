@@ -119,7 +119,9 @@ typedef struct {
 
 /*
  * Bytes of device workspace that gdnq_ssm_prefill needs for this descriptor,
- * number of sequences and number of token rows (0: none).
+ * number of sequences and number of token rows (0: none).  Never less for more
+ * sequences or more rows: the workspace of a program's largest call serves the
+ * others.
  */
 int gdnq_ssm_workspace(const gdnq_ssm_desc *desc, int32_t n_seqs, int32_t T, size_t *bytes_out);
 

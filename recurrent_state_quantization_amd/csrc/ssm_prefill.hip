@@ -708,11 +708,33 @@ struct Shares {
     unsigned ids;
 };
 
+// f(n) for the numbers of shares that a call may be dealt out in, growing: an
+// eighth to six rounds of one workgroup per compute unit, more than one round
+// only where that fills the last one better by a hundredth (by the estimate
+// below a call loses 1.5% to this at most, and 1 in 100 loses any; the
+// workspace is up to 6 times smaller for it).
+template <class F>
+void share_counts(double blocks, F &&f)
+{
+    double fill = 0.0;
+    for (const double r : {0.125, 0.25, 0.5, 1.0, 2.0, 3.0, 4.0, 6.0}) {
+        const long long n = (long long)(r * 256.0 / blocks);
+        if (n < 2) continue;
+        if (r >= 1.0) {
+            const double x = (double)n * blocks / (r * 256.0);
+            if (x <= 1.01 * fill) continue;
+            fill = x;
+        }
+        f(n);
+    }
+}
+
+long long places_of(int n, int T) { return T + PAD * (n - 1); }
+
 // How a call is dealt out.  Up to 384 tokens a share is a whole sequence: the
 // two other kernels cost more than they save (300 tokens of 64 heads of
-// 128 x 64: 32 us; 39 when cut at 128).  Above, equal shares of the places for
-// about one to six rounds of one workgroup per compute unit, or for an eighth
-// to half of one, or one share for all, whichever has the least estimated time: 6.0 us
+// 128 x 64: 32 us; 39 when cut at 128).  Above, equal shares of the places,
+// one or as many as share_counts() says, whichever has the least estimated time: 6.0 us
 // a chunk and half as much again to begin in the main kernel, 3.4 us a chunk
 // and one more in the states' kernel, and the joined states at 5 TB/s (dk =
 // 128; with dk = 64 all three are about half).  Measured in us for half a
@@ -724,12 +746,10 @@ Shares shares(const gdnq_ssm_desc &d, int n, int T)
 {
     if (T <= 384) return {0, (unsigned)n};
     const double blocks = d.H / heads_per_group(d), join = (double)d.H * 128 * d.dv * 8 / 5e6;
-    const long long places = T + PAD * (n - 1);
+    const long long places = places_of(n, T);
     Shares best{places, 1};
     double least = std::ceil(blocks / 256.0) * ((double)places / CH + 1.5) * 6.0;
-    for (const double r : {0.125, 0.25, 0.5, 1.0, 2.0, 3.0, 4.0, 6.0}) {
-        const long long want = (long long)(r * 256.0 / blocks);
-        if (want < 2) continue;
+    share_counts(blocks, [&](long long want) {
         const long long len = std::max(((places + want - 1) / want + CH - 1) / CH * CH, 2ll * CH);
         const double ids = (double)((places + len - 1) / len), chunks = (double)len / CH;
         const double us = std::ceil(ids * blocks / 256.0) * (chunks + 1.5) * 6.0 +
@@ -738,17 +758,21 @@ Shares shares(const gdnq_ssm_desc &d, int n, int T)
             best = {len, (unsigned)ids};
             least = us;
         }
-    }
+    });
     return best;
 }
 
 }  // namespace
 
+// Room for the most shares of any call with as many sequences and rows or
+// fewer (a share has 2 CH places at least), not for this call's own number,
+// which is the least of an estimate and may be larger for a shorter call.
 size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T)
 {
-    const unsigned ids = shares(d, n, T).ids;
-    if (T <= 384 || ids == 1) return 0;
-    return (size_t)ids * (size_t)d.H * (2 * (size_t)d.dk * d.dv + 1) * 4;
+    long long most = 0;
+    if (T > 384) share_counts((double)(d.H / heads_per_group(d)), [&](long long want) { most = want; });
+    most = std::min(most, (places_of(n, T) + 2 * CH - 1) / (2 * CH));
+    return (size_t)most * (size_t)d.H * (2 * (size_t)d.dk * d.dv + 1) * 4;
 }
 
 hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStream_t st)
