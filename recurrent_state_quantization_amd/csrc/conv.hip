@@ -19,6 +19,7 @@ struct ConvArgs {
     int C;
     unsigned waves;   // channel blocks times tiles (prompts) or entries (single tokens)
     Divisor byCb;     // channel blocks per row
+    unsigned nx;      // width of the grid
 };
 
 // act(bias + taps), one fused multiply-add per tap
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(256) void conv_prefill_kernel(ConvArgs A)
     using P = Pack<BF16, V>;
     constexpr int TT = 1 << SH, U = 8;
     const int lane = (int)(__builtin_amdgcn_workitem_id_x() & 63u);
-    const unsigned wave = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_workgroup_id_x() * 4u +
+    const unsigned wave = __builtin_amdgcn_readfirstlane(block_id(A.nx) * 4u +
                                                          (__builtin_amdgcn_workitem_id_x() >> 6));
     if (wave >= A.waves) return;
     const unsigned id = div_by(wave, A.byCb);
@@ -152,7 +153,7 @@ template <bool BF16, int V, int W, bool SILU>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs A)
 {
     const int lane = (int)(__builtin_amdgcn_workitem_id_x() & 63u);
-    const unsigned wave = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_workgroup_id_x() * 4u +
+    const unsigned wave = __builtin_amdgcn_readfirstlane(block_id(A.nx) * 4u +
                                                          (__builtin_amdgcn_workitem_id_x() >> 6));
     if (wave >= A.waves) return;
     const unsigned i = div_by(wave, A.byCb);
@@ -200,9 +201,10 @@ hipError_t launch_conv_prefill(const gdnq_conv_desc &d, const ConvCall &c, hipSt
         constexpr int SH = 4;   // 32 and 8 tokens a tile: 201 and 197 us for 32768 x 8192 bf16, 16: 190
         const unsigned ncb = (unsigned)((d.C + 64 * V.value - 1) / (64 * V.value));
         const unsigned waves = ncb * ((unsigned)(c.T >> SH) + (unsigned)c.n);
-        const ConvArgs A{c, d.C, waves, make_divisor(ncb)};
+        const dim3 grid = grid_of((waves + 3) / 4, 256);
+        const ConvArgs A{c, d.C, waves, make_divisor(ncb), grid.x};
         hipLaunchKernelGGL((conv_prefill_kernel<decltype(BF)::value, V.value, W.value, decltype(SILU)::value, SH>),
-                           dim3((waves + 3) / 4), dim3(256), 0, st, A);
+                           grid, dim3(256), 0, st, A);
         return hipGetLastError();
     });
 }
@@ -212,9 +214,10 @@ hipError_t launch_conv_step(const gdnq_conv_desc &d, const ConvCall &c, hipStrea
     return conv_dispatch(d, c, [&](auto BF, auto V, auto W, auto SILU) {
         const unsigned ncb = (unsigned)((d.C + 64 * V.value - 1) / (64 * V.value));
         const unsigned waves = ncb * (unsigned)c.n;
-        const ConvArgs A{c, d.C, waves, make_divisor(ncb)};
+        const dim3 grid = grid_of((waves + 3) / 4, 256);
+        const ConvArgs A{c, d.C, waves, make_divisor(ncb), grid.x};
         hipLaunchKernelGGL((conv_step_kernel<decltype(BF)::value, V.value, W.value, decltype(SILU)::value>),
-                           dim3((waves + 3) / 4), dim3(256), 0, st, A);
+                           grid, dim3(256), 0, st, A);
         return hipGetLastError();
     });
 }

@@ -258,6 +258,8 @@ int gdnq_ssm_prefill(const gdnq_ssm_desc *desc, const gdnq_ssm_io *io, float *S,
         return fail(GDNQ_EINVAL, "workspace of %zu bytes is too small (%zu are needed)", workspace_bytes, need);
     if (need) TRY(flat(sp, workspace, need, "workspace", WRITE));
     TRY(check_grid(((unsigned long long)T / 128 + n_seqs + 8) * desc->H * 16, "T*H"));
+    if (T <= gdnq::SSM_WHOLE)   // 2 dv threads for every sequence and head, in one dimension of a grid
+        TRY(check_grid((unsigned long long)n_seqs * desc->H * desc->dv, "n_seqs*H"));
     return launched(gdnq::launch_ssm_prefill(*desc, c, stream_of(stream)));
 }
 

@@ -19,6 +19,9 @@ struct ConvCall {
     int n_slots, n, T;
 };
 
+// Calls of this many token rows or fewer leave every sequence of the scan whole.
+constexpr int SSM_WHOLE = 384;
+
 struct SsmCall {
     gdnq_ssm_io io;   // row distances filled in
     float *S;
@@ -43,6 +46,15 @@ size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T);
 hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStream_t st);
 hipError_t launch_norm_gated(const gdnq_norm_desc &d, const NormCall &c, hipStream_t st);
 hipError_t launch_norm_residual(const gdnq_norm_desc &d, const NormCall &c, hipStream_t st);
+
+// The grid of `blocks` workgroups or a few more.  One dimension holds fewer than
+// 2^32 threads, which narrow rows and small groups pass at a few GB: such calls
+// take two, whose workgroups block_id() numbers through.
+inline dim3 grid_of(unsigned long long blocks, unsigned threads)
+{
+    const unsigned long long most = 0xFFFFFFFFull / threads, ny = (blocks + most - 1) / most;
+    return dim3((unsigned)((blocks + ny - 1) / ny), (unsigned)ny);
+}
 
 // Whether rows at p, ld elements of `es` bytes apart, can be read in 16-byte
 // pieces.

@@ -23,6 +23,7 @@ struct NormArgs {
     Divisor byGroups;  // groups per row
     uint32_t flags;
     float eps, w_offset, inv_n;
+    unsigned nx;       // width of the grid
 };
 
 // Sum over a group's NT threads, in each of them.  `slot` numbers the sums
@@ -60,7 +61,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_gated_kernel(NormArg
     using P = Pack<BF16, V>;
     __shared__ float part[1][16];
     const int t = (int)__builtin_amdgcn_workitem_id_x();
-    const unsigned gi = __builtin_amdgcn_workgroup_id_x() * (WG / NT) + (unsigned)t / NT;
+    const unsigned gi = block_id(A.nx) * (WG / NT) + (unsigned)t / NT;
     if (gi >= A.groups) return;   // whole groups of lanes; a group of several waves has its workgroup to itself
     const unsigned row = div_by(gi, A.byGroups);
     const int c0 = (int)(gi - row * A.byGroups.d) * A.group, l = t % NT;
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void norm_residual_kernel(Norm
     constexpr int WG = NT < 256 ? 256 : NT;
     __shared__ float part[2][16];
     const int t = (int)__builtin_amdgcn_workitem_id_x();
-    const unsigned row = __builtin_amdgcn_workgroup_id_x() * (WG / NT) + (unsigned)t / NT;
+    const unsigned row = block_id(A.nx) * (WG / NT) + (unsigned)t / NT;
     if (row >= A.groups) return;
     const int l = t % NT;
     float p[K][V], r[K][V];
@@ -224,14 +225,14 @@ NormArgs norm_args(const gdnq_norm_desc &d, const NormCall &c)
     const int group = d.group ? d.group : d.D;
     const unsigned per = (unsigned)(d.D / group);
     return NormArgs{c, d.D, group, (unsigned)c.rows * per, make_divisor(per), d.flags, d.eps, d.w_offset,
-                    1.0f / (float)group};
+                    1.0f / (float)group, 0};
 }
 
 }  // namespace
 
 hipError_t launch_norm_gated(const gdnq_norm_desc &d, const NormCall &c, hipStream_t st)
 {
-    const NormArgs A = norm_args(d, c);
+    NormArgs A = norm_args(d, c);
     const bool bf = d.io_dtype == GDNQ_IO_BF16;
     const int es = bf ? 2 : 4;
     const bool wide = A.group % (16 / es) == 0 && wide_rows(c.x, c.ldx, es) && wide_rows(c.y, c.ldy, es) &&
@@ -241,8 +242,10 @@ hipError_t launch_norm_gated(const gdnq_norm_desc &d, const NormCall &c, hipStre
             constexpr int V = decltype(WIDE)::value ? (decltype(BF)::value ? 8 : 4) : 1;
             return norm_dispatch<V>(A.group, [&](auto NT, auto K) {
                 constexpr int WG = NT.value < 256 ? 256 : NT.value, per = WG / NT.value;
+                const dim3 grid = grid_of((A.groups + per - 1) / per, WG);
+                A.nx = grid.x;
                 hipLaunchKernelGGL((norm_gated_kernel<decltype(BF)::value, V, NT.value, K.value>),
-                                   dim3((A.groups + per - 1) / per), dim3(WG), 0, st, A);
+                                   grid, dim3(WG), 0, st, A);
                 return hipGetLastError();
             });
         });
@@ -251,7 +254,7 @@ hipError_t launch_norm_gated(const gdnq_norm_desc &d, const NormCall &c, hipStre
 
 hipError_t launch_norm_residual(const gdnq_norm_desc &d, const NormCall &c, hipStream_t st)
 {
-    const NormArgs A = norm_args(d, c);
+    NormArgs A = norm_args(d, c);
     const bool bf = d.io_dtype == GDNQ_IO_BF16, r32 = bf && (d.flags & GDNQ_NORM_RES_F32);
     const int es = bf ? 2 : 4, rs = r32 ? 4 : es;
     const bool wide = d.D % (16 / es) == 0 && wide_rows(c.x, c.ldx, es) && wide_rows(c.res, c.ldr, rs) &&
@@ -260,8 +263,10 @@ hipError_t launch_norm_residual(const gdnq_norm_desc &d, const NormCall &c, hipS
         constexpr int V = decltype(WIDE)::value ? (decltype(BF)::value ? 8 : 4) : 1;
         return norm_dispatch<V>(d.D, [&](auto NT, auto K) {
             constexpr int WG = NT.value < 256 ? 256 : NT.value, per = WG / NT.value;
+            const dim3 grid = grid_of((A.groups + per - 1) / per, WG);
+            A.nx = grid.x;
             hipLaunchKernelGGL((norm_residual_kernel<decltype(BF)::value, decltype(R32)::value, V, NT.value, K.value>),
-                               dim3((A.groups + per - 1) / per), dim3(WG), 0, st, A);
+                               grid, dim3(WG), 0, st, A);
             return hipGetLastError();
         });
     };

@@ -11,6 +11,13 @@
 
 namespace gdnq {
 
+// The workgroup's number in a grid of grid_of() that is nx wide (an argument of
+// the kernel's own, read with the others).
+__device__ __forceinline__ unsigned block_id(unsigned nx)
+{
+    return __builtin_amdgcn_workgroup_id_y() * nx + __builtin_amdgcn_workgroup_id_x();
+}
+
 // V consecutive io-dtype values, as one access of V elements (V = 1, or the
 // 16 bytes of 8 bf16 / 4 fp32 values).
 template <bool BF16, int V>

@@ -731,7 +731,7 @@ void share_counts(double blocks, F &&f)
 
 long long places_of(int n, int T) { return T + PAD * (n - 1); }
 
-// How a call is dealt out.  Up to 384 tokens a share is a whole sequence: the
+// How a call is dealt out.  Up to SSM_WHOLE tokens a share is a whole sequence: the
 // two other kernels cost more than they save (300 tokens of 64 heads of
 // 128 x 64: 32 us; 39 when cut at 128).  Above, equal shares of the places,
 // one or as many as share_counts() says, whichever has the least estimated time: 6.0 us
@@ -744,7 +744,7 @@ long long places_of(int n, int T) { return T + PAD * (n - 1); }
 // heads 79, 63, 78, 79.
 Shares shares(const gdnq_ssm_desc &d, int n, int T)
 {
-    if (T <= 384) return {0, (unsigned)n};
+    if (T <= SSM_WHOLE) return {0, (unsigned)n};
     const double blocks = d.H / heads_per_group(d), join = (double)d.H * 128 * d.dv * 8 / 5e6;
     const long long places = places_of(n, T);
     Shares best{places, 1};
@@ -770,7 +770,7 @@ Shares shares(const gdnq_ssm_desc &d, int n, int T)
 size_t ssm_workspace(const gdnq_ssm_desc &d, int n, int T)
 {
     long long most = 0;
-    if (T > 384) share_counts((double)(d.H / heads_per_group(d)), [&](long long want) { most = want; });
+    if (T > SSM_WHOLE) share_counts((double)(d.H / heads_per_group(d)), [&](long long want) { most = want; });
     most = std::min(most, (places_of(n, T) + 2 * CH - 1) / (2 * CH));
     return (size_t)most * (size_t)d.H * (2 * (size_t)d.dk * d.dv + 1) * 4;
 }

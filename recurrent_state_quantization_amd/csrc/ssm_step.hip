@@ -20,6 +20,7 @@ struct SsmStepArgs {
     float dt_min, dt_max;
     bool sp;
     Divisor byH, byG;
+    unsigned nx;   // width of the grid
 };
 
 template <bool BF16, int DK, int DV>
@@ -30,11 +31,12 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepArgs A)
     constexpr int NP = DK / RP;
     __shared__ float bl[DK], cl[DK], red[4][DV];
     const int t = (int)__builtin_amdgcn_workitem_id_x();
-    const unsigned g = __builtin_amdgcn_workgroup_id_x();
+    const unsigned g = block_id(A.nx);
     const unsigned i = __builtin_amdgcn_readfirstlane(div_by(g, A.byH));
     const unsigned h = __builtin_amdgcn_readfirstlane(g - i * (unsigned)A.H);
     const unsigned hb = div_by(h, A.byG);
     const gdnq_ssm_io &io = A.c.io;
+    if (i >= (unsigned)A.c.n) return;
     const int slot = A.c.slots ? A.c.slots[i] : (int)i;
     if (slot < 0 || slot >= A.c.n_slots) return;   // uniform, before the barriers
     const int cq = t % QL, r0 = t / QL;
@@ -93,12 +95,13 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmStepArgs A)
 hipError_t launch_ssm_step(const gdnq_ssm_desc &d, const SsmCall &c, hipStream_t st)
 {
     const int hk = d.hk ? d.hk : d.H;
+    const dim3 grid = grid_of((unsigned)c.n * (unsigned)d.H, 256);
     const SsmStepArgs A{c, d.H, hk, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
-                        make_divisor((unsigned)d.H), make_divisor((unsigned)(d.H / hk))};
+                        make_divisor((unsigned)d.H), make_divisor((unsigned)(d.H / hk)), grid.x};
     return with_dims(d.dk, d.dv, [&](auto DK, auto DV) {
         return with_bool(d.io_dtype == GDNQ_IO_BF16, [&](auto bf) {
             hipLaunchKernelGGL((ssm_step_kernel<decltype(bf)::value, decltype(DK)::value, decltype(DV)::value>),
-                               dim3((unsigned)c.n * (unsigned)d.H), dim3(256), 0, st, A);
+                               grid, dim3(256), 0, st, A);
             return hipGetLastError();
         });
     });

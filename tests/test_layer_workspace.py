@@ -33,3 +33,14 @@ def test_workspace_of_a_long_call_is_as_large_as_its_shares(g):
     """64 heads in blocks of 4 are 16 workgroups a share, so 16 shares fill 256
     compute units: two states and an exponent for each and every head."""
     assert g.gdnq_ssm_workspace(g.SsmDesc(H=64, dk=128, dv=64, hk=1), 1, 16384) == 16 * 64 * (2 * 128 * 64 + 1) * 4
+
+
+def test_more_workgroups_than_a_grid_holds(g):
+    """Sequences of a short call without tokens still take workgroups."""
+    from recurrent_state_quantization_amd import layer
+    base, far = 1 << 40, 1 << 36
+    io = layer._SsmIo(*[base + i * far for i in range(8)], 0, 0, 0, 0, 0)
+    d = g.SsmDesc(H=64, dk=64, dv=64, hk=64).c()
+    p = [base + i * far for i in range(8, 13)]
+    rc = g.lib.gdnq_ssm_prefill(d, io, p[0], 2, p[1], None, p[2], 1 << 19, 384, p[3], 1 << 30, 0)
+    assert rc == 1 and "n_seqs*H" in g.lib.gdnq_last_error().decode()
