@@ -73,8 +73,9 @@ constexpr long long PAD = 192;
 struct SsmArgs {
     SsmCall c;
     int H, hk;
-    long long len;       // places of a share; 0: one share per sequence, its whole length
+    long long len;       // places of a share (share_len() has the last word); 0: one share per sequence, its whole length
     unsigned ids;        // shares
+    double per_chunk;    // 1 / (CH ids)
     float dt_min, dt_max;
     bool sp;
     Divisor byHB;        // head blocks per share
@@ -252,26 +253,49 @@ struct SsmLds {
     int mode[2][HEADS];
 };
 
-// The last sequence that begins at place `at` or before it (sequence b begins
-// at cu[b] + PAD b): a probe per lane, 64 sequences a round, in [0, n) also
-// with bounds that break the rules.
-__device__ __forceinline__ int seq_at(const int32_t *cu, int n, long long at)
+// The last of the numbers 0 .. n - 1 for which `in` holds, where it holds up to
+// one and not behind (0 is taken to): a probe per lane, 64 numbers a round, in
+// [0, n) whatever `in` says.
+template <class In>
+__device__ __forceinline__ int last_of(int n, In &&in)
 {
     const int lane = (int)(__builtin_amdgcn_workitem_id_x() & 63u);
     int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int step = (hi - lo + 63) / 64;
         const long long p = lo + (long long)lane * step;
-        bool in = lane == 0;
-        if (p < hi && lane) in = (long long)cu[p] + PAD * p <= at;
-        const int k = __popcll(__ballot(in));
+        bool yes = lane == 0;
+        if (p < hi && lane) yes = in(p);
+        const int k = __popcll(__ballot(yes));
         lo += (k - 1) * step;
         if (lo + step < hi) hi = lo + step;
     }
     return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// A share: the pieces of sequences on its A.len places, one after another.
+// The last sequence that begins at place `at` or before it (sequence b begins
+// at cu[b] + PAD b).
+__device__ __forceinline__ int seq_at(const int32_t *cu, int n, long long at)
+{
+    return last_of(n, [&](long long p) { return (long long)cu[p] + PAD * p <= at; });
+}
+
+// Places of a share.  The host's length deals out all T rows and n sequences;
+// where rows behind the last sequence, or sequences without tokens at the end,
+// pad the call, the shares are cut from the places before them (4096 tokens in
+// one of 512 sequences 96 us, 380 with the host's; 2048 of 16384 rows 54, 145).
+// total and before are the last two bounds, which a kernel reads first of all.
+__device__ __forceinline__ long long share_len(const SsmArgs &A, int total, int before)
+{
+    const int n = A.c.n;
+    const bool empty = n > 1 && before == total;
+    if (total < 0 || total > A.c.T || (total == A.c.T && !empty)) return A.len;
+    const int used = empty ? last_of(n, [&](long long p) { return A.c.cu[p] < total; }) : n - 1;
+    const long long chunks = (long long)((double)(total + PAD * used) * A.per_chunk) + 1;
+    return min(max(chunks, 2ll) * CH, A.len);
+}
+
+// A share: the pieces of sequences on its places of share_len(), one after another.
 // STATE: only the state and decay of its last piece, if that piece's sequence
 // goes on behind it.  MANY: a share may hold more than one piece; one alone
 // spares the loop's registers (16384 tokens of 64 heads of 128 x 64 191 us,
@@ -296,14 +320,15 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
     const int c = lane & 31, hh = lane >> 5;
     // accumulator r of the state's block nb is row 32 nb + 8 (r/4) + 4 hh + r % 4, column 32 slice + c
     const size_t soff = (size_t)(4 * hh) * DV + slice * 32 + c;
+    const int total = A.c.cu[A.c.n], before = A.c.cu[A.c.n - 1];
     const float Ah = uniform(io.A[head] * 1.44269504f), bias = uniform(io.dt_bias ? io.dt_bias[head] : 0.0f);
     const float Dh = uniform(io.D ? io.D[head] : 0.0f);
     if constexpr (!STATE) {   // the blocks above the diagonal stay zero
         for (int i = t; i < 2 * 6 * 2 * 64; i += G::NT)
             *reinterpret_cast<uint4 *>(&L.g[0][0][0][i * 8]) = make_uint4(0, 0, 0, 0);
     }
-    const long long from = A.len * id, to = from + A.len;
-    const int b0 = A.len == 0 ? (int)id : seq_at(A.c.cu, A.c.n, STATE ? to - 1 : from);
+    const long long len = A.len ? share_len(A, total, before) : 0, from = len * id, to = from + len;
+    const int b0 = len == 0 ? (int)id : seq_at(A.c.cu, A.c.n, STATE ? to - 1 : from);
     for (int sq = b0; sq < A.c.n; sq++) {
         if (MANY && sq > b0) {   // a bound out of range ends nothing: its sequences are skipped below
             const int at = A.c.cu[sq];
@@ -313,8 +338,8 @@ __global__ __launch_bounds__((SsmGeom<DK, DV, HPW>::NT)) void ssm_chunk_kernel(S
         const bool is = seq_rows(A.c.cu, A.c.slots, sq, A.c.T, A.c.n_slots, q);
         // the piece's first token and the one behind its last, in the sequence
         const long long v0 = q.start + PAD * sq;
-        const int t0 = A.len && from > v0 ? (int)min(from - v0, (long long)q.len) : 0;
-        const int t1 = A.len ? (int)max(min(to - v0, (long long)q.len), 0ll) : q.len;
+        const int t0 = len && from > v0 ? (int)min(from - v0, (long long)q.len) : 0;
+        const int t1 = len ? (int)max(min(to - v0, (long long)q.len), 0ll) : q.len;
         const bool last = t1 == q.len;
         if (!is || t0 >= t1 || (STATE && last)) {
             if constexpr (MANY) continue;
@@ -672,12 +697,14 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart
     const unsigned g = __builtin_amdgcn_workgroup_id_x();
     const unsigned bh = div_by(g, byPart), part = g - bh * byPart.d;
     const unsigned nr = __builtin_amdgcn_readfirstlane(div_by(bh, byH)), h = bh - nr * byH.d;
-    const int b = shared ? seq_at(A.c.cu, A.c.n, A.len * (nr + 1) - 1) : (int)nr;
+    const long long len = share_len(A, A.c.cu[A.c.n], A.c.cu[A.c.n - 1]);
+    const int b = shared ? seq_at(A.c.cu, A.c.n, len * (nr + 1) - 1) : (int)nr;
     SeqTile q;
     if (!seq_rows(A.c.cu, A.c.slots, b, A.c.T, A.c.n_slots, q)) return;
     const long long v0 = q.start + PAD * b;
-    const size_t first = (size_t)(v0 / A.len), end = (size_t)((v0 + q.len - 1) / A.len);   // the shares it is in
-    if (first == end || (shared && first != nr)) return;
+    // the shares it is in (bounds that break the rules may put it behind the last)
+    const size_t first = (size_t)(v0 / len), end = min((size_t)((v0 + q.len - 1) / len), (size_t)A.ids - 1);
+    if (first >= end || (shared && first != nr)) return;
     const size_t at = (size_t)part * 256 + __builtin_amdgcn_workitem_id_x(), step = (size_t)A.H * E / 4;
     float4 *ws = reinterpret_cast<float4 *>(A.ws) + (size_t)h * (E / 4) + at;
     const float *lg = A.ws + 2 * (size_t)A.ids * A.H * E + h;
@@ -783,7 +810,7 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
     const int hk = d.hk ? d.hk : d.H, hpw = wide ? heads_per_group(d) : 1;
     const Shares sh = shares(d, c.n, c.T);
     const unsigned ids = sh.ids, blocks = (unsigned)(d.H / hpw);
-    const SsmArgs A{c, d.H, hk, sh.len, ids, d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
+    const SsmArgs A{c, d.H, hk, sh.len, ids, 1.0 / ((double)CH * ids), d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
                     make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
     return with_dims(d.dk, d.dv, [&](auto DK, auto DV) {
         const auto go = [&](auto HPW, auto WIDE) {

@@ -161,3 +161,60 @@ def test_tokens_with_steps_of_the_largest_and_lowest_value(io):
         b = ym[0] * (e + (dk + 8) * L.U)[:, None]
         got = y[i].double().cpu().numpy().reshape(H, dv)
         assert not (np.abs(got - ref[0]) > b + (np.abs(ref[0]) + b) * L.ROUND[io] + 2.0 ** -120).any()
+
+
+def _packed(g, T, lens, n, H=64, dk=128, dv=64):
+    """A call of `lens` in n sequences (the rest empty) over T rows, as a closure."""
+    torch = torch_cuda()
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    t = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    de = g.SsmDesc(H=H, dk=dk, dv=dv, hk=1).c()
+    x, B, C, dt = t(T, H * dv), t(T, dk), t(T, dk), t(T, H)
+    A = -torch.rand(H, generator=gen, device="cuda") - 1
+    S = torch.zeros(n, H, dk, dv, device="cuda")
+    cu = torch.full((n + 1,), sum(lens), dtype=torch.int32, device="cuda")
+    cu[:len(lens) + 1] = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32)
+    ws = torch.empty(max(1, g.gdnq_ssm_workspace(de, n, T)), dtype=torch.uint8, device="cuda")
+    y = torch.empty_like(x)
+    return lambda: g.gdnq_ssm_prefill(de, x, B, C, dt, A, None, None, y, S, n, None, None, cu, n, T, ws)
+
+
+def _time(f):
+    torch = torch_cuda()
+    best = 1e9
+    for _ in range(5):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        f()
+        a.record()
+        for _ in range(5):
+            f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) / 5)
+    return best
+
+
+@pytest.mark.parametrize("T,lens,n", [(4096, [4096], 512), (4096, [3000, 1096], 256), (16384, [2048], 64),
+                                      (16384, [2048], 1)])
+def test_padded_batches_take_no_longer(T, lens, n):
+    """Empty sequences behind the last and rows of none (a batch padded to
+    the sizes of a captured graph) leave the work spread over the card."""
+    g = lib()
+    say("scan padded", T, lens, n)
+    plain, padded = _time(_packed(g, sum(lens), lens, len(lens))), _time(_packed(g, T, lens, n))
+    print(f"{plain * 1e3:.1f} us, padded {padded * 1e3:.1f} us")
+    assert padded < 2 * plain
+
+
+@pytest.mark.parametrize("lens,tail", [([700, 0, 33] + [0] * 60, 0), ([0] * 40 + [450] + [0] * 300, 900), ([129, 500], 3000),
+                                       ([600], 2000), ([0] * 5, 1000), ([5] + [0] * 70, 600)])
+def test_padded_batches(lens, tail):
+    say("scan padded values", len(lens), tail)
+    H, dk, dv, T = 8, 64, 64, sum(lens) + tail
+    p = _problem(T, T, H, dk, dv, 2, "bf16", len(lens))
+    cont = [i % 2 for i in range(len(lens))]
+    got, gS = _call(p, lens, H, dk, dv, 2, tail=tail, cont=cont)
+    _check(p, got, gS, lens, cont, H, dk, dv, 2)
+    for i, m in enumerate(lens):
+        if m == 0:
+            assert np.array_equal(gS[i], p["S"][i].astype(np.float64))
