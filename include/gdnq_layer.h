@@ -32,7 +32,8 @@
  *    non-decreasing, from >= 0 to <= T).  Rows that belong to no sequence are
  *    left as they were.  A sequence whose bounds are outside 0 <= start <=
  *    end <= T is skipped on the device; one of zero tokens leaves its slot as
- *    it was.
+ *    it was.  Where cu_seqlens decreases, rows and slots of other sequences
+ *    may be left as they were too, or in part; nothing else is touched.
  *  - State pools: sequence or token i uses slot slots[i] (device int32; NULL:
  *    slot i, which needs n_slots >= n) of the n_slots in the pool.  An entry
  *    whose slot is outside [0, n_slots) is skipped on the device (nothing
@@ -132,6 +133,10 @@ int gdnq_ssm_workspace(const gdnq_ssm_desc *desc, int32_t n_seqs, int32_t T, siz
  * 2^22 elements apart (GDNQ_EUNSUPPORTED otherwise).  Runs chunk by chunk on
  * the matrix cores, fp32 operands split into bf16 parts (two for outputs, three
  * for states).
+ * Range: inside a chunk values carry factors from 2^-80 to 2^80, so a head's
+ * states and its sums of delta x and B (delta x)^T must stay below 2^40 in
+ * magnitude (larger ones may overflow), and y takes values that are not far
+ * above 2^-30 with an absolute error of up to 2^-46 (sum |C| + 64 max |B C|).
  * workspace: device, 16-byte aligned, at least gdnq_ssm_workspace bytes
  * (NULL where that is 0), free for other use once the call has run; calls
  * that may run at the same time need one each.

@@ -218,3 +218,61 @@ def test_padded_batches(lens, tail):
     for i, m in enumerate(lens):
         if m == 0:
             assert np.array_equal(gS[i], p["S"][i].astype(np.float64))
+
+
+@pytest.mark.parametrize("kind", ["even", "resets", "strong"])
+def test_each_head_by_its_own_decays(kind):
+    torch = torch_cuda()
+    say("scan heads", kind)
+    bits = np.array([0, 1e-3, 20, 70, 79, 81, 100, 140, 158, 162, 400, 5000], np.float64)
+    H, dk, dv, lens = len(bits), 128, 64, [300, 0, 1, 520]
+    T = sum(lens)
+    p = _problem(78, T, H, dk, dv, 2, "bf16", len(lens), kind == "strong")
+    if kind != "strong":
+        step = np.full((T, H), 0.25)
+        if kind == "resets":
+            step[:] = 1e-3
+            step[np.random.default_rng(3).integers(0, T, 3 * T // 64)] = 4.0
+        p["dt"] = torch.from_numpy(np.log(np.expm1(step)).astype(np.float32)).bfloat16()
+        p["dt_bias"] = np.zeros(H, np.float32)
+        p["A"] = (-bits * np.log(2.0) / (16.0 if kind == "even" else 12.0)).astype(np.float32)
+    cont = [1, 0, 1, 1]
+    got, gS = _call(p, lens, H, dk, dv, 2, cont=cont)
+    _check(p, got, gS, lens, cont, H, dk, dv, 2)
+
+
+@pytest.mark.parametrize("lens", [[100, 7], [700, 90]])
+@pytest.mark.parametrize("sp,D,bias", [(False, True, False), (True, False, True), (False, False, True), (True, True, False)])
+def test_options(lens, sp, D, bias):
+    """No softplus, clamped steps, no skip term, no bias."""
+    g = lib()
+    say("scan options", lens, sp, D, bias)
+    H, dk, dv, T = 4, 64, 128, sum(lens)
+    p = _problem(T, T, H, dk, dv, 2, "bf16", len(lens))
+    lo, hi = np.float32(0.004), np.float32(0.3)
+    if not sp:
+        p["dt"] = (p["dt"].float() * 0.3).bfloat16()   # about half of them below zero
+    got, gS = _call(p, lens, H, dk, dv, 2, D=D, bias=bias, cont=[1, 1], flags=g.SSM_SOFTPLUS if sp else 0,
+                    dt_min=float(lo), dt_max=float(hi))
+    _check(p, got, gS, lens, [1, 1], H, dk, dv, 2, D=D, bias=bias, sp=sp, lo=float(lo), hi=float(hi))
+
+
+@pytest.mark.parametrize("power", [-30, 0, 38])
+def test_magnitudes(power):
+    """States and inputs at the ends of the stated range, over decays up to
+    the kernel's borders.  What an output loses below it: parts of S 2^cs and
+    of w x under 2^-126, whose row's factor is 2^80 at most."""
+    torch = torch_cuda()
+    say("scan magnitudes", power)
+    bits = np.array([0, 20, 70, 79, 82, 110, 150, 158, 163, 900], np.float64)
+    H, dk, dv, lens = len(bits), 128, 64, [200, 450]
+    T = sum(lens)
+    p = _problem(9, T, H, dk, dv, 1, "bf16", 2)
+    p["x"] = p["x"] * 2.0 ** power
+    p["S"] = (p["S"] * 2.0 ** power).astype(np.float32)
+    p["dt"] = torch.full((T, H), 0.25).bfloat16()
+    p["A"] = (-bits * np.log(2.0) / 16.0).astype(np.float32)
+    got, gS = _call(p, lens, H, dk, dv, 1, bias=False, cont=[1, 1], flags=0)
+    C = p["C"].double().abs().sum(1).max().item()
+    CB = 64 * (p["C"].double() @ p["B"].double().T).abs().max().item()
+    _check(p, got, gS, lens, [1, 1], H, dk, dv, 1, low=2.0 ** -46 * (C + CB), exact_delta=True, bias=False, sp=False)
