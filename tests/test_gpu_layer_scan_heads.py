@@ -276,3 +276,66 @@ def test_magnitudes(power):
     C = p["C"].double().abs().sum(1).max().item()
     CB = 64 * (p["C"].double() @ p["B"].double().T).abs().max().item()
     _check(p, got, gS, lens, [1, 1], H, dk, dv, 1, low=2.0 ** -46 * (C + CB), exact_delta=True, bias=False, sp=False)
+
+
+def test_one_graph_for_batches_of_many_sizes():
+    """A call captured at its largest size, replayed over other bounds: each
+    replay equals the eager call on the same bounds, bit for bit."""
+    torch = torch_cuda()
+    g = lib()
+    say("scan graph of padded batches")
+    H, dk, dv, n, T = 16, 128, 64, 24, 3000
+    p = _problem(6, T, H, dk, dv, 1, "bf16", n)
+    d = _dev(p)
+    S0, y = d["S"].clone(), torch.zeros_like(d["x"])
+    cu = torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    cont = torch.ones(n, dtype=torch.int32, device="cuda")
+    de = g.SsmDesc(H=H, dk=dk, dv=dv, hk=1)
+    ws = torch.empty(g.gdnq_ssm_workspace(de, n, T), dtype=torch.uint8, device="cuda")
+
+    def call(stream=None):
+        g.gdnq_ssm_prefill(de, d["x"], d["B"], d["C"], d["dt"], d["A"], d["D"], d["dt_bias"], y, d["S"], n, None, cont, cu,
+                           n, T, ws, stream=stream)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens in ([T], [1] * n, [700, 0, 800, 1], [0, 0, 5], [], [125] * n, [2999] + [0] * 10 + [1], [400] * 7):
+        bounds = np.full(n + 1, sum(lens))
+        bounds[:len(lens) + 1] = np.concatenate([[0], np.cumsum(lens)])
+        cu.copy_(torch.from_numpy(bounds.astype(np.int32)))
+        both = []
+        for f in (call, graph.replay):
+            d["S"].copy_(S0)
+            y.fill_(7.0)
+            f()
+            torch.cuda.synchronize()
+            both.append((y.clone(), d["S"].clone()))
+        assert torch.equal(both[0][0], both[1][0]) and torch.equal(both[0][1], both[1][1]), lens
+        assert bool((both[0][0][sum(lens):] == 7).all())
+        for i in range(n):
+            if bounds[i] == bounds[i + 1]:
+                assert torch.equal(both[0][1][i], S0[i])
+
+
+@pytest.mark.parametrize("cu", [[0, 1000, 400], [0, 1400, 3], [1000, 1200, 0], [0, 1500, 1499], [600, 1, 1]])
+def test_decreasing_bounds_touch_nothing_outside(cu):
+    torch = torch_cuda()
+    g = lib()
+    say("scan decreasing bounds", cu)
+    H, dk, dv, T = 16, 64, 64, 1500
+    p = _problem(1, T, H, dk, dv, 1, "bf16", 2)
+    d = _dev(p)
+    de = g.SsmDesc(H=H, dk=dk, dv=dv, hk=1)
+    buf = torch.full((T + 128, H * dv), 3.0, dtype=torch.bfloat16, device="cuda")
+    nb = g.gdnq_ssm_workspace(de, 2, T)
+    ws = torch.full((nb + 256,), 0x7F, dtype=torch.uint8, device="cuda")
+    g.gdnq_ssm_prefill(de, d["x"], d["B"], d["C"], d["dt"], d["A"], None, None, buf[64:64 + T], d["S"], 2, None, None,
+                       torch.tensor(cu, dtype=torch.int32, device="cuda"), 2, T, ws)
+    torch.cuda.synchronize()
+    assert (buf[:64] == 3).all() and (buf[64 + T:] == 3).all() and (ws[nb:] == 0x7F).all()
+    for i in range(2):
+        if not 0 <= cu[i] < cu[i + 1] <= T:
+            assert np.array_equal(d["S"][i].cpu().numpy(), p["S"][i])
