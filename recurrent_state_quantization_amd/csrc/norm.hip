@@ -9,7 +9,10 @@
 // consecutive.  NT and K grow with the group (norm_dispatch).  Measured in
 // bf16: 32768 rows of 4096 gated in groups of 512 135 us (6.0 TB/s; a large
 // copy reaches 5.0), 32768 x 4096 on an fp32 residual stream with a norm
-// behind the block 297 us (5.4 TB/s).
+// behind the block 297 us (5.4 TB/s).  Small groups leave lanes idle (16 a
+// group at least: 32768 x 4096 in groups of 64 186 us, 4.3 TB/s; 4080 in groups
+// of 24 429 us), and rows that are not multiples of 16 bytes take one value a
+// lane (32768 x 4097 369 us, 2.2 TB/s; residual 526 us, 3.1 TB/s).
 #include "layer_launchers.hpp"
 #include "rows.hpp"
 

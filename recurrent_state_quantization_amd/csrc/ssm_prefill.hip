@@ -16,13 +16,18 @@
 // tokens behind j, which keeps it exact where it is small.  A head whose
 // chunk decays further, to -2 RANGE, counts the exponents from a whole number
 // h near cs_63 / 2 instead of 0 and decays S by 2^{cs_63 - h} before and by
-// 2^h after, both as exact as without; beyond that its outputs are formed from factors that are all at most one:
+// 2^h after, which loses no digits; beyond that its outputs are formed from
+// factors that are all at most one:
 //   Y = (tril(C B^T) . e^{cs_i - cs_j} delta_j) X + diag(e^{cs_i}) C S + D X.
 //
 // Precision: the products run on the bf16 matrix instructions with fp32
 // sums.  B, C and x are bf16, so C B^T is exact up to the sum.  The fp32
 // operands of the outputs, tril(C B^T), S' and w X, are taken in two bf16
-// parts (off by at most 2^-16 of an operand); the state's update takes w X in
+// parts (off by at most 2^-16 of an operand; by a model of one chunk 4e-6 of
+// an output row in norm, where the outputs' own rounding is 1.7e-3, so that 3
+// outputs in 1000 round to a neighbour; a third part would be a third more
+// products).  An output's decays come from sums over a chunk of at most 160 in
+// base 2, each off by up to 8 2^-24 of that.  The state's update takes w X in
 // three (2^-24), so that states stay as exact as fp32 (with two they measured
 // 1.7e-6 off in norm, and the call took 0.86 of the time).
 //
@@ -73,7 +78,7 @@ constexpr long long PAD = 192;
 struct SsmArgs {
     SsmCall c;
     int H, hk;
-    long long len;       // places of a share (share_len() has the last word); 0: one share per sequence, its whole length
+    long long len;       // places of a share at most (share_len()); 0: one share per sequence, its whole length
     unsigned ids;        // shares
     double per_chunk;    // 1 / (CH ids)
     float dt_min, dt_max;
@@ -721,7 +726,10 @@ __global__ __launch_bounds__(256) void ssm_join_kernel(SsmArgs A, Divisor byPart
 }
 
 // Heads per workgroup: as many as share B and C and fit its 8 waves, a power
-// of two; rows that need narrow accesses take one.
+// of two; rows that need narrow accesses take one.  Fewer waves have nothing
+// to overlap their splits with: 16384 tokens of 60 heads of 128 x 64 take 246
+// us at H / hk = 6, 451 at 3; 64 heads 218 at 4, 464 at 1, 435 with y alone
+// unaligned.
 int heads_per_group(const gdnq_ssm_desc &d)
 {
     const int per = d.hk ? d.H / d.hk : 1;
@@ -768,7 +776,8 @@ long long places_of(int n, int T) { return T + PAD * (n - 1); }
 // round, one, two, three: 16384 tokens of 64 heads of 128 x 64 290, 194, 224,
 // 257; 32731 tokens in 9 sequences of 32 heads of 128 x 128 566, 368, 404, 423;
 // 32768 in 4 of 80 heads of 128 x 64 1196, 635, 634, 633; 6000 in 20 of 24
-// heads 79, 63, 78, 79.
+// heads 79, 63, 78, 79.  The prices are those of workgroups of 8 waves, and
+// narrow rows are dealt out as wide ones are.
 Shares shares(const gdnq_ssm_desc &d, int n, int T)
 {
     if (T <= SSM_WHOLE) return {0, (unsigned)n};
@@ -810,8 +819,8 @@ hipError_t launch_ssm_prefill(const gdnq_ssm_desc &d, const SsmCall &c, hipStrea
     const int hk = d.hk ? d.hk : d.H, hpw = wide ? heads_per_group(d) : 1;
     const Shares sh = shares(d, c.n, c.T);
     const unsigned ids = sh.ids, blocks = (unsigned)(d.H / hpw);
-    const SsmArgs A{c, d.H, hk, sh.len, ids, 1.0 / ((double)CH * ids), d.dt_min, d.dt_max, (d.flags & GDNQ_SSM_SOFTPLUS) != 0,
-                    make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
+    const SsmArgs A{c, d.H, hk, sh.len, ids, 1.0 / ((double)CH * ids), d.dt_min, d.dt_max,
+                    (d.flags & GDNQ_SSM_SOFTPLUS) != 0, make_divisor(blocks), reinterpret_cast<float *>(c.ws)};
     return with_dims(d.dk, d.dv, [&](auto DK, auto DV) {
         const auto go = [&](auto HPW, auto WIDE) {
             using G = SsmGeom<DK.value, DV.value, HPW.value>;
