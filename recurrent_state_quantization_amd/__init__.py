@@ -235,3 +235,9 @@ def alloc_state(desc: Desc, device="cuda"):
 from .layer import (CONV_SILU, NORM_GATE_FIRST, NORM_GATE_SIGMOID, NORM_GROUP_WEIGHT, NORM_RES_F32,  # noqa: E402,F401
                     SSM_SOFTPLUS, ConvDesc, NormDesc, SsmDesc, gdnq_conv_prefill, gdnq_conv_step, gdnq_norm_gated,
                     gdnq_norm_residual, gdnq_ssm_prefill, gdnq_ssm_step, gdnq_ssm_workspace)
+
+# The operators of a softmax attention layer beside it (include/gdnq_attn.h).
+from .attn import (ROPE_BASE, ROPE_INTERLEAVED, ROPE_INVERSE, ROPE_LINEAR, ROPE_PLAIN,  # noqa: E402,F401
+                   ROPE_RAMP_INDEX, ROPE_RAMP_TURNS, AttnDesc, Kv, RopeDesc, RopeFreqs, gdnq_attn_step,
+                   gdnq_attn_workspace, gdnq_kv_append, gdnq_kv_evict, gdnq_kv_evict_workspace, gdnq_rope,
+                   gdnq_rope_table)

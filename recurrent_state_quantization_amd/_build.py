@@ -30,8 +30,10 @@ LIB = os.path.join(HERE, "libgdnq.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.cpp", "decode.hip", "window.hip", "codec.hip", "calibrate.hip", "prefill.hip", "prefill_kda.hip",
-           "layer_api.cpp", "conv.hip", "ssm_step.hip", "ssm_prefill.hip", "norm.hip"]
-HEADERS = ["tile.hpp", "codec.hpp", "launch.hpp", "launchers.hpp", "errors.hpp", "rows.hpp", "layer_launchers.hpp"]
+           "layer_api.cpp", "conv.hip", "ssm_step.hip", "ssm_prefill.hip", "norm.hip",
+           "attn_api.cpp", "rope.hip", "kv_append.hip", "attn_step.hip", "kv_evict.hip"]
+HEADERS = ["tile.hpp", "codec.hpp", "launch.hpp", "launchers.hpp", "errors.hpp", "checks.hpp", "rows.hpp",
+           "layer_launchers.hpp", "attn_launchers.hpp", "paged.hpp", "rotate.hpp"]
 
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off",

@@ -1,0 +1,82 @@
+// rope.hip -- rotary positions of every head of a batch of token rows
+// (gdnq_rope).
+//
+// A workgroup takes some rows: it forms the (cos, sin) pairs of each row once,
+// in LDS, and turns all heads with them.
+#include "attn_launchers.hpp"
+#include "rotate.hpp"
+
+namespace gdnq {
+namespace {
+
+constexpr int MAX_CS = 2048;   // (cos, sin) pairs of a workgroup's rows: 16 KB
+
+struct RopeArgs {
+    RopeCall c;
+    HeadPieces p;
+    int d, rows, heads;   // rows and heads per workgroup
+    float amp;
+    bool inverse;
+    Divisor byRow, byPairs, bySplit;   // pieces per row, pairs per row, groups of heads
+    unsigned nx;              // width of the grid
+};
+
+template <bool BF16, int V, bool INTER>
+__global__ __launch_bounds__(256) void rope_kernel(RopeArgs A)
+{
+    __shared__ float2 cs[MAX_CS];
+    const int t = (int)__builtin_amdgcn_workitem_id_x();
+    const unsigned id = block_id(A.nx), rb = div_by(id, A.bySplit);
+    const long long first = (long long)rb * A.rows;
+    if (first >= A.c.rows) return;
+    const int r0 = (int)first, h0 = (int)(id - rb * A.bySplit.d) * A.heads;
+    const int nr = min(A.rows, A.c.rows - r0), nh = min(A.heads, A.c.H - h0);
+    const int pairs = A.p.rot / 2;
+    for (int i = t; i < nr * pairs; i += 256) {
+        const int r = (int)div_by((unsigned)i, A.byPairs);
+        const long long pos = A.c.pos[r0 + r];
+        unsigned long long f = A.c.table[i - r * pairs] * (unsigned long long)pos;
+        if (A.inverse) f = 0ull - f;
+        cs[i] = turn(f, A.amp);
+    }
+    __syncthreads();
+    const int per = A.heads * A.p.ni;
+    for (int i = t; i < nr * per; i += 256) {
+        const int r = (int)div_by((unsigned)i, A.byRow), in_row = i - r * per;
+        const int h = (int)div_by((unsigned)in_row, A.p.byNi);
+        if (h >= nh) continue;
+        const size_t at = (size_t)(h0 + h) * A.d;
+        turn_piece<BF16, V, INTER>(A.c.x, (size_t)(r0 + r) * A.c.ldx + at, A.c.y, (size_t)(r0 + r) * A.c.ldy + at,
+                                   in_row - h * A.p.ni, cs + r * pairs, A.p);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rope(const gdnq_rope_desc &d, const RopeCall &c, hipStream_t st)
+{
+    const bool bf16 = d.io_dtype == GDNQ_IO_BF16, inter = d.flags & GDNQ_ROPE_INTERLEAVED;
+    const int es = bf16 ? 2 : 4;
+    const bool wide = wide_pieces(d.d, d.rot, inter, es) && wide_rows(c.x, c.ldx, es) && wide_rows(c.y, c.ldy, es);
+    RopeArgs A{c, head_pieces(d.d, d.rot, inter, wide ? 16 / es : 1), d.d, 1, c.H, d.amp,
+               (d.flags & GDNQ_ROPE_INVERSE) != 0, {}, {}, {}, 0};
+    A.rows = 1;
+    A.byRow = make_divisor((unsigned)(A.heads * A.p.ni));
+    A.byPairs = make_divisor((unsigned)(d.rot / 2));
+    const unsigned split = (unsigned)((c.H + A.heads - 1) / A.heads);
+    A.bySplit = make_divisor(split);
+    const dim3 grid = grid_of((unsigned long long)((c.rows + A.rows - 1) / A.rows) * split, 256);
+    A.nx = grid.x;
+    return with_bool(bf16, [&](auto b) {
+        return with_bool(wide, [&](auto w) {
+            return with_bool(inter, [&](auto n) {
+                constexpr bool B = decltype(b)::value;
+                constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
+                hipLaunchKernelGGL((rope_kernel<B, V, decltype(n)::value>), grid, dim3(256), 0, st, A);
+                return hipGetLastError();
+            });
+        });
+    });
+}
+
+}  // namespace gdnq
