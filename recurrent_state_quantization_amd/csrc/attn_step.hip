@@ -3,6 +3,31 @@
 //   s_r = scale q . k_r,  w_r = e^{s_r - m} / sum e^{s - m},  o = sum w_r v_r
 // with one pass over the rows, which keeps the running maximum m, the sum and
 // the output, all in fp32.
+//
+// Keys and values are read once, 4 d H rows operations against them: bound by
+// HBM, so the kernel is made of loads in flight.  The query heads of a cache
+// head are the columns of a matrix product (16 at a time, the missing ones
+// zeros), so a row is read once for all of them:
+//
+//   S [rows x heads] = K Q^T,  then  O^T [d x heads] += V^T W^T
+//
+// The instruction's accumulator has a head per lane and four rows of a lane in
+// its registers, which is how its second operand wants the weights if the sum
+// over rows is taken in that order: the weights never leave their lane.  The
+// other operand wants for one column of V eight rows in one lane: a lane loads
+// 16 bytes of each of its rows and picks the columns apart with byte
+// permutes, so neither K nor V goes through LDS.  In bf16 a weight is split
+// into two bf16 parts, which leave 2^-17 of it (one part would leave 2^-9,
+// and the matrix cores have nothing else to do); in fp32 the products are fp32.
+//
+// Work is dealt out in units of 4 steps (one per wave) of an entry and a cache
+// head, entry after entry, in equal shares over a fixed number of workgroups,
+// whatever the entries' lengths: every workgroup finds its share from all
+// lengths by a prefix sum.  An entry and head inside one share is finished there;
+// the pieces of the others (maximum, sum, output) go to the workspace, and a
+// second kernel joins them.
+#include <algorithm>
+
 #include "attn_launchers.hpp"
 #include "paged.hpp"
 #include "rows.hpp"
@@ -11,100 +36,747 @@ namespace gdnq {
 namespace {
 
 constexpr float LOG2E = 1.44269504f, LOWEST = -3.4028234e38f;
+constexpr int NT = 256, NW = NT / 64;
+constexpr int SHARES = 512;   // workgroups at most: two for each compute unit
 
-struct AttnArgs {
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned long long u64;
+
+// Where a share begins: entry, pair (cache head and 16 of its query heads), unit of
+// the pair, and the pair's units; and the units of all entries (0: the share has
+// none).
+struct Start {
+    int i, p, u, units;
+    u64 all;
+};
+
+// The workspace's parts.
+struct Space {
+    Start *start;       // [shares], for the second kernel
+    float *part_ml;     // [2 shares][16][2]: maximum and sum of a share's first and last piece
+    float *part_o;      // [2 shares][gt][D]
+    float *whole_ml;    // [n P][16][2], for the sums of weights
+    float *scores;      // [n_pages][hk][G][page], likewise
+};
+
+struct StepArgs {
     AttnCall c;
-    int H, hk, shift, window;
-    float scale2, decay;   // scale log2(e): weights are powers of two
-    Divisor byHk;
-    unsigned nx;
+    Space w;
+    int H, hk, G, gt, nt, P;   // query heads per cache head, per pair; pairs per cache head, per entry
+    int shift, window, shares;
+    float scale2, decay;       // scale log2(e): weights are powers of two
+    bool wide_q;
 };
 
 template <bool BF16, int D>
-__global__ __launch_bounds__(256) void attn_simple_kernel(AttnArgs A)
-{
-    constexpr int E = D / 64;
-    __shared__ float mj[4], lj[4], oj[4][D];
-    const AttnCall &c = A.c;
-    const unsigned id = block_id(A.nx);
-    const unsigned i = div_by(id, A.byHk), h = id - i * (unsigned)A.hk;
-    if (i >= (unsigned)c.n) return;
+struct Geo {
+    static constexpr int J = BF16 ? 2 : 1, ROWS = 16 * J;      // rows of a step
+    static constexpr int ES = BF16 ? 2 : 4, E = 16 / ES;       // values in 16 bytes
+    static constexpr int KP = D / (4 * E);                     // 16-byte pieces of a key row in a lane
+    static constexpr int VW = D / 16;                          // values of a value row in a lane,
+    static constexpr int VP = VW * ES > 16 ? VW * ES / 16 : 1; // in pieces
+    static constexpr int VE = VW / VP;                         // of 16 bytes (8 for 64 bf16)
+    static constexpr int UNIT = NW * ROWS;                     // rows of a unit
+};
+
+// Rows [first, len) of an entry, in steps [t0, t1) and units.
+struct Entry {
     SlotRows s;
-    if (!slot_rows(c.kv, c.slots, (int)i, A.shift, s)) return;
-    const int t = (int)__builtin_amdgcn_workitem_id_x(), lane = t & 63, w = t >> 6;
-    const int first = A.window ? max(0, s.len - A.window) : 0, G = A.H / A.hk;
-    for (int g = 0; g < G; g++) {
-        const size_t hq = (size_t)(h * G + g) * D + lane * E;
-        float q[E], o[E], m = LOWEST, l = 0.0f;
+    int first, t0, t1, units;   // units 0: skipped; an entry without rows has one, without steps
+};
+
+template <int ROWS>
+__device__ __forceinline__ Entry entry_of(const StepArgs &A, int i)
+{
+    Entry e{};
+    if (!slot_rows(A.c.kv, A.c.slots, i, A.shift, e.s)) return e;
+    e.first = A.window ? max(0, e.s.len - A.window) : 0;
+    e.t0 = e.first / ROWS;
+    e.t1 = (e.s.len + ROWS - 1) / ROWS;
+    e.units = max(1, (e.t1 - e.t0 + NW - 1) / NW);
+    return e;
+}
+
+// First unit of share b of `shares` that divide `all` units; the share that holds unit x.
+__device__ __forceinline__ u64 share_begin(u64 all, int shares, int b) { return all * (unsigned)b / (unsigned)shares; }
+__device__ __forceinline__ int share_of(u64 all, int shares, u64 x) { return (int)(((x + 1) * (unsigned)shares - 1) / all); }
+
+// Sum over the lower threads, and over all, of the workgroup.
+__device__ __forceinline__ u64 sum_before(u64 x, u64 *part, u64 &all)
+{
+    const int t = (int)__builtin_amdgcn_workitem_id_x(), lane = t & 63;
+    u64 in = x;
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-            q[e] = load1<BF16>(c.q, (size_t)i * c.ldq + hq + e) * A.scale2;
-            o[e] = 0.0f;
+    for (int d = 1; d < 64; d *= 2) {
+        const u64 y = __shfl_up(in, d);
+        if (lane >= d) in += y;
+    }
+    if (lane == 63) part[t >> 6] = in;
+    __syncthreads();
+    u64 before = in - x;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+        if (w < (t >> 6)) before += part[w];
+        all += part[w];
+    }
+    return before;
+}
+
+// The units [x, end) of one of `shares` shares, and where it begins.
+struct Share {
+    u64 x, end;
+    int shares;
+    Start at;
+
+    __device__ __forceinline__ void bounds(const StepArgs &A, int b)
+    {
+        shares = (int)min((u64)A.shares, at.all);
+        x = share_begin(at.all, shares, b);
+        end = share_begin(at.all, shares, b + 1);
+    }
+};
+
+// Workgroup b's share; false: none.
+template <int ROWS>
+__device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh)
+{
+    __shared__ u64 part[NW];
+    __shared__ int at[4];
+    const int t = (int)__builtin_amdgcn_workitem_id_x();
+    const int per = (A.c.n + NT - 1) / NT, lo = min(t * per, A.c.n), hi = min(lo + per, A.c.n);
+    u64 mine = 0;
+    for (int i = lo; i < hi; i++) mine += (unsigned)entry_of<ROWS>(A, i).units;
+    const u64 before = sum_before(mine, part, sh.at.all) * (unsigned)A.P;
+    sh.at.all *= (unsigned)A.P;
+    mine *= (unsigned)A.P;
+    if ((unsigned)b >= min((u64)A.shares, sh.at.all)) {
+        sh.at.all = 0;
+        return false;
+    }
+    sh.bounds(A, b);
+    if (sh.x >= before && sh.x < before + mine) {
+        int i = lo;
+        u64 x = sh.x - before;
+        unsigned units;
+        for (;; i++) {
+            units = (unsigned)entry_of<ROWS>(A, i).units;
+            if (x < (u64)units * (unsigned)A.P) break;
+            x -= (u64)units * (unsigned)A.P;
         }
-        auto score = [&](int r, size_t &at, size_t &sum) {
-            const int p = s.table[r >> A.shift], off = r & ((1 << A.shift) - 1);
-            if (p < 0 || p >= c.kv.n_pages) return -INFINITY;
-            at = row_at(c.kv, p, (int)h, off) + lane * E;
-            sum = sum_at(A.hk, A.shift, p, (int)h, off);
-            float x = 0.0f;
-#pragma unroll
-            for (int e = 0; e < E; e++) x = fmaf(q[e], load1<BF16>(c.kv.k, at + e), x);
-            return lanes_sum<64>(x);
-        };
-        size_t at = 0, sum = 0;
-        for (int r = first + w; r < s.len; r += 4) {
-            const float x = score(r, at, sum);
-            if (x == -INFINITY) continue;
-            const float mn = fmaxf(m, x), f = __builtin_amdgcn_exp2f(m - mn), p = __builtin_amdgcn_exp2f(x - mn);
-            m = mn;
-            l = fmaf(l, f, p);
-#pragma unroll
-            for (int e = 0; e < E; e++) o[e] = fmaf(p, load1<BF16>(c.kv.v, at + e), o[e] * f);
+        const int p = (int)(x / units);
+        at[0] = i;
+        at[1] = p;
+        at[2] = (int)(x - (u64)p * units);
+        at[3] = (int)units;
+    }
+    __syncthreads();
+    sh.at.i = __builtin_amdgcn_readfirstlane(at[0]);
+    sh.at.p = __builtin_amdgcn_readfirstlane(at[1]);
+    sh.at.u = __builtin_amdgcn_readfirstlane(at[2]);
+    sh.at.units = __builtin_amdgcn_readfirstlane(at[3]);
+    return true;
+}
+
+// Every piece of the share: f(entry number, entry, pair, first and last unit).
+template <int ROWS, class F>
+__device__ __forceinline__ void for_pieces(const StepArgs &A, const Share &sh, F &&f)
+{
+    u64 x = sh.x;
+    int i = sh.at.i, p = sh.at.p, u = sh.at.u;
+    Entry e = entry_of<ROWS>(A, i);
+    while (x < sh.end) {
+        const int ue = (int)min((u64)e.units, u + (sh.end - x));
+        f(i, e, p, u, ue);
+        x += (unsigned)(ue - u);
+        u = 0;
+        if (++p == A.P && x < sh.end) {
+            p = 0;
+            do e = entry_of<ROWS>(A, ++i);   // units are left, so an entry with some follows
+            while (e.units == 0 && i + 1 < A.c.n);
         }
-        __syncthreads();
-        mj[w] = m;
-        lj[w] = l;
-#pragma unroll
-        for (int e = 0; e < E; e++) oj[w][lane * E + e] = o[e];
-        __syncthreads();
-        const float M = fmaxf(fmaxf(mj[0], mj[1]), fmaxf(mj[2], mj[3]));
-        float L = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; k++) L = fmaf(lj[k], __builtin_amdgcn_exp2f(mj[k] - M), L);
-        if (w == 0) {
-#pragma unroll
-            for (int e = 0; e < E; e++) {
-                float x = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 4; k++) x = fmaf(oj[k][lane * E + e], __builtin_amdgcn_exp2f(mj[k] - M), x);
-                store1<BF16>(c.o, (size_t)i * c.ldo + hq + e, L > 0.0f ? x / L : 0.0f);
-            }
-        }
-        if (c.kv.acc)
-            for (int r = first + w; r < s.len; r += 4) {
-                const float x = score(r, at, sum);
-                if (x == -INFINITY || lane != 0) continue;
-                const float was = c.kv.acc[sum];
-                c.kv.acc[sum] = (g == 0 ? A.decay * was : was) + __builtin_amdgcn_exp2f(x - M) / L;
-            }
     }
 }
 
+__device__ __forceinline__ float across_rows_max(float x)
+{
+    float a = x, b = x;
+    swap16(a, b);
+    x = fmaxf(a, b);
+    a = b = x;
+    swap32(a, b);
+    return fmaxf(a, b);
+}
+
+__device__ __forceinline__ float across_rows_sum(float x)
+{
+    float a = x, b = x;
+    swap16(a, b);
+    x = a + b;
+    a = b = x;
+    swap32(a, b);
+    return a + b;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+{
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, (bf16x2{(__bf16)a, (__bf16)b}));
+}
+
+// One wave's steps over a piece.  Lane = (head or row or column n = lane & 15, group g = lane >> 4).
+template <bool BF16, int D, bool SUMS>
+struct Steps {
+    using X = Geo<BF16, D>;
+    static constexpr int J = X::J;
+
+    const StepArgs &A;
+    const Entry &e;
+    int h, n, g;
+    size_t head;                 // of the cache, in elements
+    uint4 q[X::KP], k[J][X::KP];
+    uint4 v[J * 4][X::VP];       // row 16 j + 4 g + i at 4 j + i
+    f32x4 o[X::VP][X::VE];
+    float m, l;
+    int page_k[J], page_v[J];    // of the step loaded next
+    bool edge;                   // the loaded step has rows that do not count,
+    bool ok[J];                  // or whose page does not exist (of this lane's rows of V and scores)
+    int at_v[J];                 // (with SUMS) their pages
+
+    __device__ __forceinline__ Steps(const StepArgs &A_, const Entry &e_, int h_) : A(A_), e(e_), h(h_)
+    {
+        const int lane = (int)(__builtin_amdgcn_workitem_id_x() & 63u);
+        n = lane & 15;
+        g = lane >> 4;
+        head = (size_t)h * A.c.kv.ldh;
+    }
+
+    __device__ __forceinline__ const char *at(const void *base, int page, int r) const
+    {
+        const size_t off = (size_t)page * A.c.kv.ldp + head + (size_t)(r & ((1 << A.shift) - 1)) * A.c.kv.ldr;
+        return reinterpret_cast<const char *>(base) + off * X::ES;
+    }
+
+    __device__ __forceinline__ void load_q(int i, int hq, int heads)
+    {
+#pragma unroll
+        for (int c = 0; c < X::KP; c++) {
+            q[c] = make_uint4(0, 0, 0, 0);
+            if (n < heads) {
+                const size_t off = (size_t)i * A.c.ldq + (size_t)(hq + n) * D + c * 4 * X::E + g * X::E;
+                if (A.wide_q) q[c] = Pack<BF16, X::E>::load(A.c.q, off);
+                else {
+                    float x[X::E];
+#pragma unroll
+                    for (int w = 0; w < X::E; w++) x[w] = load1<BF16>(A.c.q, off + w);
+                    q[c] = Pack<BF16, X::E>::narrow(x);
+                }
+            }
+        }
+    }
+
+    // a row's page; rows behind the last take its page
+    __device__ __forceinline__ int page_of(int r) const { return e.s.table[min(r, e.s.len - 1) >> A.shift]; }
+
+    __device__ __forceinline__ void load_pages(int t)
+    {
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            page_k[j] = page_of(t * X::ROWS + 16 * j + n);
+            page_v[j] = page_of(t * X::ROWS + 16 * j + 4 * g);
+        }
+    }
+
+    __device__ __forceinline__ bool there(int page) const { return page >= 0 && page < A.c.kv.n_pages; }
+
+    __device__ __forceinline__ void load_k(int t)
+    {
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            const char *p = at(A.c.kv.k, there(page_k[j]) ? page_k[j] : 0, t * X::ROWS + 16 * j + n) + g * 16;
+#pragma unroll
+            for (int c = 0; c < X::KP; c++) k[j][c] = *reinterpret_cast<const uint4 *>(p + c * 64);
+        }
+    }
+
+    __device__ __forceinline__ void load_v(int t)
+    {
+        const int r0 = t * X::ROWS;
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            ok[j] = there(page_v[j]);
+            bad |= !ok[j];
+            at_v[j] = ok[j] ? page_v[j] : 0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const char *p = at(A.c.kv.v, at_v[j], r0 + 16 * j + 4 * g + i) + n * (X::VE * X::ES);
+#pragma unroll
+                for (int c = 0; c < X::VP; c++) {
+                    if constexpr (X::VE * X::ES == 16)
+                        v[4 * j + i][c] = *reinterpret_cast<const uint4 *>(p + c * 256);
+                    else {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                        v[4 * j + i][c] = make_uint4(x.x, x.y, 0, 0);
+                    }
+                }
+            }
+        }
+        edge = r0 < e.first || r0 + X::ROWS > e.s.len || __any(bad);
+    }
+
+    __device__ __forceinline__ f32x4 scores(int j) const
+    {
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < X::KP; c++) {
+            if constexpr (BF16)
+                s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[j][c]),
+                                                            __builtin_bit_cast(bf16x8, q[c]), s, 0, 0, 0);
+            else {
+                const f32x4 a = __builtin_bit_cast(f32x4, k[j][c]), b = __builtin_bit_cast(f32x4, q[c]);
+#pragma unroll
+                for (int w = 0; w < 4; w++) s = __builtin_amdgcn_mfma_f32_16x16x4f32(a[w], b[w], s, 0, 0, 0);
+            }
+        }
+        return s;
+    }
+
+    // column w of piece c of the eight rows
+    __device__ __forceinline__ bf16x8 column(int c, int w) const
+    {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint4 &a = v[2 * i][c], &b = v[2 * i + 1][c];
+            const uint32_t lo = w / 2 == 0 ? a.x : w / 2 == 1 ? a.y : w / 2 == 2 ? a.z : a.w;
+            const uint32_t hi = w / 2 == 0 ? b.x : w / 2 == 1 ? b.y : w / 2 == 2 ? b.z : b.w;
+            x[i] = __builtin_amdgcn_perm(hi, lo, w & 1 ? 0x07060302u : 0x05040100u);
+        }
+        return __builtin_bit_cast(bf16x8, make_uint4(x[0], x[1], x[2], x[3]));
+    }
+
+    __device__ __forceinline__ void add_values(const float (&p)[4 * J])
+    {
+        if constexpr (BF16) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const float a = p[2 * i], b = p[2 * i + 1];
+                hi[i] = pack_bf16(a, b);
+                lo[i] = pack_bf16(a - __uint_as_float(hi[i] << 16), b - __uint_as_float(hi[i] & 0xFFFF0000u));
+            }
+            const bf16x8 ph = __builtin_bit_cast(bf16x8, make_uint4(hi[0], hi[1], hi[2], hi[3]));
+            const bf16x8 pl = __builtin_bit_cast(bf16x8, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+            for (int c = 0; c < X::VP; c++)
+#pragma unroll
+                for (int w = 0; w < X::VE; w++) {
+                    const bf16x8 col = column(c, w);
+                    o[c][w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(col, ph, o[c][w], 0, 0, 0);
+                    o[c][w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(col, pl, o[c][w], 0, 0, 0);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+#pragma unroll
+                for (int c = 0; c < X::VP; c++) {
+                    const f32x4 a = __builtin_bit_cast(f32x4, v[i][c]);
+#pragma unroll
+                    for (int w = 0; w < X::VE; w++)
+                        o[c][w] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[w], p[i], o[c][w], 0, 0, 0);
+                }
+        }
+    }
+
+    __device__ __forceinline__ void run(int t, int end)
+    {
+        m = LOWEST;
+        l = 0.0f;
+#pragma unroll
+        for (int c = 0; c < X::VP; c++)
+#pragma unroll
+            for (int w = 0; w < X::VE; w++) o[c][w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (t >= end) return;
+        load_pages(t);
+        load_k(t);
+        load_v(t);
+        if (t + NW < end) load_pages(t + NW);
+        for (; t < end; t += NW) {
+            float s[4 * J], top = LOWEST;
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                const f32x4 x = scores(j);
+#pragma unroll
+                for (int i = 0; i < 4; i++) s[4 * j + i] = x[i] * A.scale2;
+            }
+            const bool more = t + NW < end;
+            if (more) load_k(t + NW);
+            if constexpr (SUMS) {
+#pragma unroll
+                for (int j = 0; j < J; j++) {
+                    const int off = (t * X::ROWS + 16 * j + 4 * g) & ((1 << A.shift) - 1);
+                    const size_t to = ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head + n) << A.shift) + off;
+                    if (ok[j] && n < sum_heads)
+                        *reinterpret_cast<float4 *>(A.w.scores + to) =
+                            make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+                }
+            }
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < J; j++)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int r = t * X::ROWS + 16 * j + 4 * g + i;
+                        const bool in = ok[j] && r >= e.first && r < e.s.len;
+                        if (!in) s[4 * j + i] = -INFINITY;
+#pragma unroll
+                        for (int c = 0; c < X::VP; c++) {   // whatever lies there, 0 x NaN among it
+                            v[4 * j + i][c].x = in ? v[4 * j + i][c].x : 0u;
+                            v[4 * j + i][c].y = in ? v[4 * j + i][c].y : 0u;
+                            v[4 * j + i][c].z = in ? v[4 * j + i][c].z : 0u;
+                            v[4 * j + i][c].w = in ? v[4 * j + i][c].w : 0u;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4 * J; i++) top = fmaxf(top, s[i]);
+            const float mn = fmaxf(m, across_rows_max(top)), f = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < 4 * J; i++) {
+                s[i] = __builtin_amdgcn_exp2f(s[i] - mn);
+                l += s[i];
+            }
+#pragma unroll
+            for (int c = 0; c < X::VP; c++)
+#pragma unroll
+                for (int w = 0; w < X::VE; w++) o[c][w] *= f;
+            add_values(s);
+            if (more) {
+                load_v(t + NW);
+                if (t + 2 * NW < end) load_pages(t + 2 * NW);
+            }
+        }
+        l = across_rows_sum(l);
+    }
+
+    int sum_head, sum_heads;   // (with SUMS) the pair's first head within the cache head's, and how many
+};
+
+template <bool BF16, int D, bool SUMS>
+__global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
+{
+    using X = Geo<BF16, D>;
+    constexpr int DC = D < 128 ? D : 128;             // columns joined at a time
+    constexpr int PC = DC / (16 * X::VE);             // in pieces of a lane
+    __shared__ float mj[NW][16], lj[NW][16];
+    __shared__ float oj[NW][16][DC + 4];              // heads 4 banks apart
+    const int t = (int)__builtin_amdgcn_workitem_id_x(), w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int b = (int)__builtin_amdgcn_workgroup_id_x();
+    Share sh{};
+    const bool some = find_share<X::ROWS>(A, b, sh);
+    if (t == 0 && A.w.start) A.w.start[b] = sh.at;
+    if (!some) return;
+    u64 done = sh.x;
+    for_pieces<X::ROWS>(A, sh, [&](int i, const Entry &e, int p, int u, int ue) {
+        const int h = p / A.nt, tile = p - h * A.nt, heads = min(16, A.G - tile * 16), hq = h * A.G + tile * 16;
+        Steps<BF16, D, SUMS> st(A, e, h);
+        st.sum_head = tile * 16;
+        st.sum_heads = heads;
+        st.load_q(i, hq, heads);
+        st.run(e.t0 + u * NW + w, min(e.t0 + ue * NW, e.t1));
+        const bool whole = u == 0 && ue == e.units;
+        const size_t slot = 2 * (size_t)b + (done != sh.x);
+        done += (unsigned)(ue - u);
+        __syncthreads();   // the last piece's sums have been read
+        if (st.g == 0) {
+            mj[w][st.n] = st.m;
+            lj[w][st.n] = st.l;
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < X::VP; c0 += PC) {
+            if (c0) __syncthreads();
+            if (st.n < heads)
+#pragma unroll
+                for (int c = 0; c < PC; c++)
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+#pragma unroll
+                        for (int x = 0; x < X::VE; x += 4)
+                            *reinterpret_cast<float4 *>(
+                                &oj[w][st.n][c * 16 * X::VE + (4 * st.g + r) * X::VE + x]) =
+                                make_float4(st.o[c0 + c][x][r], st.o[c0 + c][x + 1][r], st.o[c0 + c][x + 2][r],
+                                            st.o[c0 + c][x + 3][r]);
+            __syncthreads();
+            for (int x = t; x < heads * DC; x += NT) {
+                const int hd = x / DC, col = x - hd * DC;
+                float M = mj[0][hd], L = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int k = 1; k < NW; k++) M = fmaxf(M, mj[k][hd]);
+#pragma unroll
+                for (int k = 0; k < NW; k++) {
+                    const float f = __builtin_amdgcn_exp2f(mj[k][hd] - M);
+                    L = fmaf(lj[k][hd], f, L);
+                    y = fmaf(oj[k][hd][col], f, y);
+                }
+                const int at = c0 / PC * DC + col;
+                if (whole)
+                    store1<BF16>(A.c.o, (size_t)i * A.c.ldo + (size_t)(hq + hd) * D + at, L > 0.0f ? y / L : 0.0f);
+                else
+                    A.w.part_o[(slot * A.gt + hd) * D + at] = y;
+                if (c0 == 0 && col == 0 && (SUMS || !whole)) {
+                    float *ml = whole ? A.w.whole_ml + ((size_t)i * A.P + p) * 32 : A.w.part_ml + slot * 32;
+                    ml[2 * hd] = M;
+                    ml[2 * hd + 1] = L;
+                }
+            }
+        }
+    });
+}
+
+// A pair whose units begin at unit `begin`: the shares that hold pieces of it, and
+// the place of a share's piece.
+struct Pieces {
+    int b0, b1;
+    bool inside;   // it begins inside share b0
+
+    __device__ __forceinline__ Pieces(const Share &sh, u64 begin, int units)
+    {
+        b0 = share_of(sh.at.all, sh.shares, begin);
+        b1 = share_of(sh.at.all, sh.shares, begin + (unsigned)units - 1);
+        inside = share_begin(sh.at.all, sh.shares, b0) != begin;
+    }
+
+    __device__ __forceinline__ size_t slot(int b) const { return 2 * (size_t)b + (b == b0 && inside); }
+};
+
+// Joins the pieces of the pairs that lie in several shares: workgroup (b, head)
+// that of the pair which share b begins inside of, if no share before it does so
+// too.
+template <bool BF16, int D>
+__device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, int b, int hd)
+{
+    constexpr int COLS = D / 4, PARTS = NT / COLS;   // threads on four columns each
+    __shared__ float f[SHARES + 1], red[2][NW];
+    __shared__ float4 oj[PARTS][COLS];
+    const int t = (int)__builtin_amdgcn_workitem_id_x();
+    if (b == 0 || sh.at.u == 0) return;
+    const u64 begin = sh.x - (unsigned)sh.at.u;
+    const Pieces pc(sh, begin, sh.at.units);
+    if (pc.b0 != b - 1) return;
+    const int h = sh.at.p / A.nt, tile = sh.at.p - h * A.nt;
+    if (hd >= min(16, A.G - tile * 16)) return;
+    const int np = pc.b1 - pc.b0 + 1;
+    float M = LOWEST;
+    for (int k = t; k < np; k += NT) {
+        f[k] = A.w.part_ml[pc.slot(pc.b0 + k) * 32 + 2 * hd];
+        M = fmaxf(M, f[k]);
+    }
+    M = fmaxf(M, __shfl_xor(M, 1));
+    M = fmaxf(M, __shfl_xor(M, 2));
+    M = fmaxf(M, __shfl_xor(M, 4));
+    M = fmaxf(M, __shfl_xor(M, 8));
+    M = across_rows_max(M);
+    if ((t & 63) == 0) red[0][t >> 6] = M;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NW; k++) M = fmaxf(M, red[0][k]);
+    float L = 0.0f;
+    for (int k = t; k < np; k += NT) {
+        f[k] = __builtin_amdgcn_exp2f(f[k] - M);
+        L = fmaf(A.w.part_ml[pc.slot(pc.b0 + k) * 32 + 2 * hd + 1], f[k], L);
+    }
+    L = lanes_sum<64>(L);
+    if ((t & 63) == 0) red[1][t >> 6] = L;
+    __syncthreads();
+    L = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    const int col = t % COLS, part = t / COLS;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int k = part; k < np; k += PARTS) {
+        const float4 x =
+            *reinterpret_cast<const float4 *>(A.w.part_o + (pc.slot(pc.b0 + k) * A.gt + hd) * D + 4 * col);
+        y.x = fmaf(x.x, f[k], y.x);
+        y.y = fmaf(x.y, f[k], y.y);
+        y.z = fmaf(x.z, f[k], y.z);
+        y.w = fmaf(x.w, f[k], y.w);
+    }
+    oj[part][col] = y;
+    __syncthreads();
+    if (t >= COLS) return;
+#pragma unroll
+    for (int k = 1; k < PARTS; k++) {
+        const float4 x = oj[k][t];
+        y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+    }
+    const float r = L > 0.0f ? 1.0f / L : 0.0f;
+    const size_t to = (size_t)sh.at.i * A.c.ldo + (size_t)(h * A.G + tile * 16 + hd) * D + 4 * t;
+    store1<BF16>(A.c.o, to, y.x * r);
+    store1<BF16>(A.c.o, to + 1, y.y * r);
+    store1<BF16>(A.c.o, to + 2, y.z * r);
+    store1<BF16>(A.c.o, to + 3, y.w * r);
+}
+
+// acc of a share's rows, from the stored scores and the pairs' maxima and sums.
+template <int ROWS>
+__device__ __forceinline__ void add_weights(const StepArgs &A, const Share &sh)
+{
+    __shared__ float M[16], R[16], mj[NW][16], lj[NW][16];
+    const int t = (int)__builtin_amdgcn_workitem_id_x(), n = t & 15, k0 = t >> 4;
+    u64 at = sh.x;
+    for_pieces<ROWS>(A, sh, [&](int i, const Entry &e, int p, int u, int ue) {
+        const u64 begin = at - (unsigned)u;
+        at += (unsigned)(ue - u);
+        const int h = p / A.nt;
+        if (p != h * A.nt) return;   // the first pair's share adds up the weights of all
+        const int lo = max(e.first, (e.t0 + u * NW) * ROWS), hi = min(e.s.len, (e.t0 + ue * NW) * ROWS);
+        for (int r0 = lo; r0 < hi; r0 += NT) {
+            const int r = r0 + t;
+            const int page = e.s.table[min(r, e.s.len - 1) >> A.shift], off = r & ((1 << A.shift) - 1);
+            const bool in = r < hi && page >= 0 && page < A.c.kv.n_pages;
+            float w = 0.0f;
+            for (int tile = 0; tile < A.nt; tile++) {
+                const int heads = min(16, A.G - tile * 16);
+                if (A.nt > 1 || r0 == lo) {   // the pair's maximum and sum
+                    const Pieces pc(sh, begin + (u64)tile * (unsigned)e.units, e.units);
+                    float m = LOWEST, l = 0.0f;
+                    if (n < heads) {
+                        if (pc.b0 == pc.b1) {
+                            const float *ml = A.w.whole_ml + ((size_t)i * A.P + p + tile) * 32 + 2 * n;
+                            if (k0 == 0) {
+                                m = ml[0];
+                                l = ml[1];
+                            }
+                        } else
+                            for (int b = pc.b0 + k0; b <= pc.b1; b += 16) {
+                                const float *ml = A.w.part_ml + pc.slot(b) * 32 + 2 * n;
+                                const float mn = fmaxf(m, ml[0]);
+                                l = l * __builtin_amdgcn_exp2f(m - mn) + ml[1] * __builtin_amdgcn_exp2f(ml[0] - mn);
+                                m = mn;
+                            }
+                    }
+                    const float mw = across_rows_max(m);
+                    const float lw = across_rows_sum(l * __builtin_amdgcn_exp2f(m - mw));
+                    __syncthreads();
+                    if ((t & 63) < 16) {
+                        mj[t >> 6][n] = mw;
+                        lj[t >> 6][n] = lw;
+                    }
+                    __syncthreads();
+                    if (t < 16) {
+                        float mm = mj[0][t], ll = 0.0f;
+#pragma unroll
+                        for (int k = 1; k < NW; k++) mm = fmaxf(mm, mj[k][t]);
+#pragma unroll
+                        for (int k = 0; k < NW; k++) ll = fmaf(lj[k][t], __builtin_amdgcn_exp2f(mj[k][t] - mm), ll);
+                        M[t] = mm;
+                        R[t] = ll > 0.0f ? 1.0f / ll : 0.0f;
+                    }
+                    __syncthreads();
+                }
+                if (in) {
+                    const float *s = A.w.scores + ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off;
+                    for (int x = 0; x < heads; x++)
+                        w = fmaf(__builtin_amdgcn_exp2f(s[(size_t)x << A.shift] - M[x]), R[x], w);
+                }
+            }
+            if (in) {
+                float *acc = A.c.kv.acc + sum_at(A.hk, A.shift, page, h, off);
+                *acc = fmaf(A.decay, *acc, w);
+            }
+        }
+    });
+}
+
+template <bool BF16, int D, bool SUMS>
+__global__ __launch_bounds__(NT) void attn_join_kernel(StepArgs A)
+{
+    using X = Geo<BF16, D>;
+    // the sums' workgroups first: they have more to do
+    const int id = (int)__builtin_amdgcn_workgroup_id_x(), sums = SUMS ? A.shares : 0;
+    const bool add = id < sums;
+    const int b = add ? id : (id - sums) / A.gt, hd = add ? 0 : (id - sums) - b * A.gt;
+    Share sh{};
+    sh.at = A.w.start[b];
+    if (sh.at.all == 0) return;
+    sh.bounds(A, b);
+    if constexpr (SUMS)
+        if (add) {
+            add_weights<X::ROWS>(A, sh);
+            return;
+        }
+    join_pieces<BF16, D>(A, sh, b, hd);
+}
+
+size_t up16(size_t x) { return (x + 15) / 16 * 16; }
+
+// How a call is dealt out, and its workspace.
+struct Plan {
+    int G, gt, nt, P, shares;
+    bool join, sums;
+    size_t start, part_ml, part_o, whole_ml, scores, bytes;   // offsets
+
+    Plan(const gdnq_attn_desc &d, const gdnq_kv &kv, int n)
+    {
+        const int rows = d.io_dtype == GDNQ_IO_BF16 ? 32 : 16;
+        G = d.H / d.hk;
+        gt = std::min(G, 16);
+        nt = (G + 15) / 16;
+        P = d.hk * nt;
+        const long long steps = (long long)kv.max_pages * d.page / rows + 2;   // one more at each end of a window
+        const long long units = (steps + NW - 1) / NW;
+        shares = (int)std::min<long long>(SHARES, (long long)n * P * std::min<long long>(units, SHARES));
+        join = units > 1;
+        sums = kv.acc != nullptr;
+        const size_t u = (size_t)shares;
+        start = 0;
+        part_ml = up16(join || sums ? u * sizeof(Start) : 0);
+        part_o = part_ml + (join ? u * 2 * 32 * 4 : 0);
+        whole_ml = part_o + up16(join ? u * 2 * gt * d.d * 4 : 0);
+        scores = whole_ml + (sums ? (size_t)n * P * 32 * 4 : 0);
+        bytes = scores + (sums ? (size_t)kv.n_pages * d.page * d.H * 4 : 0);
+    }
+};
+
 }  // namespace
 
-size_t attn_workspace(const gdnq_attn_desc &, const gdnq_kv &, int) { return 0; }
+size_t attn_workspace(const gdnq_attn_desc &d, const gdnq_kv &kv, int n) { return Plan(d, kv, n).bytes; }
 
 hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStream_t st)
 {
-    const dim3 grid = grid_of((unsigned long long)c.n * d.hk, 256);
-    const AttnArgs A{c, d.H, d.hk, __builtin_ctz((unsigned)d.page), d.window, d.scale * LOG2E, d.acc_decay,
-                     make_divisor((unsigned)d.hk), grid.x};
+    const Plan p(d, c.kv, c.n);
+    char *ws = static_cast<char *>(c.ws);
+    const int es = d.io_dtype == GDNQ_IO_BF16 ? 2 : 4;
+    Space w{nullptr, nullptr, nullptr, nullptr, nullptr};
+    if (p.join || p.sums) w.start = reinterpret_cast<Start *>(ws + p.start);
+    if (p.join) {
+        w.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
+        w.part_o = reinterpret_cast<float *>(ws + p.part_o);
+    }
+    if (p.sums) {
+        w.whole_ml = reinterpret_cast<float *>(ws + p.whole_ml);
+        w.scores = reinterpret_cast<float *>(ws + p.scores);
+    }
+    const StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, __builtin_ctz((unsigned)d.page), d.window, p.shares,
+                     d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es)};
     return with_bool(d.io_dtype == GDNQ_IO_BF16, [&](auto bf) {
-        constexpr bool B = decltype(bf)::value;
-        if (d.d == 64) hipLaunchKernelGGL((attn_simple_kernel<B, 64>), grid, dim3(256), 0, st, A);
-        else if (d.d == 128) hipLaunchKernelGGL((attn_simple_kernel<B, 128>), grid, dim3(256), 0, st, A);
-        else hipLaunchKernelGGL((attn_simple_kernel<B, 256>), grid, dim3(256), 0, st, A);
-        return hipGetLastError();
+        return with_bool(p.sums, [&](auto sm) {
+            auto go = [&](auto dd) {
+                constexpr bool B = decltype(bf)::value, S = decltype(sm)::value;
+                constexpr int D = decltype(dd)::value;
+                hipLaunchKernelGGL((attn_kernel<B, D, S>), dim3((unsigned)p.shares), dim3(NT), 0, st, A);
+                if (p.join || p.sums)
+                    hipLaunchKernelGGL((attn_join_kernel<B, D, S>), dim3((unsigned)p.shares * (p.gt + (S ? 1 : 0))),
+                                       dim3(NT), 0, st, A);
+                return hipGetLastError();
+            };
+            if (d.d == 64) return go(std::integral_constant<int, 64>{});
+            if (d.d == 128) return go(std::integral_constant<int, 128>{});
+            return go(std::integral_constant<int, 256>{});
+        });
     });
 }
 
