@@ -187,7 +187,7 @@ def _step(g, desc=None, kv=None, n=4, ldq=0, ldo=0, size=1 << 40, no_kv=False, *
                                         b["ws"], size, 0))
 
 
-def _evict(g, desc=None, kv=None, n=4, budget=64, sink=4, recent=8, size=1 << 40, no_kv=False, **over):
+def _evict(g, desc=None, kv=None, n=4, budget=96, sink=4, recent=8, size=1 << 40, no_kv=False, **over):
     d = g.AttnDesc(**{"H": 6, "hk": 2, "d": 64, "page": 16, **(desc or {})}).c()
     b = _bufs(["slots", "ws"] + KV, over)
     return _err(g, g.lib.gdnq_kv_evict(d, None if no_kv else _cache(b, kv), budget, sink, recent, b["slots"], n,
@@ -292,7 +292,7 @@ def test_step_refusals(g, kw, code, msg):
     (dict(budget=0), 1, "budget must"),
     (dict(sink=-1), 1, "sink and recent"),
     (dict(recent=-1), 1, "sink and recent"),
-    (dict(sink=60), 1, "sink and recent"),
+    (dict(sink=89), 1, "sink and recent"),
     (dict(acc=None), 1, "kv.acc is NULL"),
     (dict(kvpos=None), 1, "kv.pos is NULL"),
     (dict(kvv=BASE + (2 << 36)), 1, "kv.v overlaps kv.k"),
