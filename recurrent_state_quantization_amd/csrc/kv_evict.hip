@@ -2,14 +2,17 @@
 // (gdnq_kv_evict).
 //
 // One workgroup per entry and head chooses.  The sums become whole numbers of
-// the same order, the protected rows the largest, and stay in registers; four
-// rounds of counting by 8 bits find the largest number that leaves, and how
-// many rows of that number leave (the lower ones).  Then the rows before the
-// budget that leave (holes) and the rows behind it that stay, equally many, are
-// numbered in order by prefix counts; the k-th of these moves into the k-th
-// hole.  Sources lie behind the budget and destinations before it, so the moves
-// are independent: a few of them are made at once, more of them by a second
-// kernel with many workgroups for each head.
+// the same order, the protected rows the largest, and stay in registers.  The
+// range of the others is cut into 1024 parts and the rows in each counted; the
+// part in which the last row to leave lies is cut again, until it leaves as a
+// whole (mostly after two rounds) or holds one number, of which the lower rows
+// leave.  Then the rows before the budget that leave (holes) and the rows behind
+// it that stay, equally many, are numbered in order by prefix counts; the k-th
+// of these moves into the k-th hole.  Sources lie behind the budget and
+// destinations before it, so the moves are independent: a few of them are made
+// at once, more of them by a second kernel with many workgroups for each head.
+// Where one row leaves, as decoding goes on over a full cache, it is the
+// smallest of all, and the last row takes its place.
 #include <algorithm>
 
 #include "attn_launchers.hpp"
@@ -20,10 +23,11 @@ namespace gdnq {
 namespace {
 
 constexpr int FEW = 64;   // moves that the choosing workgroup makes itself
+constexpr unsigned STAYS = 0xFFFFFFFFu;   // the number of protected rows, above all others
 
-// A row's page and its place in it, before and behind a move.
+// A row's numbers before and behind a move.
 struct Move {
-    int from, from_off, to, to_off;
+    int from, to;
 };
 
 struct EvictArgs {
@@ -43,31 +47,44 @@ __device__ __forceinline__ unsigned order_of(float x)
     return (int)u < 0 ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ void move_sums(const EvictArgs &A, int h, const Move &m)
+// Piece j of a row's key and value; with the first, its sum and position.
+__device__ __forceinline__ void move_piece(const EvictArgs &A, const int32_t *table, int h, const Move &m, int j)
 {
-    const size_t from = sum_at(A.hk, A.shift, m.from, h, m.from_off), to = sum_at(A.hk, A.shift, m.to, h, m.to_off);
-    A.c.kv.acc[to] = A.c.kv.acc[from];
-    A.c.kv.pos[to] = A.c.kv.pos[from];
-}
-
-__device__ __forceinline__ void move_piece(const EvictArgs &A, int h, const Move &m, int j)
-{
-    const size_t from = row_at(A.c.kv, m.from, h, m.from_off) + j, to = row_at(A.c.kv, m.to, h, m.to_off) + j;
+    const int mask = (1 << A.shift) - 1, pf = table[m.from >> A.shift], pt = table[m.to >> A.shift];
+    const size_t from = row_at(A.c.kv, pf, h, m.from & mask) + j, to = row_at(A.c.kv, pt, h, m.to & mask) + j;
     uint4 *K = reinterpret_cast<uint4 *>(A.c.kv.k), *V = reinterpret_cast<uint4 *>(A.c.kv.v);
     const uint4 k = K[from], v = V[from];
+    if (j == 0) {
+        const size_t sf = sum_at(A.hk, A.shift, pf, h, m.from & mask), st = sum_at(A.hk, A.shift, pt, h, m.to & mask);
+        A.c.kv.acc[st] = A.c.kv.acc[sf];
+        A.c.kv.pos[st] = A.c.kv.pos[sf];
+    }
     K[to] = k;
     V[to] = v;
 }
 
-// NT threads of K consecutive rows each; more rows than that (MANY) in several
-// rounds, whose numbers are formed again in every pass.
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int lanes_before(int x)
+{
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xF, 0xF, true);    // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xF, 0xF, true);    // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xF, 0xF, true);    // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xF, 0xF, true);    // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xA, 0xF, true);    // row_bcast:15
+    return x + __builtin_amdgcn_update_dpp(0, x, 0x143, 0xC, 0xF, true);   // row_bcast:31
+}
+
+// NT threads of K rows each, four consecutive ones (16 bytes, in one page) of
+// every NT * 4 rows; more rows than NT K (MANY) in several rounds, whose numbers
+// are formed again in every pass.
 template <int NT, int K, bool MANY>
 __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
 {
-    constexpr int NW = NT / 64, COPIES = NW < 4 ? NW : 4;
-    __shared__ int hist[COPIES][256];
-    __shared__ unsigned long long part[NW];
-    __shared__ int chosen[3], top;
+    constexpr int NW = NT / 64, BITS = 10, BINS = 1 << BITS, BT = BINS / NT, Q = K / 4;
+    constexpr int PARTS = Q * NW;      // waves' parts of a round, in the order of their rows
+    static_assert(PARTS <= 128 && NT * K <= 65535, "two parts a lane, counts of 16 bits");
+    __shared__ int hist[BINS], part[PARTS], chosen[3], top, open, last, sum;
+    __shared__ unsigned least, most;
     __shared__ Move few[FEW];
     const EvictCall &c = A.c;
     const unsigned id = block_id(A.nx);
@@ -81,45 +98,51 @@ __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
 
     unsigned key[K];
     int pos[K];
+    // f(k) for the thread's rows k of a round, four at a time, as far as there are any
+    auto each = [&](int round, auto &&f) {
+        const int fours = (n - round * NT * K + 4 * NT - 1) / (4 * NT);
+#pragma unroll
+        for (int q = 0; q < Q; q++)
+            if (q < fours)
+#pragma unroll
+                for (int k = 4 * q; k < 4 * q + 4; k++) f(k);
+    };
+    auto row = [&](int round, int k) { return ((round * Q + k / 4) * NT + t) * 4 + k % 4; };
     // the sums and positions of the thread's rows in a round; false: a page does not exist
     auto load = [&](int round) {
-        const int r0 = (round * NT + t) * K;
         bool all = true;
-#pragma unroll
-        for (int g = 0; g < K; g += 8) {   // eight rows lie in one page
-            const int r = r0 + g;
+        each(round, [&](int g) {
+            if (g % 4) return;
+            const int r = row(round, g);
             int p = r < n ? s.table[r >> A.shift] : 0;
             if (p < 0 || p >= c.kv.n_pages) {
                 all = false;
                 p = 0;
             }
             const size_t at = sum_at(A.hk, A.shift, p, h, r & mask);
-            const uint4 *a = reinterpret_cast<const uint4 *>(c.kv.acc + at);
-            const int4 *q = reinterpret_cast<const int4 *>(c.kv.pos + at);
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            int4 u = make_int4(INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN), v = u;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            int4 u = make_int4(INT32_MIN, INT32_MIN, INT32_MIN, INT32_MIN);
             if (r < n) {
-                x = a[0];
-                y = a[1];
-                u = q[0];
-                v = q[1];
+                x = *reinterpret_cast<const uint4 *>(c.kv.acc + at);
+                u = *reinterpret_cast<const int4 *>(c.kv.pos + at);
             }
             key[g] = x.x; key[g + 1] = x.y; key[g + 2] = x.z; key[g + 3] = x.w;
-            key[g + 4] = y.x; key[g + 5] = y.y; key[g + 6] = y.z; key[g + 7] = y.w;
+            if (r + 3 >= n) {   // rows behind the last: protected (a sink is never below zero)
+                if (r + 1 >= n) u.y = INT32_MIN;
+                if (r + 2 >= n) u.z = INT32_MIN;
+                u.w = INT32_MIN;
+            }
             pos[g] = u.x; pos[g + 1] = u.y; pos[g + 2] = u.z; pos[g + 3] = u.w;
-            pos[g + 4] = v.x; pos[g + 5] = v.y; pos[g + 6] = v.z; pos[g + 7] = v.w;
-        }
+        });
         return all;
     };
-    long long recent = 0;
-    // their numbers; rows behind the last are the largest and come behind the protected ones
+    int newest = INT32_MIN;
+    // the rows' numbers: rows behind the last are among the protected ones, behind them
     auto number = [&](int round) {
-        const int r0 = (round * NT + t) * K;
-#pragma unroll
-        for (int k = 0; k < K; k++) {
-            const bool stay = pos[k] < c.sink || pos[k] > recent || r0 + k >= n;
-            key[k] = stay ? 0xFFFFFFFFu : order_of(__uint_as_float(key[k]));
-        }
+        each(round, [&](int k) {
+            const bool stay = pos[k] < c.sink || (unsigned)newest - (unsigned)pos[k] < (unsigned)c.recent;
+            key[k] = stay ? STAYS : order_of(__uint_as_float(key[k]));
+        });
     };
     auto again = [&](int round) {
         if constexpr (MANY) {
@@ -128,147 +151,190 @@ __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
         }
     };
 
-    if (t == 0) top = INT32_MIN;
-    for (int x = t; x < COPIES * 256; x += NT) (&hist[0][0])[x] = 0;
-    int newest = INT32_MIN;
+    if (t == 0) {
+        top = INT32_MIN;
+        least = STAYS;
+        most = 0;
+        open = 0;
+        last = INT32_MAX;
+    }
+    for (int x = t; x < BINS; x += NT) hist[x] = 0;
     bool bad = false;
     for (int round = 0; round < rounds; round++) {
         bad |= !load(round);
-#pragma unroll
-        for (int k = 0; k < K; k++)
-            if ((round * NT + t) * K + k < n) newest = max(newest, pos[k]);
+        each(round, [&](int k) { newest = max(newest, pos[k]); });
     }
     if (__syncthreads_or(bad)) return;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) newest = max(newest, __shfl_xor(newest, d));
     if (lane == 0) atomicMax(&top, newest);
     __syncthreads();
-    recent = (long long)top - c.recent;
+    newest = top;
     number(0);
 
-    // the number of the last row to leave: `prefix` fills from the top; `need` rows of those with it leave
-    unsigned prefix = 0;
-    int need = n - c.budget, ties = 0;
-    for (int bits = 24; bits >= 0; bits -= 8) {
-        const unsigned above = bits == 24 ? 0u : ~0u << (bits + 8);
+    // the range of the rows that are not protected (hi: one more), and how many these are
+    unsigned lo = STAYS, hi = 0;
+    int free = 0;
+    for (int round = 0; round < rounds; round++) {
+        again(round);
+        each(round, [&](int k) {
+            lo = min(lo, key[k]);
+            hi = max(hi, key[k] + 1);   // 0 of a protected row
+            free += key[k] != STAYS;
+        });
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        lo = min(lo, (unsigned)__shfl_xor((int)lo, d));
+        hi = max(hi, (unsigned)__shfl_xor((int)hi, d));
+        free += __shfl_xor(free, d);
+    }
+    if (lane == 0) {
+        atomicMin(&least, lo);
+        atomicMax(&most, hi);
+        atomicAdd(&open, free);
+    }
+    __syncthreads();
+    lo = least;
+    hi = most - 1;
+    free = open;
+
+    int need = n - c.budget;
+    if (need == 1) {   // the lowest row of the smallest number; the last row takes its place
+        int r = INT32_MAX;
         for (int round = 0; round < rounds; round++) {
             again(round);
-#pragma unroll
-            for (int k = 0; k < K; k++) {
-                const bool in = (key[k] & above) == prefix;
-                const int digit = (int)((key[k] >> bits) & 255u);
-                // sums are alike: lanes of one digit count together
-                const unsigned long long b = __ballot(in);
-                if (b == 0) continue;
-                const int d0 = __builtin_amdgcn_readlane(digit, (int)__ffsll((long long)b) - 1);
-                const unsigned long long same = __ballot(in && digit == d0);
-                if (lane == 0) atomicAdd(&hist[w % COPIES][d0], __popcll(same));
-                if (in && digit != d0) atomicAdd(&hist[w % COPIES][digit], 1);
-            }
+            each(round, [&](int k) {
+                if (key[k] == lo) r = min(r, row(round, k));
+            });
         }
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) r = min(r, __shfl_xor(r, d));
+        if (lane == 0) atomicMin(&last, r);
         __syncthreads();
-        if (w == 0) {   // four digits a lane
-            int cnt[4], sum = 0;
+        r = last;
+        if (r == n - 1) return;
+        if (t < A.pieces) move_piece(A, s.table, h, Move{n - 1, r}, t);
+        return;
+    }
+
+    // the rows below `lo` leave, and `need` of the `ties` rows of that number, the lower ones
+    int ties = n - free;
+    if (need > free) {   // and some of the protected ones
+        need -= free;
+        lo = STAYS;
+    } else {
+        int shift = lo == hi ? 0 : max(0, 32 - BITS - __clz((int)(hi - lo)));
+        for (;;) {
+            for (int round = 0; round < rounds; round++) {
+                again(round);
+                each(round, [&](int k) {
+                    // numbers below `lo`, where there are some, are 2^24 from its other side, and shift is
+                    // at most 12 then
+                    const unsigned d = (key[k] - lo) >> shift;
+                    if (d < BINS && key[k] != STAYS) atomicAdd(&hist[d], 1);
+                });
+            }
+            __syncthreads();
+            int cnt[BT], sum = 0;
 #pragma unroll
-            for (int x = 0; x < 4; x++) {
-                cnt[x] = 0;
-#pragma unroll
-                for (int y = 0; y < COPIES; y++) {
-                    cnt[x] += hist[y][4 * lane + x];
-                    hist[y][4 * lane + x] = 0;
-                }
+            for (int x = 0; x < BT; x++) {
+                cnt[x] = hist[t * BT + x];
+                hist[t * BT + x] = 0;
                 sum += cnt[x];
             }
-            int before = sum;
+            const int in = lanes_before(sum);
+            if (lane == 63) part[w] = in;
+            __syncthreads();
+            int before = in - sum;
 #pragma unroll
-            for (int d = 1; d < 64; d *= 2) {
-                const int y = __shfl_up(before, d);
-                if (lane >= d) before += y;
-            }
-            before -= sum;
+            for (int k = 0; k < NW; k++)
+                if (k < w) before += part[k];
 #pragma unroll
-            for (int x = 0; x < 4; x++) {
+            for (int x = 0; x < BT; x++) {
                 if (need > before && need <= before + cnt[x]) {
-                    chosen[0] = 4 * lane + x;
+                    chosen[0] = t * BT + x;
                     chosen[1] = need - before;
                     chosen[2] = cnt[x];
                 }
                 before += cnt[x];
             }
+            __syncthreads();
+            lo += (unsigned)chosen[0] << shift;
+            need = chosen[1];
+            ties = chosen[2];
+            if (ties == need) {   // all of the part
+                lo += 1u << shift;
+                need = ties = 0;
+                break;
+            }
+            if (shift == 0) break;
+            shift = max(0, shift - BITS);
+            __syncthreads();   // before the counts and the choice of the next round
         }
-        __syncthreads();
-        prefix |= (unsigned)chosen[0] << bits;
-        need = chosen[1];
-        ties = chosen[2];
-        __syncthreads();
     }
 
-    // sums over the lower threads, and over all
-    auto sum_before = [&](unsigned long long x, unsigned long long &all) {
-        unsigned long long in = x;
+    // x[q]: counts (two of 16 bits) of the thread's rows of quarter q of a round, made the counts
+    // of all rows of the round before them; returns those of the whole round
+    auto count_before = [&](unsigned (&x)[Q]) {
+        unsigned in[Q];
 #pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const unsigned long long y = __shfl_up(in, d);
-            if (lane >= d) in += y;
-        }
-        if (lane == 63) part[w] = in;
-        __syncthreads();
-        unsigned long long before = in - x;
-        all = 0;
-#pragma unroll
-        for (int k = 0; k < NW; k++) {
-            if (k < w) before += part[k];
-            all += part[k];
+        for (int q = 0; q < Q; q++) {
+            in[q] = (unsigned)lanes_before((int)x[q]);
+            if (lane == 63) part[q * NW + w] = (int)in[q];
         }
         __syncthreads();
-        return before;
+        if (w == 0) {
+            const int a = 2 * lane < PARTS ? part[2 * lane] : 0, b = 2 * lane + 1 < PARTS ? part[2 * lane + 1] : 0;
+            const int all = lanes_before(a + b);
+            if (2 * lane < PARTS) part[2 * lane] = all - a - b;
+            if (2 * lane + 1 < PARTS) part[2 * lane + 1] = all - b;
+            if (lane == 63) sum = all;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < Q; q++) x[q] = (unsigned)part[q * NW + w] + in[q] - x[q];
+        const unsigned all = (unsigned)sum;
+        __syncthreads();
+        return all;
     };
 
     int tied = 0, moved = 0, kept = 0;
     Move *list = A.moves ? A.moves + (size_t)id * A.most : nullptr;
+    // rows in order: the same numbers on both sides make a move
+    auto note = [&](int x, int r, bool to) {
+        if (x < FEW) (to ? few[x].to : few[x].from) = r;
+        if (list && x < A.most) (to ? list[x].to : list[x].from) = r;
+    };
     for (int round = 0; round < rounds; round++) {
         again(round);
-        const int r0 = (round * NT + t) * K;
-        int tb = 0;
-        unsigned long long all;
+        unsigned before[Q] = {}, flags[Q] = {};
         if (ties > need) {   // some of the equal ones stay: number them
-            int mine = 0;
+            each(round, [&](int k) { before[k / 4] += key[k] == lo && row(round, k) < n; });
+            const int all = (int)count_before(before);
+            each(round, [&](int k) {
+                if (key[k] == lo && row(round, k) < n && tied + (int)before[k / 4]++ < need) key[k] = 0;
+            });
+            tied += all;
 #pragma unroll
-            for (int k = 0; k < K; k++) mine += key[k] == prefix && r0 + k < n;
-            tb = tied + (int)sum_before((unsigned)mine, all);
-            tied += (int)all;
+            for (int q = 0; q < Q; q++) before[q] = 0;
         }
-        unsigned gone = 0, in = 0;   // flags of the thread's rows
-        static_assert(K <= 32, "a flag for each row of a thread");
+        // what is below `lo` leaves now
+        each(round, [&](int k) {
+            const int r = row(round, k);
+            const bool gone = key[k] < lo, hole = gone && r < c.budget, keep = !gone && r >= c.budget && r < n;
+            before[k / 4] += (hole ? 0x10000u : 0u) + (keep ? 1u : 0u);
+            flags[k / 4] |= (hole ? 1u : 0u) << (k % 4) | (keep ? 16u : 0u) << (k % 4);
+        });
+        const unsigned all = count_before(before);
 #pragma unroll
-        for (int k = 0; k < K; k++) {
-            const bool tie = key[k] == prefix && r0 + k < n;
-            if (key[k] < prefix || (tie && (ties <= need || tb < need))) gone |= 1u << k;
-            tb += tie;
-            if (r0 + k < n) in |= 1u << k;
+        for (int q = 0; q < Q; q++) {
+            int hb = moved + (int)(before[q] >> 16), kb = kept + (int)(before[q] & 0xFFFFu);
+            for (unsigned f = flags[q] & 15u; f; f &= f - 1) note(hb++, row(round, 4 * q) + __ffs(f) - 1, true);
+            for (unsigned f = flags[q] >> 4; f; f &= f - 1) note(kb++, row(round, 4 * q) + __ffs(f) - 1, false);
         }
-        const unsigned front = r0 >= c.budget ? 0u : c.budget - r0 >= 32 ? ~0u : (1u << (c.budget - r0)) - 1;
-        const unsigned holes = gone & front, keeps = in & ~gone & ~front;
-        const unsigned long long b =
-            sum_before((unsigned long long)__popc(holes) << 32 | (unsigned)__popc(keeps), all);
-        int hb = moved + (int)(b >> 32), kb = kept + (int)(unsigned)b;
-        moved += (int)(all >> 32);
-        kept += (int)(unsigned)all;
-        // rows in order: the same numbers on both sides make a move
-        auto note = [&](int x, int r, bool to) {
-            if (x >= A.most) return;
-            const int p = s.table[r >> A.shift];
-            if (x < FEW) {
-                (to ? few[x].to : few[x].from) = p;
-                (to ? few[x].to_off : few[x].from_off) = r & mask;
-            }
-            if (list) {
-                (to ? list[x].to : list[x].from) = p;
-                (to ? list[x].to_off : list[x].from_off) = r & mask;
-            }
-        };
-        for (unsigned f = holes; f; f &= f - 1) note(hb++, r0 + __ffs(f) - 1, true);
-        for (unsigned f = keeps; f; f &= f - 1) note(kb++, r0 + __ffs(f) - 1, false);
+        moved += (int)(all >> 16);
+        kept += (int)(all & 0xFFFFu);
     }
     if (moved > FEW) {
         if (t == 0) A.count[id] = moved;
@@ -277,9 +343,8 @@ __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
     __syncthreads();
     for (int x = t; x < moved * A.pieces; x += NT) {
         const int m = x / A.pieces;
-        move_piece(A, h, few[m], x - m * A.pieces);
+        move_piece(A, s.table, h, few[m], x - m * A.pieces);
     }
-    if (t < moved) move_sums(A, h, few[t]);
 }
 
 // The moves of a head, by `split` workgroups.
@@ -288,14 +353,12 @@ __global__ __launch_bounds__(256) void kv_move_kernel(EvictArgs A)
     const unsigned id = block_id(A.nx), pair = div_by(id, A.bySplit), part = id - pair * A.bySplit.d;
     if (pair >= (unsigned)A.c.n * (unsigned)A.hk) return;
     const int t = (int)__builtin_amdgcn_workitem_id_x(), count = A.count[pair];
-    const int h = (int)(pair - div_by(pair, A.byHk) * (unsigned)A.hk);
+    const int i = (int)div_by(pair, A.byHk), h = (int)(pair - (unsigned)i * (unsigned)A.hk);
+    SlotRows s;
+    if (count == 0 || !slot_rows(A.c.kv, A.c.slots, i, A.shift, s)) return;
     const Move *list = A.moves + (size_t)pair * A.most;
     const int rows = 256 / A.pieces, j = t % A.pieces, step = rows * (int)A.bySplit.d;
-    for (int m = (int)part * rows + t / A.pieces; m < count; m += step) {
-        const Move x = list[m];
-        move_piece(A, h, x, j);
-        if (j == 0) move_sums(A, h, x);
-    }
+    for (int m = (int)part * rows + t / A.pieces; m < count; m += step) move_piece(A, s.table, h, list[m], j);
 }
 
 // Moves of a head at most: rows that leave before the budget, rows that stay behind it.
