@@ -38,6 +38,7 @@ namespace {
 constexpr float LOG2E = 1.44269504f, LOWEST = -3.4028234e38f;
 constexpr int NT = 256, NW = NT / 64;
 constexpr int SHARES = 512;   // workgroups at most: two for each compute unit
+constexpr int SUM_ROWS = NT * 4;   // rows of which a workgroup adds up the weights at a time
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -56,17 +57,20 @@ struct Space {
     Start *start;       // [shares], for the second kernel
     float *part_ml;     // [2 shares][16][2]: maximum and sum of a share's first and last piece
     float *part_o;      // [2 shares][gt][D]
-    float *whole_ml;    // [n P][16][2], for the sums of weights
-    float *scores;      // [n_pages][hk][G][page], likewise
+    u64 *before;        // [n]: units of the entries before, for the sums of weights, as are
+    float *whole_ml;    // [n P][16][2]
+    float *scores;      // [n_pages][hk][G][page]
 };
 
 struct StepArgs {
     AttnCall c;
     Space w;
     int H, hk, G, gt, nt, P;   // query heads per cache head, per pair; pairs per cache head, per entry
-    int shift, window, shares;
+    int shift, window, shares, splits;   // splits: workgroups for the sums of an entry and cache head
     float scale2, decay;       // scale log2(e): weights are powers of two
     bool wide_q;
+    Divisor bySplits, byHk;
+    unsigned nx;               // width of the second kernel's grid
 };
 
 template <bool BF16, int D>
@@ -149,6 +153,13 @@ __device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh)
     u64 mine = 0;
     for (int i = lo; i < hi; i++) mine += (unsigned)entry_of<ROWS>(A, i).units;
     const u64 before = sum_before(mine, part, sh.at.all) * (unsigned)A.P;
+    if (b == 0 && A.w.before) {
+        u64 x = before;
+        for (int i = lo; i < hi; i++) {
+            A.w.before[i] = x;
+            x += (u64)(unsigned)entry_of<ROWS>(A, i).units * (unsigned)A.P;
+        }
+    }
     sh.at.all *= (unsigned)A.P;
     mine *= (unsigned)A.P;
     if ((unsigned)b >= min((u64)A.shares, sh.at.all)) {
@@ -217,6 +228,15 @@ __device__ __forceinline__ float across_rows_sum(float x)
     a = b = x;
     swap32(a, b);
     return a + b;
+}
+
+// 16 bytes that are read once: kept out of the caches' way (64 requests to 32768
+// rows 410 -> 366 us, 5.8 -> 6.5 TB/s).
+__device__ __forceinline__ uint4 stream16(const char *p)
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    return make_uint4(x.x, x.y, x.z, x.w);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -296,7 +316,7 @@ struct Steps {
         for (int j = 0; j < J; j++) {
             const char *p = at(A.c.kv.k, there(page_k[j]) ? page_k[j] : 0, t * X::ROWS + 16 * j + n) + g * 16;
 #pragma unroll
-            for (int c = 0; c < X::KP; c++) k[j][c] = *reinterpret_cast<const uint4 *>(p + c * 64);
+            for (int c = 0; c < X::KP; c++) k[j][c] = stream16(p + c * 64);
         }
     }
 
@@ -315,9 +335,9 @@ struct Steps {
 #pragma unroll
                 for (int c = 0; c < X::VP; c++) {
                     if constexpr (X::VE * X::ES == 16)
-                        v[4 * j + i][c] = *reinterpret_cast<const uint4 *>(p + c * 256);
+                        v[4 * j + i][c] = stream16(p + c * 256);
                     else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                        const uint2 x = load_nt8(reinterpret_cast<const int8_t *>(p));
                         v[4 * j + i][c] = make_uint4(x.x, x.y, 0, 0);
                     }
                 }
@@ -620,47 +640,58 @@ __device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, 
     store1<BF16>(A.c.o, to + 3, y.w * r);
 }
 
-// acc of a share's rows, from the stored scores and the pairs' maxima and sums.
+// acc of an entry's rows in a cache head, from the stored scores and the pairs'
+// maxima and sums: four rows (16 bytes, in one page) of a thread, SUM_ROWS at a
+// time by one of `splits` workgroups.
 template <int ROWS>
-__device__ __forceinline__ void add_weights(const StepArgs &A, const Share &sh)
+__device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
 {
     __shared__ float M[16], R[16], mj[NW][16], lj[NW][16];
     const int t = (int)__builtin_amdgcn_workitem_id_x(), n = t & 15, k0 = t >> 4;
-    u64 at = sh.x;
-    for_pieces<ROWS>(A, sh, [&](int i, const Entry &e, int p, int u, int ue) {
-        const u64 begin = at - (unsigned)u;
-        at += (unsigned)(ue - u);
-        const int h = p / A.nt;
-        if (p != h * A.nt) return;   // the first pair's share adds up the weights of all
-        const int lo = max(e.first, (e.t0 + u * NW) * ROWS), hi = min(e.s.len, (e.t0 + ue * NW) * ROWS);
-        for (int r0 = lo; r0 < hi; r0 += NT) {
-            const int r = r0 + t;
-            const int page = e.s.table[min(r, e.s.len - 1) >> A.shift], off = r & ((1 << A.shift) - 1);
-            const bool in = r < hi && page >= 0 && page < A.c.kv.n_pages;
-            float w = 0.0f;
-            for (int tile = 0; tile < A.nt; tile++) {
-                const int heads = min(16, A.G - tile * 16);
-                if (A.nt > 1 || r0 == lo) {   // the pair's maximum and sum
-                    const Pieces pc(sh, begin + (u64)tile * (unsigned)e.units, e.units);
-                    float m = LOWEST, l = 0.0f;
-                    if (n < heads) {
-                        if (pc.b0 == pc.b1) {
-                            const float *ml = A.w.whole_ml + ((size_t)i * A.P + p + tile) * 32 + 2 * n;
-                            if (k0 == 0) {
-                                m = ml[0];
-                                l = ml[1];
-                            }
-                        } else
-                            for (int b = pc.b0 + k0; b <= pc.b1; b += 16) {
-                                const float *ml = A.w.part_ml + pc.slot(b) * 32 + 2 * n;
-                                const float mn = fmaxf(m, ml[0]);
-                                l = l * __builtin_amdgcn_exp2f(m - mn) + ml[1] * __builtin_amdgcn_exp2f(ml[0] - mn);
-                                m = mn;
-                            }
+    const unsigned ih = div_by(id, A.bySplits);
+    const int which = (int)(id - ih * (unsigned)A.splits), i = (int)div_by(ih, A.byHk), h = (int)ih - i * A.hk, p = h * A.nt;
+    Share sh{};
+    sh.at.all = A.w.start[0].all;
+    const u64 before = A.w.before[i];
+    const Entry e = entry_of<ROWS>(A, i);
+    if (e.units == 0) return;
+    sh.bounds(A, 0);
+    const int lo = e.t0 * ROWS, hi = e.s.len;
+    bool known = false;
+    for (int r0 = lo + which * SUM_ROWS; r0 < hi; r0 += A.splits * SUM_ROWS) {
+        const int r = r0 + 4 * t, off = r & ((1 << A.shift) - 1);
+        const int page = r < hi ? e.s.table[r >> A.shift] : -1;
+        const bool in = page >= 0 && page < A.c.kv.n_pages;
+        float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int tile = 0; tile < A.nt; tile++) {
+            const int heads = min(16, A.G - tile * 16);
+            float4 s[16];
+            if (in) {
+                const float *from = A.w.scores + ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off;
+#pragma unroll
+                for (int x = 0; x < 16; x++)
+                    if (x < heads) s[x] = *reinterpret_cast<const float4 *>(from + ((size_t)x << A.shift));
+            }
+            if (A.nt > 1 || !known) {   // the pair's maximum and sum
+                const Pieces pc(sh, before + (u64)(p + tile) * (unsigned)e.units, e.units);
+                __syncthreads();
+                if (pc.b0 == pc.b1) {
+                    if (t < heads) {
+                        const float *ml = A.w.whole_ml + ((size_t)i * A.P + p + tile) * 32 + 2 * t;
+                        M[t] = ml[0];
+                        R[t] = ml[1] > 0.0f ? 1.0f / ml[1] : 0.0f;
                     }
+                } else {
+                    float m = LOWEST, l = 0.0f;
+                    if (n < heads)
+                        for (int b = pc.b0 + k0; b <= pc.b1; b += 16) {
+                            const float *ml = A.w.part_ml + pc.slot(b) * 32 + 2 * n;
+                            const float mn = fmaxf(m, ml[0]);
+                            l = l * __builtin_amdgcn_exp2f(m - mn) + ml[1] * __builtin_amdgcn_exp2f(ml[0] - mn);
+                            m = mn;
+                        }
                     const float mw = across_rows_max(m);
                     const float lw = across_rows_sum(l * __builtin_amdgcn_exp2f(m - mw));
-                    __syncthreads();
                     if ((t & 63) < 16) {
                         mj[t >> 6][n] = mw;
                         lj[t >> 6][n] = lw;
@@ -675,20 +706,33 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, const Share &sh)
                         M[t] = mm;
                         R[t] = ll > 0.0f ? 1.0f / ll : 0.0f;
                     }
-                    __syncthreads();
                 }
-                if (in) {
-                    const float *s = A.w.scores + ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off;
-                    for (int x = 0; x < heads; x++)
-                        w = fmaf(__builtin_amdgcn_exp2f(s[(size_t)x << A.shift] - M[x]), R[x], w);
+                __syncthreads();
+                known = true;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; x++)
+                if (x < heads) {
+                    w[0] = fmaf(__builtin_amdgcn_exp2f(s[x].x - M[x]), R[x], w[0]);
+                    w[1] = fmaf(__builtin_amdgcn_exp2f(s[x].y - M[x]), R[x], w[1]);
+                    w[2] = fmaf(__builtin_amdgcn_exp2f(s[x].z - M[x]), R[x], w[2]);
+                    w[3] = fmaf(__builtin_amdgcn_exp2f(s[x].w - M[x]), R[x], w[3]);
                 }
-            }
-            if (in) {
-                float *acc = A.c.kv.acc + sum_at(A.hk, A.shift, page, h, off);
-                *acc = fmaf(A.decay, *acc, w);
-            }
         }
-    });
+        if (!in) continue;
+        float *acc = A.c.kv.acc + sum_at(A.hk, A.shift, page, h, off);
+        if (r >= e.first && r + 4 <= e.s.len) {
+            float4 a = *reinterpret_cast<const float4 *>(acc);
+            a.x = fmaf(A.decay, a.x, w[0]);
+            a.y = fmaf(A.decay, a.y, w[1]);
+            a.z = fmaf(A.decay, a.z, w[2]);
+            a.w = fmaf(A.decay, a.w, w[3]);
+            *reinterpret_cast<float4 *>(acc) = a;
+        } else
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                if (r + x >= e.first && r + x < e.s.len) acc[x] = fmaf(A.decay, acc[x], w[x]);
+    }
 }
 
 template <bool BF16, int D, bool SUMS>
@@ -696,18 +740,21 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(StepArgs A)
 {
     using X = Geo<BF16, D>;
     // the sums' workgroups first: they have more to do
-    const int id = (int)__builtin_amdgcn_workgroup_id_x(), sums = SUMS ? A.shares : 0;
-    const bool add = id < sums;
-    const int b = add ? id : (id - sums) / A.gt, hd = add ? 0 : (id - sums) - b * A.gt;
+    unsigned id = block_id(A.nx);
+    if constexpr (SUMS) {
+        const unsigned sums = (unsigned)A.c.n * (unsigned)A.hk * (unsigned)A.splits;
+        if (id < sums) {
+            add_weights<X::ROWS>(A, id);
+            return;
+        }
+        id -= sums;
+    }
+    const int b = (int)(id / (unsigned)A.gt), hd = (int)id - b * A.gt;
+    if (b >= A.shares) return;
     Share sh{};
     sh.at = A.w.start[b];
     if (sh.at.all == 0) return;
     sh.bounds(A, b);
-    if constexpr (SUMS)
-        if (add) {
-            add_weights<X::ROWS>(A, sh);
-            return;
-        }
     join_pieces<BF16, D>(A, sh, b, hd);
 }
 
@@ -715,9 +762,9 @@ size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
 // How a call is dealt out, and its workspace.
 struct Plan {
-    int G, gt, nt, P, shares;
+    int G, gt, nt, P, shares, splits;
     bool join, sums;
-    size_t start, part_ml, part_o, whole_ml, scores, bytes;   // offsets
+    size_t start, part_ml, part_o, before, whole_ml, scores, bytes;   // offsets
 
     Plan(const gdnq_attn_desc &d, const gdnq_kv &kv, int n)
     {
@@ -731,11 +778,15 @@ struct Plan {
         shares = (int)std::min<long long>(SHARES, (long long)n * P * std::min<long long>(units, SHARES));
         join = units > 1;
         sums = kv.acc != nullptr;
+        // enough workgroups to fill the compute units, and none without rows
+        const long long parts = ((long long)kv.max_pages * d.page + SUM_ROWS - 1) / SUM_ROWS;
+        splits = (int)std::max(1LL, std::min(parts, 4096 / ((long long)n * d.hk)));
         const size_t u = (size_t)shares;
         start = 0;
         part_ml = up16(join || sums ? u * sizeof(Start) : 0);
         part_o = part_ml + (join ? u * 2 * 32 * 4 : 0);
-        whole_ml = part_o + up16(join ? u * 2 * gt * d.d * 4 : 0);
+        before = part_o + up16(join ? u * 2 * gt * d.d * 4 : 0);
+        whole_ml = before + up16(sums ? (size_t)n * 8 : 0);
         scores = whole_ml + (sums ? (size_t)n * P * 32 * 4 : 0);
         bytes = scores + (sums ? (size_t)kv.n_pages * d.page * d.H * 4 : 0);
     }
@@ -750,18 +801,22 @@ hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStrea
     const Plan p(d, c.kv, c.n);
     char *ws = static_cast<char *>(c.ws);
     const int es = d.io_dtype == GDNQ_IO_BF16 ? 2 : 4;
-    Space w{nullptr, nullptr, nullptr, nullptr, nullptr};
+    Space w{};
     if (p.join || p.sums) w.start = reinterpret_cast<Start *>(ws + p.start);
     if (p.join) {
         w.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
         w.part_o = reinterpret_cast<float *>(ws + p.part_o);
     }
     if (p.sums) {
+        w.before = reinterpret_cast<u64 *>(ws + p.before);
         w.whole_ml = reinterpret_cast<float *>(ws + p.whole_ml);
         w.scores = reinterpret_cast<float *>(ws + p.scores);
     }
+    const dim3 joins = grid_of((unsigned long long)p.shares * p.gt +
+                                   (p.sums ? (unsigned long long)c.n * d.hk * p.splits : 0), NT);
     const StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, __builtin_ctz((unsigned)d.page), d.window, p.shares,
-                     d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es)};
+                     p.splits, d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es),
+                     make_divisor((unsigned)p.splits), make_divisor((unsigned)d.hk), joins.x};
     return with_bool(d.io_dtype == GDNQ_IO_BF16, [&](auto bf) {
         return with_bool(p.sums, [&](auto sm) {
             auto go = [&](auto dd) {
@@ -769,8 +824,7 @@ hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStrea
                 constexpr int D = decltype(dd)::value;
                 hipLaunchKernelGGL((attn_kernel<B, D, S>), dim3((unsigned)p.shares), dim3(NT), 0, st, A);
                 if (p.join || p.sums)
-                    hipLaunchKernelGGL((attn_join_kernel<B, D, S>), dim3((unsigned)p.shares * (p.gt + (S ? 1 : 0))),
-                                       dim3(NT), 0, st, A);
+                    hipLaunchKernelGGL((attn_join_kernel<B, D, S>), joins, dim3(NT), 0, st, A);
                 return hipGetLastError();
             };
             if (d.d == 64) return go(std::integral_constant<int, 64>{});
