@@ -259,7 +259,8 @@ struct Steps {
     uint4 v[J * 4][X::VP];       // row 16 j + 4 g + i at 4 j + i
     f32x4 o[X::VP][X::VE];
     float m, l;
-    int page_k[J], page_v[J];    // of the step loaded next
+    int page_k[J], page_v[J];    // of the step loaded next,
+    int then_k[J], then_v[J];    // and of the one after it
     bool edge;                   // the loaded step has rows that do not count,
     bool ok[J];                  // or whose page does not exist (of this lane's rows of V and scores)
     int at_v[J];                 // (with SUMS) their pages
@@ -299,12 +300,12 @@ struct Steps {
     // a row's page; rows behind the last take its page
     __device__ __forceinline__ int page_of(int r) const { return e.s.table[min(r, e.s.len - 1) >> A.shift]; }
 
-    __device__ __forceinline__ void load_pages(int t)
+    __device__ __forceinline__ void load_pages(int t, int (&k)[J], int (&v)[J]) const
     {
 #pragma unroll
         for (int j = 0; j < J; j++) {
-            page_k[j] = page_of(t * X::ROWS + 16 * j + n);
-            page_v[j] = page_of(t * X::ROWS + 16 * j + 4 * g);
+            k[j] = page_of(t * X::ROWS + 16 * j + n);
+            v[j] = page_of(t * X::ROWS + 16 * j + 4 * g);
         }
     }
 
@@ -410,6 +411,80 @@ struct Steps {
         }
     }
 
+    // Step t, which is loaded; with MORE the next is loaded meanwhile.  Loads return in order, so
+    // a wait for one is a wait for those before it: the pages come before the rows, and no
+    // condition stands around either (a wait would be one for all of them then).
+    template <bool MORE>
+    __device__ __forceinline__ void step(int t)
+    {
+        float s[4 * J], top = LOWEST;
+        if constexpr (MORE) load_pages(t + 2 * NW, then_k, then_v);
+#pragma unroll
+        for (int j = 0; j < J; j++) {
+            const f32x4 x = scores(j);
+#pragma unroll
+            for (int i = 0; i < 4; i++) s[4 * j + i] = x[i] * A.scale2;
+        }
+        if constexpr (MORE) load_k(t + NW);
+        float4 raw[J];
+        size_t to[J];
+        bool put[J];
+        if constexpr (SUMS) {
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                raw[j] = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+                const int off = (t * X::ROWS + 16 * j + 4 * g) & ((1 << A.shift) - 1);
+                to[j] = ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head + n) << A.shift) + off;
+                put[j] = ok[j] && n < sum_heads;
+            }
+        }
+        if (edge) {
+#pragma unroll
+            for (int j = 0; j < J; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int r = t * X::ROWS + 16 * j + 4 * g + i;
+                    const bool in = ok[j] && r >= e.first && r < e.s.len;
+                    s[4 * j + i] = in ? s[4 * j + i] : -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < X::VP; c++) {   // whatever lies there, 0 x NaN among it
+                        v[4 * j + i][c].x = in ? v[4 * j + i][c].x : 0u;
+                        v[4 * j + i][c].y = in ? v[4 * j + i][c].y : 0u;
+                        v[4 * j + i][c].z = in ? v[4 * j + i][c].z : 0u;
+                        v[4 * j + i][c].w = in ? v[4 * j + i][c].w : 0u;
+                    }
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4 * J; i++) top = fmaxf(top, s[i]);
+        const float mn = fmaxf(m, across_rows_max(top)), f = __builtin_amdgcn_exp2f(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < 4 * J; i++) {
+            s[i] = __builtin_amdgcn_exp2f(s[i] - mn);
+            l += s[i];
+        }
+#pragma unroll
+        for (int c = 0; c < X::VP; c++)
+#pragma unroll
+            for (int w = 0; w < X::VE; w++) o[c][w] *= f;
+        add_values(s);
+        if constexpr (MORE) {
+            load_v(t + NW);
+#pragma unroll
+            for (int j = 0; j < J; j++) {
+                page_k[j] = then_k[j];
+                page_v[j] = then_v[j];
+            }
+        }
+        if constexpr (SUMS) {   // behind the loads: a wait for these is none for the stores
+#pragma unroll
+            for (int j = 0; j < J; j++)
+                if (put[j]) *reinterpret_cast<float4 *>(A.w.scores + to[j]) = raw[j];
+        }
+    }
+
     __device__ __forceinline__ void run(int t, int end)
     {
         m = LOWEST;
@@ -419,67 +494,17 @@ struct Steps {
 #pragma unroll
             for (int w = 0; w < X::VE; w++) o[c][w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (t >= end) return;
-        load_pages(t);
+        load_pages(t, page_k, page_v);
+        load_pages(t + NW, then_k, then_v);
         load_k(t);
         load_v(t);
-        if (t + NW < end) load_pages(t + NW);
-        for (; t < end; t += NW) {
-            float s[4 * J], top = LOWEST;
 #pragma unroll
-            for (int j = 0; j < J; j++) {
-                const f32x4 x = scores(j);
-#pragma unroll
-                for (int i = 0; i < 4; i++) s[4 * j + i] = x[i] * A.scale2;
-            }
-            const bool more = t + NW < end;
-            if (more) load_k(t + NW);
-            if constexpr (SUMS) {
-#pragma unroll
-                for (int j = 0; j < J; j++) {
-                    const int off = (t * X::ROWS + 16 * j + 4 * g) & ((1 << A.shift) - 1);
-                    const size_t to = ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head + n) << A.shift) + off;
-                    if (ok[j] && n < sum_heads)
-                        *reinterpret_cast<float4 *>(A.w.scores + to) =
-                            make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
-                }
-            }
-            if (edge) {
-#pragma unroll
-                for (int j = 0; j < J; j++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int r = t * X::ROWS + 16 * j + 4 * g + i;
-                        const bool in = ok[j] && r >= e.first && r < e.s.len;
-                        if (!in) s[4 * j + i] = -INFINITY;
-#pragma unroll
-                        for (int c = 0; c < X::VP; c++) {   // whatever lies there, 0 x NaN among it
-                            v[4 * j + i][c].x = in ? v[4 * j + i][c].x : 0u;
-                            v[4 * j + i][c].y = in ? v[4 * j + i][c].y : 0u;
-                            v[4 * j + i][c].z = in ? v[4 * j + i][c].z : 0u;
-                            v[4 * j + i][c].w = in ? v[4 * j + i][c].w : 0u;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < 4 * J; i++) top = fmaxf(top, s[i]);
-            const float mn = fmaxf(m, across_rows_max(top)), f = __builtin_amdgcn_exp2f(m - mn);
-            m = mn;
-            l *= f;
-#pragma unroll
-            for (int i = 0; i < 4 * J; i++) {
-                s[i] = __builtin_amdgcn_exp2f(s[i] - mn);
-                l += s[i];
-            }
-#pragma unroll
-            for (int c = 0; c < X::VP; c++)
-#pragma unroll
-                for (int w = 0; w < X::VE; w++) o[c][w] *= f;
-            add_values(s);
-            if (more) {
-                load_v(t + NW);
-                if (t + 2 * NW < end) load_pages(t + 2 * NW);
-            }
+        for (int j = 0; j < J; j++) {
+            page_k[j] = then_k[j];
+            page_v[j] = then_v[j];
         }
+        for (; t + NW < end; t += NW) step<true>(t);
+        step<false>(t);
         l = across_rows_sum(l);
     }
 
