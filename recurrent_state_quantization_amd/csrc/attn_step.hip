@@ -59,18 +59,20 @@ struct Space {
     float *part_o;      // [2 shares][gt][D]
     u64 *before;        // [n]: units of the entries before, for the sums of weights, as are
     float *whole_ml;    // [n P][16][2]
-    float *scores;      // [n_pages][hk][G][page]
+    float *scores;      // [n_pages][hk][G][page], and four more
+    size_t spare;       // where these are, for rows on no page
 };
 
 struct StepArgs {
     AttnCall c;
     Space w;
     int H, hk, G, gt, nt, P;   // query heads per cache head, per pair; pairs per cache head, per entry
-    int shift, window, shares, splits;   // splits: workgroups for the sums of an entry and cache head
+    int shift, window;
+    int shares, splits;        // 0: a wave for each pair; workgroups for the sums of an entry and cache head
     float scale2, decay;       // scale log2(e): weights are powers of two
-    bool wide_q;
-    Divisor bySplits, byHk;
-    unsigned nx;               // width of the second kernel's grid
+    bool wide_q, wide_o;
+    Divisor bySplits, byHk, byP;
+    unsigned nx;               // width of the grid, where it is not the shares
 };
 
 template <bool BF16, int D>
@@ -91,10 +93,10 @@ struct Entry {
 };
 
 template <int ROWS>
-__device__ __forceinline__ Entry entry_of(const StepArgs &A, int i)
+__device__ __forceinline__ Entry entry_of(const StepArgs &A, const SlotRows &s)
 {
     Entry e{};
-    if (!slot_rows(A.c.kv, A.c.slots, i, A.shift, e.s)) return e;
+    e.s = s;
     e.first = A.window ? max(0, e.s.len - A.window) : 0;
     e.t0 = e.first / ROWS;
     e.t1 = (e.s.len + ROWS - 1) / ROWS;
@@ -102,9 +104,25 @@ __device__ __forceinline__ Entry entry_of(const StepArgs &A, int i)
     return e;
 }
 
-// First unit of share b of `shares` that divide `all` units; the share that holds unit x.
-__device__ __forceinline__ u64 share_begin(u64 all, int shares, int b) { return all * (unsigned)b / (unsigned)shares; }
-__device__ __forceinline__ int share_of(u64 all, int shares, u64 x) { return (int)(((x + 1) * (unsigned)shares - 1) / all); }
+template <int ROWS>
+__device__ __forceinline__ Entry entry_of(const StepArgs &A, int i)
+{
+    SlotRows s;
+    return slot_rows(A.c.kv, A.c.slots, i, A.shift, s) ? entry_of<ROWS>(A, s) : Entry{};
+}
+
+// The shares of `all` units: one unit each, or SHARES of them.  (A call has fewer
+// workgroups than SHARES only where its units cannot be more than these.)
+__device__ __forceinline__ int shares_of(u64 all) { return (int)min((u64)SHARES, all); }
+// First unit of share b; the share that holds unit x.
+__device__ __forceinline__ u64 share_begin(u64 all, int b)
+{
+    return all <= SHARES ? (u64)(unsigned)b : all * (unsigned)b / SHARES;
+}
+__device__ __forceinline__ int share_of(u64 all, u64 x)
+{
+    return all <= SHARES ? (int)x : (int)(((x + 1) * SHARES - 1) / all);
+}
 
 // Sum over the lower threads, and over all, of the workgroup.
 __device__ __forceinline__ u64 sum_before(u64 x, u64 *part, u64 &all)
@@ -128,26 +146,25 @@ __device__ __forceinline__ u64 sum_before(u64 x, u64 *part, u64 &all)
     return before;
 }
 
-// The units [x, end) of one of `shares` shares, and where it begins.
+// The units [x, end) of a share, and where it begins.
 struct Share {
     u64 x, end;
-    int shares;
     Start at;
 
-    __device__ __forceinline__ void bounds(const StepArgs &A, int b)
+    __device__ __forceinline__ void bounds(int b)
     {
-        shares = (int)min((u64)A.shares, at.all);
-        x = share_begin(at.all, shares, b);
-        end = share_begin(at.all, shares, b + 1);
+        x = share_begin(at.all, b);
+        end = share_begin(at.all, b + 1);
     }
 };
 
-// Workgroup b's share; false: none.
+// Workgroup b's share and the rows of its first entry; false: none.
 template <int ROWS>
-__device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh)
+__device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh, Entry &e)
 {
     __shared__ u64 part[NW];
     __shared__ int at[4];
+    __shared__ SlotRows rows;
     const int t = (int)__builtin_amdgcn_workitem_id_x();
     const int per = (A.c.n + NT - 1) / NT, lo = min(t * per, A.c.n), hi = min(lo + per, A.c.n);
     u64 mine = 0;
@@ -162,41 +179,42 @@ __device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh)
     }
     sh.at.all *= (unsigned)A.P;
     mine *= (unsigned)A.P;
-    if ((unsigned)b >= min((u64)A.shares, sh.at.all)) {
+    if (b >= shares_of(sh.at.all)) {
         sh.at.all = 0;
         return false;
     }
-    sh.bounds(A, b);
+    sh.bounds(b);
     if (sh.x >= before && sh.x < before + mine) {
         int i = lo;
         u64 x = sh.x - before;
-        unsigned units;
+        Entry f;
         for (;; i++) {
-            units = (unsigned)entry_of<ROWS>(A, i).units;
-            if (x < (u64)units * (unsigned)A.P) break;
-            x -= (u64)units * (unsigned)A.P;
+            f = entry_of<ROWS>(A, i);
+            if (x < (u64)(unsigned)f.units * (unsigned)A.P) break;
+            x -= (u64)(unsigned)f.units * (unsigned)A.P;
         }
-        const int p = (int)(x / units);
+        const int p = (int)(x / (unsigned)f.units);
         at[0] = i;
         at[1] = p;
-        at[2] = (int)(x - (u64)p * units);
-        at[3] = (int)units;
+        at[2] = (int)(x - (u64)p * (unsigned)f.units);
+        at[3] = f.units;
+        rows = f.s;
     }
     __syncthreads();
     sh.at.i = __builtin_amdgcn_readfirstlane(at[0]);
     sh.at.p = __builtin_amdgcn_readfirstlane(at[1]);
     sh.at.u = __builtin_amdgcn_readfirstlane(at[2]);
     sh.at.units = __builtin_amdgcn_readfirstlane(at[3]);
+    e = entry_of<ROWS>(A, rows);
     return true;
 }
 
 // Every piece of the share: f(entry number, entry, pair, first and last unit).
 template <int ROWS, class F>
-__device__ __forceinline__ void for_pieces(const StepArgs &A, const Share &sh, F &&f)
+__device__ __forceinline__ void for_pieces(const StepArgs &A, const Share &sh, Entry e, F &&f)
 {
     u64 x = sh.x;
     int i = sh.at.i, p = sh.at.p, u = sh.at.u;
-    Entry e = entry_of<ROWS>(A, i);
     while (x < sh.end) {
         const int ue = (int)min((u64)e.units, u + (sh.end - x));
         f(i, e, p, u, ue);
@@ -245,8 +263,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, (bf16x2{(__bf16)a, (__bf16)b}));
 }
 
-// One wave's steps over a piece.  Lane = (head or row or column n = lane & 15, group g = lane >> 4).
-template <bool BF16, int D, bool SUMS>
+// One wave's steps over a piece, STRIDE apart.  Lane = (head or row or column n = lane & 15, group g = lane >> 4).
+template <bool BF16, int D, bool SUMS, int STRIDE>
 struct Steps {
     using X = Geo<BF16, D>;
     static constexpr int J = X::J;
@@ -283,16 +301,13 @@ struct Steps {
     {
 #pragma unroll
         for (int c = 0; c < X::KP; c++) {
-            q[c] = make_uint4(0, 0, 0, 0);
-            if (n < heads) {
-                const size_t off = (size_t)i * A.c.ldq + (size_t)(hq + n) * D + c * 4 * X::E + g * X::E;
-                if (A.wide_q) q[c] = Pack<BF16, X::E>::load(A.c.q, off);
-                else {
-                    float x[X::E];
+            const size_t off = (size_t)i * A.c.ldq + (size_t)(hq + n % heads) * D + c * 4 * X::E + g * X::E;
+            if (A.wide_q) q[c] = Pack<BF16, X::E>::load(A.c.q, off);
+            else {
+                float x[X::E];
 #pragma unroll
-                    for (int w = 0; w < X::E; w++) x[w] = load1<BF16>(A.c.q, off + w);
-                    q[c] = Pack<BF16, X::E>::narrow(x);
-                }
+                for (int w = 0; w < X::E; w++) x[w] = load1<BF16>(A.c.q, off + w);
+                q[c] = Pack<BF16, X::E>::narrow(x);
             }
         }
     }
@@ -418,24 +433,22 @@ struct Steps {
     __device__ __forceinline__ void step(int t)
     {
         float s[4 * J], top = LOWEST;
-        if constexpr (MORE) load_pages(t + 2 * NW, then_k, then_v);
+        if constexpr (MORE) load_pages(t + 2 * STRIDE, then_k, then_v);
 #pragma unroll
         for (int j = 0; j < J; j++) {
             const f32x4 x = scores(j);
 #pragma unroll
             for (int i = 0; i < 4; i++) s[4 * j + i] = x[i] * A.scale2;
         }
-        if constexpr (MORE) load_k(t + NW);
+        if constexpr (MORE) load_k(t + STRIDE);
         float4 raw[J];
         size_t to[J];
-        bool put[J];
         if constexpr (SUMS) {
 #pragma unroll
             for (int j = 0; j < J; j++) {
                 raw[j] = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
                 const int off = (t * X::ROWS + 16 * j + 4 * g) & ((1 << A.shift) - 1);
-                to[j] = ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head + n) << A.shift) + off;
-                put[j] = ok[j] && n < sum_heads;
+                to[j] = ok[j] ? ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head) << A.shift) + off : A.w.spare;
             }
         }
         if (edge) {
@@ -471,7 +484,7 @@ struct Steps {
             for (int w = 0; w < X::VE; w++) o[c][w] *= f;
         add_values(s);
         if constexpr (MORE) {
-            load_v(t + NW);
+            load_v(t + STRIDE);
 #pragma unroll
             for (int j = 0; j < J; j++) {
                 page_k[j] = then_k[j];
@@ -480,8 +493,7 @@ struct Steps {
         }
         if constexpr (SUMS) {   // behind the loads: a wait for these is none for the stores
 #pragma unroll
-            for (int j = 0; j < J; j++)
-                if (put[j]) *reinterpret_cast<float4 *>(A.w.scores + to[j]) = raw[j];
+            for (int j = 0; j < J; j++) *reinterpret_cast<float4 *>(A.w.scores + to[j]) = raw[j];
         }
     }
 
@@ -495,7 +507,7 @@ struct Steps {
             for (int w = 0; w < X::VE; w++) o[c][w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (t >= end) return;
         load_pages(t, page_k, page_v);
-        load_pages(t + NW, then_k, then_v);
+        load_pages(t + STRIDE, then_k, then_v);
         load_k(t);
         load_v(t);
 #pragma unroll
@@ -503,12 +515,12 @@ struct Steps {
             page_k[j] = then_k[j];
             page_v[j] = then_v[j];
         }
-        for (; t + NW < end; t += NW) step<true>(t);
+        for (; t + STRIDE < end; t += STRIDE) step<true>(t);
         step<false>(t);
         l = across_rows_sum(l);
     }
 
-    int sum_head, sum_heads;   // (with SUMS) the pair's first head within the cache head's, and how many
+    int sum_head;   // (with SUMS) the lane's head within the cache head's
 };
 
 template <bool BF16, int D, bool SUMS>
@@ -522,15 +534,15 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
     const int t = (int)__builtin_amdgcn_workitem_id_x(), w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int b = (int)__builtin_amdgcn_workgroup_id_x();
     Share sh{};
-    const bool some = find_share<X::ROWS>(A, b, sh);
+    Entry first;
+    const bool some = find_share<X::ROWS>(A, b, sh, first);
     if (t == 0 && A.w.start) A.w.start[b] = sh.at;
     if (!some) return;
     u64 done = sh.x;
-    for_pieces<X::ROWS>(A, sh, [&](int i, const Entry &e, int p, int u, int ue) {
+    for_pieces<X::ROWS>(A, sh, first, [&](int i, const Entry &e, int p, int u, int ue) {
         const int h = p / A.nt, tile = p - h * A.nt, heads = min(16, A.G - tile * 16), hq = h * A.G + tile * 16;
-        Steps<BF16, D, SUMS> st(A, e, h);
-        st.sum_head = tile * 16;
-        st.sum_heads = heads;
+        Steps<BF16, D, SUMS, NW> st(A, e, h);
+        st.sum_head = tile * 16 + st.n % heads;
         st.load_q(i, hq, heads);
         st.run(e.t0 + u * NW + w, min(e.t0 + ue * NW, e.t1));
         const bool whole = u == 0 && ue == e.units;
@@ -582,17 +594,60 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
     });
 }
 
+// Short caches: a wave for each pair of an entry, without shares, workspace or
+// join.
+template <bool BF16, int D, bool SUMS>
+__global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_short_kernel(StepArgs A)
+{
+    using X = Geo<BF16, D>;
+    const int w = __builtin_amdgcn_readfirstlane((int)__builtin_amdgcn_workitem_id_x() >> 6);
+    const unsigned id = block_id(A.nx) * NW + (unsigned)w, i = div_by(id, A.byP), p = id - i * (unsigned)A.P;
+    if (i >= (unsigned)A.c.n) return;
+    const Entry e = entry_of<X::ROWS>(A, (int)i);
+    if (e.units == 0) return;
+    const int h = (int)p / A.nt, tile = (int)p - h * A.nt, heads = min(16, A.G - tile * 16), hq = h * A.G + tile * 16;
+    Steps<BF16, D, SUMS, 1> st(A, e, h);
+    st.sum_head = tile * 16 + st.n % heads;
+    st.load_q((int)i, hq, heads);
+    st.run(e.t0, e.t1);
+    if (st.n >= heads) return;
+    if (SUMS && st.g == 0) {
+        float *ml = A.w.whole_ml + (size_t)id * 32 + 2 * st.n;
+        ml[0] = st.m;
+        ml[1] = st.l;
+    }
+    const float f = st.l > 0.0f ? 1.0f / st.l : 0.0f;
+#pragma unroll
+    for (int c = 0; c < X::VP; c++)
+#pragma unroll
+        for (int r = 0; r < 4; r++) {
+            const size_t to = (size_t)i * A.c.ldo + (size_t)(hq + st.n) * D + (c * 16 + 4 * st.g + r) * X::VE;
+            float y[X::VE];
+#pragma unroll
+            for (int x = 0; x < X::VE; x++) y[x] = st.o[c][x][r] * f;
+            if constexpr (X::VE == X::E) {
+                if (A.wide_o) {
+                    store_vec<BF16, X::E>(A.c.o, to, y);
+                    continue;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < X::VE; x++) store1<BF16>(A.c.o, to + x, y[x]);
+        }
+}
+
 // A pair whose units begin at unit `begin`: the shares that hold pieces of it, and
 // the place of a share's piece.
 struct Pieces {
     int b0, b1;
     bool inside;   // it begins inside share b0
 
-    __device__ __forceinline__ Pieces(const Share &sh, u64 begin, int units)
+    __device__ __forceinline__ Pieces(int f, int l, bool in) : b0(f), b1(l), inside(in) {}
+    __device__ __forceinline__ Pieces(u64 all, u64 begin, int units)
     {
-        b0 = share_of(sh.at.all, sh.shares, begin);
-        b1 = share_of(sh.at.all, sh.shares, begin + (unsigned)units - 1);
-        inside = share_begin(sh.at.all, sh.shares, b0) != begin;
+        b0 = share_of(all, begin);
+        b1 = share_of(all, begin + (unsigned)units - 1);
+        inside = share_begin(all, b0) != begin;
     }
 
     __device__ __forceinline__ size_t slot(int b) const { return 2 * (size_t)b + (b == b0 && inside); }
@@ -610,7 +665,7 @@ __device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, 
     const int t = (int)__builtin_amdgcn_workitem_id_x();
     if (b == 0 || sh.at.u == 0) return;
     const u64 begin = sh.x - (unsigned)sh.at.u;
-    const Pieces pc(sh, begin, sh.at.units);
+    const Pieces pc(sh.at.all, begin, sh.at.units);
     if (pc.b0 != b - 1) return;
     const int h = sh.at.p / A.nt, tile = sh.at.p - h * A.nt;
     if (hd >= min(16, A.G - tile * 16)) return;
@@ -675,14 +730,11 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
     const int t = (int)__builtin_amdgcn_workitem_id_x(), n = t & 15, k0 = t >> 4;
     const unsigned ih = div_by(id, A.bySplits);
     const int which = (int)(id - ih * (unsigned)A.splits), i = (int)div_by(ih, A.byHk), h = (int)ih - i * A.hk, p = h * A.nt;
-    Share sh{};
-    sh.at.all = A.w.start[0].all;
-    const u64 before = A.w.before[i];
+    const u64 all = A.shares ? A.w.start[0].all : 0, before = A.shares ? A.w.before[i] : 0;
     const Entry e = entry_of<ROWS>(A, i);
     if (e.units == 0) return;
-    sh.bounds(A, 0);
     const int lo = e.t0 * ROWS, hi = e.s.len;
-    bool known = false;
+    bool known = false;   // M and R are the pair's
     for (int r0 = lo + which * SUM_ROWS; r0 < hi; r0 += A.splits * SUM_ROWS) {
         const int r = r0 + 4 * t, off = r & ((1 << A.shift) - 1);
         const int page = r < hi ? e.s.table[r >> A.shift] : -1;
@@ -690,15 +742,19 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
         float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int tile = 0; tile < A.nt; tile++) {
             const int heads = min(16, A.G - tile * 16);
-            float4 s[16];
-            if (in) {
-                const float *from = A.w.scores + ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off;
+            // eight heads at a time: of the first ones before the maximum and the sum are known
+            const float *from =
+                A.w.scores + (in ? ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off : 0);
+            float4 s[8];
+            auto load = [&](int x0) {
 #pragma unroll
-                for (int x = 0; x < 16; x++)
-                    if (x < heads) s[x] = *reinterpret_cast<const float4 *>(from + ((size_t)x << A.shift));
-            }
+                for (int x = 0; x < 8; x++)
+                    if (x0 + x < heads && in) s[x] = *reinterpret_cast<const float4 *>(from + ((size_t)(x0 + x) << A.shift));
+            };
+            load(0);
             if (A.nt > 1 || !known) {   // the pair's maximum and sum
-                const Pieces pc(sh, before + (u64)(p + tile) * (unsigned)e.units, e.units);
+                Pieces pc{0, 0, false};
+                if (A.shares) pc = Pieces(all, before + (u64)(p + tile) * (unsigned)e.units, e.units);
                 __syncthreads();
                 if (pc.b0 == pc.b1) {
                     if (t < heads) {
@@ -735,14 +791,18 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
                 __syncthreads();
                 known = true;
             }
+            for (int x0 = 0; x0 < heads; x0 += 8) {
+                if (x0) load(x0);
 #pragma unroll
-            for (int x = 0; x < 16; x++)
-                if (x < heads) {
-                    w[0] = fmaf(__builtin_amdgcn_exp2f(s[x].x - M[x]), R[x], w[0]);
-                    w[1] = fmaf(__builtin_amdgcn_exp2f(s[x].y - M[x]), R[x], w[1]);
-                    w[2] = fmaf(__builtin_amdgcn_exp2f(s[x].z - M[x]), R[x], w[2]);
-                    w[3] = fmaf(__builtin_amdgcn_exp2f(s[x].w - M[x]), R[x], w[3]);
-                }
+                for (int x = 0; x < 8; x++)
+                    if (x0 + x < heads) {
+                        const float m = M[x0 + x], f = R[x0 + x];
+                        w[0] = fmaf(__builtin_amdgcn_exp2f(s[x].x - m), f, w[0]);
+                        w[1] = fmaf(__builtin_amdgcn_exp2f(s[x].y - m), f, w[1]);
+                        w[2] = fmaf(__builtin_amdgcn_exp2f(s[x].z - m), f, w[2]);
+                        w[3] = fmaf(__builtin_amdgcn_exp2f(s[x].w - m), f, w[3]);
+                    }
+            }
         }
         if (!in) continue;
         float *acc = A.c.kv.acc + sum_at(A.hk, A.shift, page, h, off);
@@ -779,7 +839,7 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(StepArgs A)
     Share sh{};
     sh.at = A.w.start[b];
     if (sh.at.all == 0) return;
-    sh.bounds(A, b);
+    sh.bounds(b);
     join_pieces<BF16, D>(A, sh, b, hd);
 }
 
@@ -788,7 +848,8 @@ size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 // How a call is dealt out, and its workspace.
 struct Plan {
     int G, gt, nt, P, shares, splits;
-    bool join, sums;
+    bool brief, join, sums;   // brief: the kernel of short caches (the workspace has room for shares
+                              // all the same: it does not shrink with more entries)
     size_t start, part_ml, part_o, before, whole_ml, scores, bytes;   // offsets
 
     Plan(const gdnq_attn_desc &d, const gdnq_kv &kv, int n)
@@ -803,6 +864,11 @@ struct Plan {
         shares = (int)std::min<long long>(SHARES, (long long)n * P * std::min<long long>(units, SHARES));
         join = units > 1;
         sums = kv.acc != nullptr;
+        // A wave for each pair, or shares.  8 heads of 128 in bf16, us, waves and shares: one entry of
+        // 128 rows 8.9 and 8.8, of 256 14.5 and 10.4; 32 entries to 256 16.3 and 14.1; 128 to 128 11.7
+        // and 17.2, to 256 19.6 and 27.5, to 512 35 and 41, to 1024 66 and 62; 2000 to 64 80 and 132,
+        // to 512 409 and 480.
+        brief = steps - 2 <= 4 || (steps - 2 <= 16 && (long long)n * P >= 1024);
         // enough workgroups to fill the compute units, and none without rows
         const long long parts = ((long long)kv.max_pages * d.page + SUM_ROWS - 1) / SUM_ROWS;
         splits = (int)std::max(1LL, std::min(parts, 4096 / ((long long)n * d.hk)));
@@ -813,7 +879,7 @@ struct Plan {
         before = part_o + up16(join ? u * 2 * gt * d.d * 4 : 0);
         whole_ml = before + up16(sums ? (size_t)n * 8 : 0);
         scores = whole_ml + (sums ? (size_t)n * P * 32 * 4 : 0);
-        bytes = scores + (sums ? (size_t)kv.n_pages * d.page * d.H * 4 : 0);
+        bytes = scores + (sums ? (size_t)kv.n_pages * d.page * d.H * 4 + 16 : 0);
     }
 };
 
@@ -827,28 +893,39 @@ hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStrea
     char *ws = static_cast<char *>(c.ws);
     const int es = d.io_dtype == GDNQ_IO_BF16 ? 2 : 4;
     Space w{};
-    if (p.join || p.sums) w.start = reinterpret_cast<Start *>(ws + p.start);
-    if (p.join) {
+    const int shares = p.brief ? 0 : p.shares;
+    if (shares && (p.join || p.sums)) w.start = reinterpret_cast<Start *>(ws + p.start);
+    if (shares && p.join) {
         w.part_ml = reinterpret_cast<float *>(ws + p.part_ml);
         w.part_o = reinterpret_cast<float *>(ws + p.part_o);
     }
     if (p.sums) {
-        w.before = reinterpret_cast<u64 *>(ws + p.before);
+        if (shares) w.before = reinterpret_cast<u64 *>(ws + p.before);
         w.whole_ml = reinterpret_cast<float *>(ws + p.whole_ml);
         w.scores = reinterpret_cast<float *>(ws + p.scores);
+        w.spare = (size_t)c.kv.n_pages * d.page * d.H;
     }
-    const dim3 joins = grid_of((unsigned long long)p.shares * p.gt +
-                                   (p.sums ? (unsigned long long)c.n * d.hk * p.splits : 0), NT);
-    const StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, __builtin_ctz((unsigned)d.page), d.window, p.shares,
-                     p.splits, d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es),
-                     make_divisor((unsigned)p.splits), make_divisor((unsigned)d.hk), joins.x};
+    const unsigned long long pairs = (unsigned long long)c.n * p.P;
+    const dim3 waves = grid_of((pairs + NW - 1) / NW, NT);
+    const unsigned long long second =
+        (p.join ? (unsigned long long)shares * p.gt : 0) + (p.sums ? (unsigned long long)c.n * d.hk * p.splits : 0);
+    const dim3 joins = second ? grid_of(second, NT) : dim3(0);
+    StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, __builtin_ctz((unsigned)d.page), d.window, shares, p.splits,
+               d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es), wide_rows(c.o, c.ldo, es),
+               make_divisor((unsigned)p.splits), make_divisor((unsigned)d.hk), make_divisor((unsigned)p.P), 0};
     return with_bool(d.io_dtype == GDNQ_IO_BF16, [&](auto bf) {
         return with_bool(p.sums, [&](auto sm) {
             auto go = [&](auto dd) {
                 constexpr bool B = decltype(bf)::value, S = decltype(sm)::value;
                 constexpr int D = decltype(dd)::value;
-                hipLaunchKernelGGL((attn_kernel<B, D, S>), dim3((unsigned)p.shares), dim3(NT), 0, st, A);
-                if (p.join || p.sums)
+                if (shares)
+                    hipLaunchKernelGGL((attn_kernel<B, D, S>), dim3((unsigned)shares), dim3(NT), 0, st, A);
+                else {
+                    A.nx = waves.x;
+                    hipLaunchKernelGGL((attn_short_kernel<B, D, S>), waves, dim3(NT), 0, st, A);
+                }
+                A.nx = joins.x;
+                if (second)
                     hipLaunchKernelGGL((attn_join_kernel<B, D, S>), joins, dim3(NT), 0, st, A);
                 return hipGetLastError();
             };

@@ -74,6 +74,12 @@ CASES = [
     ("bf16", 8, 1, 128, 16, [4097, 9000, 20], 0, "hr", 0),
     ("f32", 4, 2, 64, 16, [5000], 0, "hr", 0),
     ("bf16", 4, 2, 64, 8, [9] * 300 + [2000, 1], 0, "hr", 0),
+    # many short caches
+    ("bf16", 16, 8, 128, 16, [(37 * i) % 513 for i in range(130)], 0, "hr", 0),
+    ("bf16", 6, 2, 64, 8, [(11 * i) % 300 for i in range(515)], 0, "rh", 1),
+    ("f32", 5, 1, 64, 16, [(5 * i) % 257 for i in range(1030)], 33, "hr", 4),
+    ("bf16", 40, 2, 256, 32, [(91 * i) % 480 for i in range(260)], 0, "hr", 8),
+    ("f32", 24, 8, 128, 64, [(29 * i) % 250 for i in range(128)], 0, "pad", 0),
 ]
 IDS = [f"{c[0]}-{c[1]}x{c[2]}-d{c[3]}-p{c[4]}-n{len(c[5])}x{max(c[5])}-w{c[6]}-{c[7]}" for c in CASES]
 
