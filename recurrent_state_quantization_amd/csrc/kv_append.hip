@@ -2,8 +2,13 @@
 // and keys turned by their positions, keys and values stored behind the rows
 // that their slot holds.
 //
-// One pass over the tokens' rows.  A workgroup takes a token: its (cos, sin)
-// pairs are formed once in LDS and serve the query and the key heads.
+// One pass over the tokens' rows.  A workgroup takes a few tokens of a sequence:
+// their (cos, sin) pairs and places are formed once in LDS and serve all heads,
+// whose pieces it deals out over its threads in one order: queries, keys, values.
+// Bound by HBM: 20011 tokens of 13 prompts, 32 query and 8 cache heads of 128,
+// 88 us (5.6 TB/s; a large copy reaches 4.9).  Of long calls the queries go past
+// the caches, both ways; keys and values do not, which are read next (and took
+// 98 us past them).
 #include "attn_launchers.hpp"
 #include "paged.hpp"
 #include "rotate.hpp"
@@ -11,68 +16,88 @@
 namespace gdnq {
 namespace {
 
+constexpr int NT = 256, MAX_ROWS = 4;
+
 struct AppendArgs {
     AppendCall c;
     HeadPieces p;
     int H, hk, d, shift;
+    int rows;         // log2 of a workgroup's tokens
+    int nv, pieces;   // pieces of a head of values, of a token
     float amp;
     bool turn, inverse;
-    unsigned nx;   // width of the grid
+    Divisor byPieces, byNv;
+    unsigned nx;      // width of the grid
 };
 
-template <bool BF16, int V, bool INTER>
-__global__ __launch_bounds__(256) void kv_append_kernel(AppendArgs A)
+template <bool BF16, int V, bool INTER, bool STREAM>
+__global__ __launch_bounds__(NT) void kv_append_kernel(AppendArgs A)
 {
     using P = Pack<BF16, V>;
-    __shared__ float2 cs[128];
+    __shared__ float2 cs[MAX_ROWS][128];
+    __shared__ int page[MAX_ROWS], at[MAX_ROWS], position[MAX_ROWS];
     const int t = (int)__builtin_amdgcn_workitem_id_x();
     const int id = (int)block_id(A.nx);
     const AppendCall &c = A.c;
-    // the token, its sequence's last row and the rows behind it
-    int tok, entry, behind;
+    // the first token, its sequence's tokens, and those from this one to the last
+    int tok, entry, count, behind;
     if (c.cu) {
-        if ((long long)id >= (long long)c.T + c.n) return;
+        if ((long long)id >= (long long)(c.T >> A.rows) + c.n) return;
         SeqTile x;
-        if (!seq_tile(c.cu, nullptr, c.n, id, 0, c.T, 0x7FFFFFFF, x)) return;
-        tok = x.start + x.k;
+        if (!seq_tile(c.cu, nullptr, c.n, id, A.rows, c.T, 0x7FFFFFFF, x)) return;
+        tok = x.start + (x.k << A.rows);
         entry = x.seq;
-        behind = x.len - x.k;
+        count = x.len;
+        behind = x.len - (x.k << A.rows);
     } else {
         if (id >= c.n) return;
         tok = entry = id;
-        behind = 1;
+        count = behind = 1;
     }
     SlotRows s;
-    if (!slot_rows(c.kv, c.slots, entry, A.shift, s)) return;
-    const int count = c.cu ? c.cu[entry + 1] - c.cu[entry] : 1, row = s.len - behind;
-    if (s.len < count) return;
-    const int pos = c.pos ? c.pos[tok] : row;
-    for (int i = t; i < A.p.rot / 2; i += 256) {
-        unsigned long long f = A.turn ? c.table[i] * (unsigned long long)(long long)pos : 0ull;
-        cs[i] = turn(A.inverse ? 0ull - f : f, A.amp);
+    if (!slot_rows(c.kv, c.slots, entry, A.shift, s) || s.len < count) return;
+    const int nr = min(1 << A.rows, behind), row0 = s.len - behind;
+    if (t < nr) {
+        const int row = row0 + t;
+        page[t] = s.table[row >> A.shift];
+        at[t] = row & ((1 << A.shift) - 1);
+        position[t] = c.pos ? c.pos[tok + t] : row;
+    }
+    const int pairs = A.turn ? A.p.rot / 2 : 0;
+    for (int i = t; i < nr * 128; i += NT) {
+        const int r = i >> 7, x = i & 127;
+        if (x >= pairs) continue;
+        const unsigned long long f = c.table[x] * (unsigned long long)(long long)(c.pos ? c.pos[tok + r] : row0 + r);
+        cs[r][x] = turn(A.inverse ? 0ull - f : f, A.amp);
     }
     __syncthreads();
-    if (c.q)
-        for (int i = t; i < A.H * A.p.ni; i += 256) {
-            const int h = (int)div_by((unsigned)i, A.p.byNi);
-            turn_piece<BF16, V, INTER>(c.q, (size_t)tok * c.ldq + (size_t)h * A.d, c.q_out,
-                                       (size_t)tok * c.ldqo + (size_t)h * A.d, i - h * A.p.ni, cs, A.p);
+    const int nq = c.q ? A.H * A.p.ni : 0, nk = A.hk * A.p.ni;
+    for (int i = t; i < nr * A.pieces; i += NT) {
+        const int r = (int)div_by((unsigned)i, A.byPieces), x = i - r * A.pieces;
+        const bool query = x < nq, key = !query && x < nq + nk;
+        const size_t row = (size_t)(tok + r);
+        if (query) {
+            const int h = (int)div_by((unsigned)x, A.p.byNi);
+            turn_piece<BF16, V, INTER, STREAM>(c.q, row * c.ldq + (size_t)h * A.d, c.q_out,
+                                               row * c.ldqo + (size_t)h * A.d, x - h * A.p.ni, cs[r], A.p);
+            continue;
         }
-    const int page = s.table[row >> A.shift], off = row & ((1 << A.shift) - 1);
-    if (page < 0 || page >= c.kv.n_pages) return;
-    for (int i = t; i < A.hk * A.p.ni; i += 256) {
-        const int h = (int)div_by((unsigned)i, A.p.byNi);
-        turn_piece<BF16, V, INTER>(c.k, (size_t)tok * c.ldk + (size_t)h * A.d, c.kv.k, row_at(c.kv, page, h, off),
-                                   i - h * A.p.ni, cs, A.p);
+        if (page[r] < 0 || page[r] >= c.kv.n_pages) continue;
+        if (key) {
+            const int y = x - nq, h = (int)div_by((unsigned)y, A.p.byNi);
+            turn_piece<BF16, V, INTER, false>(c.k, row * c.ldk + (size_t)h * A.d, c.kv.k,
+                                              row_at(c.kv, page[r], h, at[r]), y - h * A.p.ni, cs[r], A.p);
+        } else {
+            const int y = x - nq - nk, h = (int)div_by((unsigned)y, A.byNv), j = (y - h * A.nv) * V;
+            P::template store_once<false>(c.kv.v, row_at(c.kv, page[r], h, at[r]) + j,
+                                           P::template load_once<STREAM>(c.v, row * c.ldv + (size_t)h * A.d + j));
+        }
     }
-    const int nv = A.d / V;
-    for (int i = t; i < A.hk * nv; i += 256) {
-        const int h = i / nv, j = (i - h * nv) * V;
-        P::store(c.kv.v, row_at(c.kv, page, h, off) + j, P::load(c.v, (size_t)tok * c.ldv + (size_t)h * A.d + j));
-    }
-    for (int h = t; h < A.hk; h += 256) {
-        if (c.kv.acc) c.kv.acc[sum_at(A.hk, A.shift, page, h, off)] = 0.0f;
-        if (c.kv.pos) c.kv.pos[sum_at(A.hk, A.shift, page, h, off)] = pos;
+    for (int i = t; i < nr * A.hk; i += NT) {
+        const int r = i / A.hk, h = i - r * A.hk;
+        if (page[r] < 0 || page[r] >= c.kv.n_pages) continue;
+        if (c.kv.acc) c.kv.acc[sum_at(A.hk, A.shift, page[r], h, at[r])] = 0.0f;
+        if (c.kv.pos) c.kv.pos[sum_at(A.hk, A.shift, page[r], h, at[r])] = position[r];
     }
 }
 
@@ -84,17 +109,28 @@ hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, co
     const int es = bf16 ? 2 : 4, rot = r ? r->rot : 0;
     const bool wide = wide_pieces(d.d, rot, inter, es) && wide_rows(c.k, c.ldk, es) && wide_rows(c.v, c.ldv, es) &&
                       (!c.q || (wide_rows(c.q, c.ldq, es) && wide_rows(c.q_out, c.ldqo, es)));
-    AppendArgs A{c, head_pieces(d.d, rot, inter, wide ? 16 / es : 1), d.H, d.hk, d.d, __builtin_ctz((unsigned)d.page),
-                 r ? r->amp : 1.0f, r != nullptr, r && (r->flags & GDNQ_ROPE_INVERSE), 0};
-    const dim3 grid = grid_of(c.cu ? (unsigned long long)c.T + c.n : c.n, 256);
+    const int v = wide ? 16 / es : 1;
+    AppendArgs A{c, head_pieces(d.d, rot, inter, v), d.H, d.hk, d.d, __builtin_ctz((unsigned)d.page), 0, d.d / v, 0,
+                 r ? r->amp : 1.0f, r != nullptr, r && (r->flags & GDNQ_ROPE_INVERSE), {}, {}, 0};
+    A.pieces = ((c.q ? d.H : 0) + d.hk) * A.p.ni + d.hk * A.nv;
+    A.byPieces = make_divisor((unsigned)A.pieces);
+    A.byNv = make_divisor((unsigned)A.nv);
+    // four tokens of a prompt: their rows of a head lie together (20011 tokens of 32 and 8 heads of 128
+    // 95 us with one token, 88 with four, 115 with eight)
+    A.rows = c.cu && c.T >= 1024 ? 2 : 0;
+    const dim3 grid = grid_of(c.cu ? (unsigned long long)(c.T >> A.rows) + c.n : c.n, NT);
     A.nx = grid.x;
+    const bool stream = streams(2ull * c.T * ((c.q ? d.H : 0) + 2 * d.hk) * d.d * es);
     return with_bool(bf16, [&](auto b) {
         return with_bool(wide, [&](auto w) {
             return with_bool(inter, [&](auto n) {
-                constexpr bool B = decltype(b)::value;
-                constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
-                hipLaunchKernelGGL((kv_append_kernel<B, V, decltype(n)::value>), grid, dim3(256), 0, st, A);
-                return hipGetLastError();
+                return with_bool(stream, [&](auto o) {
+                    constexpr bool B = decltype(b)::value;
+                    constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
+                    hipLaunchKernelGGL((kv_append_kernel<B, V, decltype(n)::value, decltype(o)::value && V != 1>),
+                                       grid, dim3(NT), 0, st, A);
+                    return hipGetLastError();
+                });
             });
         });
     });

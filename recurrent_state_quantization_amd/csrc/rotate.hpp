@@ -62,17 +62,17 @@ inline HeadPieces head_pieces(int d, int rot, bool inter, int v)
 
 // Piece `it` of a head at element xo of x into the head at element yo of y;
 // cs: the row's (cos, sin) pairs.
-template <bool BF16, int V, bool INTER>
+template <bool BF16, int V, bool INTER, bool STREAM>
 __device__ __forceinline__ void turn_piece(const void *x, size_t xo, void *y, size_t yo, int it, const float2 *cs,
                                            const HeadPieces &p)
 {
     using P = Pack<BF16, V>;
     if (it >= p.np) {
         const int j = p.rot + (it - p.np) * V;
-        P::store(y, yo + j, P::load(x, xo + j));
+        P::template store_once<STREAM>(y, yo + j, P::template load_once<STREAM>(x, xo + j));
     } else if constexpr (INTER && V > 1) {
         float v[V];
-        load_vec<BF16, V>(x, xo + it * V, v);
+        P::widen(P::template load_once<STREAM>(x, xo + it * V), v);
 #pragma unroll
         for (int i = 0; i < V / 2; i++) {
             const float2 t = cs[it * (V / 2) + i];
@@ -80,12 +80,13 @@ __device__ __forceinline__ void turn_piece(const void *x, size_t xo, void *y, si
             v[2 * i] = fmaf(a, t.x, -b * t.y);
             v[2 * i + 1] = fmaf(b, t.x, a * t.y);
         }
-        store_vec<BF16, V>(y, yo + it * V, v);
+        P::template store_once<STREAM>(y, yo + it * V, P::narrow(v));
     } else {
         const int ja = INTER ? 2 * it : it * V, jb = INTER ? 2 * it + 1 : p.rot / 2 + it * V;
         float a[V], b[V];
-        load_vec<BF16, V>(x, xo + ja, a);
-        load_vec<BF16, V>(x, xo + jb, b);
+        const typename P::raw ra = P::template load_once<STREAM>(x, xo + ja), rb = P::template load_once<STREAM>(x, xo + jb);
+        P::widen(ra, a);
+        P::widen(rb, b);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const float2 t = cs[it * V + i];
@@ -93,9 +94,12 @@ __device__ __forceinline__ void turn_piece(const void *x, size_t xo, void *y, si
             a[i] = fmaf(u, t.x, -w * t.y);
             b[i] = fmaf(w, t.x, u * t.y);
         }
-        store_vec<BF16, V>(y, yo + ja, a);
-        store_vec<BF16, V>(y, yo + jb, b);
+        P::template store_once<STREAM>(y, yo + ja, P::narrow(a));
+        P::template store_once<STREAM>(y, yo + jb, P::narrow(b));
     }
 }
+
+// Whether a call's rows, read and written, are more than the caches would keep.
+inline bool streams(unsigned long long bytes) { return bytes >= 64ull << 20; }
 
 }  // namespace gdnq
