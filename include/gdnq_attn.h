@@ -139,7 +139,9 @@ typedef struct {
  * skipped).
  *   k, v    device io_dtype [T, hk*d]: keys, turned as in gdnq_rope, and values
  *   q       device io_dtype [T, H*d], turned into q_out (or q itself, with the
- *           same row distance); both NULL: only k and v
+ *           same row distance); both NULL: only k and v.  q_out may be other
+ *           columns of the rows that k and v are columns of, with their row
+ *           distance: a fused projection's output is turned where it is
  *   rope    with d and io_dtype of desc and its table; NULL: nothing turns
  *   pos     device int32 [T], or NULL: each token's row is its position
  * kv->acc, if there, is set to 0 and kv->pos, if there, to the position in the

@@ -163,6 +163,15 @@ int check_workspace(void *p, size_t got, size_t need, Spans &sp)
     return GDNQ_OK;
 }
 
+// Whether n rows of two operands, ld elements apart in both, are columns of the same rows that
+// share no element (the parts of a fused projection's output).
+bool apart(const void *a, long long na, const void *b, long long nb, int64_t ld, int es)
+{
+    const uint64_t row = (uint64_t)ld * es, x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const uint64_t d = y >= x ? (y - x) % row : (row - (x - y) % row) % row;   // from a to the next b
+    return d >= (uint64_t)na * es && d + (uint64_t)nb * es <= row;
+}
+
 // x turned into y, or in place
 int check_turned(Spans &sp, const void *x, int64_t &ldx, void *y, int64_t &ldy, long long n, long long len, int es,
                  const char *xn, const char *yn)
@@ -262,10 +271,17 @@ int gdnq_kv_append(const gdnq_attn_desc *desc, const gdnq_rope_desc *rope, const
     TRY(flat(sp, cu_seqlens, ((size_t)n + 1) * 4, "cu_seqlens", READ, true));
     TRY(flat(sp, pos, (size_t)T * 4, "pos", READ, true));
     TRY(check_cache(d, kv, WRITE, WRITE, WRITE, sp));
-    TRY(rows(sp, k, T, (long long)d.hk * d.d, ldk, es, "k"));
-    TRY(rows(sp, v, T, (long long)d.hk * d.d, ldv, es, "v"));
+    const long long nq = (long long)d.H * d.d, nk = (long long)d.hk * d.d;
+    Spans queries = sp;
+    TRY(rows(sp, k, T, nk, ldk, es, "k"));
+    TRY(rows(sp, v, T, nk, ldv, es, "v"));
     if (!q != !q_out) return fail(GDNQ_EINVAL, "q and q_out must both be there, or neither");
-    if (q) TRY(check_turned(sp, q, ldq, q_out, ldqo, T, (long long)d.H * d.d, es, "q", "q_out"));
+    if (q) {
+        TRY(check_turned(queries, q, ldq, q_out, ldqo, T, nq, es, "q", "q_out"));
+        // k and v may be other columns of the same rows
+        if (ldk != ldqo || !apart(q_out, nq, k, nk, ldk, es)) TRY(rows(queries, k, T, nk, ldk, es, "k"));
+        if (ldv != ldqo || !apart(q_out, nq, v, nk, ldv, es)) TRY(rows(queries, v, T, nk, ldv, es, "v"));
+    }
     TRY(check_grid(((unsigned long long)T + n) * 4, "T"));
     const gdnq::AppendCall c{kv, q, k, v, q_out, table, pos, slots, cu_seqlens, ldq, ldqo, ldk, ldv, n, T};
     return launched(gdnq::launch_kv_append(d, rope ? &r : nullptr, c, stream_of(stream)));

@@ -260,7 +260,12 @@ def test_cache_refusals(g, call, kw, code, msg):
     (dict(ld=(0, 0, 127, 0)), 1, "rows of k"),
     (dict(ld=(0, 0, 0, 127)), 1, "rows of v"),
     (dict(q_out=BASE + (1 << 36), ld=(400, 390, 0, 0)), 1, "another distance"),
-    (dict(q_out=BASE + (3 << 36)), 1, "q_out overlaps k"),
+    (dict(q_out=BASE + (3 << 36)), 1, "k overlaps q_out"),
+    # columns of the same rows: the second's run into the first's, by one element, and round the row's end
+    (dict(q_out=BASE + (3 << 36) - 766, ld=(0, 700, 700, 0)), 1, "k overlaps q_out"),
+    (dict(q_out=BASE + (4 << 36) + 254, ld=(0, 700, 0, 700)), 1, "v overlaps q_out"),
+    (dict(q_out=BASE + (3 << 36) + 512, ld=(0, 500, 500, 0)), 1, "k overlaps q_out"),
+    (dict(q_out=BASE + (3 << 36) + 256, ld=(0, 700, 640, 0)), 1, "k overlaps q_out"),
     (dict(kvk=BASE + (3 << 36)), 1, "overlaps"),
     (dict(kvv=BASE + (8 << 36)), 1, "kv.v overlaps kv.k"),
     (dict(kvpos=BASE + (10 << 36) + 64), 1, "kv.pos overlaps kv.acc"),
@@ -332,6 +337,18 @@ def test_workspaces(g):
     assert isinstance(kv, attn._Kv)
 
 
+def test_append_takes_columns_of_the_same_rows(g):
+    """q turned in place beside k and v: past the argument checks, to the launch
+    (which fails here, without a GPU, or would fault on these addresses with one: not run there)."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("checks only")
+    at = BASE + (1 << 36)
+    for q, k, v, ld in ((0, 768, 1024, 640), (512, 0, 256, 640), (128, 1792 + 128, 896, 1024)):
+        rc, m = _append(g, q=at + q, q_out=at + q, k=at + k, v=at + v, ld=(ld, ld, ld, ld))
+        assert rc == 3, (rc, m)
+
+
 def test_no_ops(g):
     """Calls of nothing touch no pointer."""
     assert _rope(g, rows=0, x=None, y=None)[0] == 0
@@ -339,3 +356,28 @@ def test_no_ops(g):
     assert _step(g, n=0, q=None)[0] == 0
     assert _evict(g, n=0, acc=None)[0] == 0
     assert _evict(g, budget=12 * 16, size=0, ws=None)[0] == 0   # no slot holds more
+
+
+# ------------------------------------------------------------ the binding
+def test_binding_refuses_tensors(g):
+    """Tensors off the GPU, of another type or shape never reach the library."""
+    torch = pytest.importorskip("torch")
+    x, pos = torch.zeros(4, 3 * 64, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+    table = g.gdnq_rope_table(g.RopeDesc(d=64), g.RopeFreqs())
+    with pytest.raises(g.GdnqError, match="not on a GPU"):
+        g.gdnq_rope(g.RopeDesc(d=64), table, x, pos, x, 4, 3, 0)
+    with pytest.raises(g.GdnqError, match="int64"):
+        g.gdnq_rope(g.RopeDesc(d=64), table.float(), BASE, BASE, BASE, 4, 3, 0)
+    k = torch.zeros(5, 2, 16, 64, dtype=torch.bfloat16)
+    kv = g.Kv(k, k, torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(g.GdnqError, match="not on a GPU"):
+        kv.c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+    d = g.AttnDesc(H=6, hk=2, d=64, page=16)
+    b = _cache(_bufs(KV, {}), None)
+    with pytest.raises(g.GdnqError, match="not on a GPU"):
+        g.gdnq_attn_step(d, b, torch.zeros(4, 384, dtype=torch.bfloat16), BASE, None, 4, BASE, 0)
+    with pytest.raises(g.GdnqError, match="not on a GPU"):
+        k = torch.zeros(4, 128, dtype=torch.bfloat16)
+        g.gdnq_kv_append(d, None, None, b, None, None, k, BASE, None, None, None, 4, 4, 0)
+    with pytest.raises(g.GdnqError, match="not on a GPU"):
+        g.gdnq_kv_evict(d, b, 64, 0, 0, torch.zeros(4, dtype=torch.int32), 4, BASE, 0)
