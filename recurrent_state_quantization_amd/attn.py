@@ -117,10 +117,13 @@ class Kv:
         ldr = st[2] if d.page > 1 else d.d
         ldh = st[1] if hk > 1 else max(ldr * d.page, d.d)
         ldp = st[0] if n > 1 else max(ldh * hk, ldr * d.page)
-        return _Kv(self.k.data_ptr(), self.v.data_ptr(), _flat(self.acc, n * hk * d.page, f32, cur, "acc"),
-                   _flat(self.pos, n * hk * d.page, i32, cur, "pos"),
-                   _flat(self.table, slots * width, i32, cur, "table"), _flat(self.lens, slots, i32, cur, "lens"),
-                   n, slots, width, ldp, ldh, ldr)
+        kv = _Kv(self.k.data_ptr(), self.v.data_ptr(), _flat(self.acc, n * hk * d.page, f32, cur, "acc"),
+                 _flat(self.pos, n * hk * d.page, i32, cur, "pos"), _flat(self.table, slots * width, i32, cur, "table"),
+                 _flat(self.lens, slots, i32, cur, "lens"),
+                 n, slots, width, ldp, ldh, ldr)
+        # what the pointers stand for, kept as long as they are, and checked by every call
+        kv.tensors, kv.of, kv.device = self, (hk, d.d, d.io_dtype, d.page), cur
+        return kv
 
 
 def _load():
@@ -147,15 +150,23 @@ def _load():
 _load()
 
 
-def _kv(kv, d):
-    return kv if isinstance(kv, _Kv) else kv.c(d)
+def _kv(kv, d, cur=None):
+    """The marshalled cache, which must be of this descriptor's sizes (and on the current device)."""
+    if not isinstance(kv, _Kv):
+        return kv.c(d)
+    if hasattr(kv, "of"):   # one of plain pointers says nothing of itself
+        if kv.of != (d.hk or d.H, d.d, d.io_dtype, d.page):
+            _bad(f"kv is a cache of hk, d, io_dtype and page {kv.of}, not of desc's")
+        if cur is not None and kv.device != cur:
+            _bad(f"kv is on device {kv.device}, not on the current device {cur}")
+    return kv
 
 
 def _table(table, d, cur):
     """Device pointer of the rot/2 frequencies (int64 or uint64 values)."""
     if table is None or type(table) is int:
         return table
-    if table.element_size() != 8 or table.is_floating_point():
+    if str(table.dtype) not in ("torch.int64", "torch.uint64"):
         _bad(f"table is {table.dtype}, not torch.int64 or torch.uint64")
     return _flat(table, (d.rot or d.d) // 2, table.dtype, cur, "table")
 
@@ -212,7 +223,7 @@ def gdnq_kv_append(desc, rope, table, kv, q, q_out, k, v, pos, slots, cu_seqlens
     kp, ldk = _rows(k, T, hk * D, io, cur, "k")
     vp, ldv = _rows(v, T, hk * D, io, cur, "v")
     rc = lib.gdnq_kv_append(
-        d, r, None if r is None else _table(table, r, cur), _kv(kv, d), qp, ldq, op, ldqo, kp, ldk, vp, ldv,
+        d, r, None if r is None else _table(table, r, cur), _kv(kv, d, cur), qp, ldq, op, ldqo, kp, ldk, vp, ldv,
         _flat(pos, T, i32, cur, "pos"), _flat(slots, n, i32, cur, "slots"),
         _flat(cu_seqlens, n + 1, i32, cur, "cu_seqlens"), n, T, st)
     if rc:
@@ -230,7 +241,7 @@ def gdnq_attn_step(desc, kv, q, o, slots, n, workspace=None, stream=None):
     d = _desc(desc)
     cur, st = _begin(stream)
     io, _, i32 = _layer._types(d)
-    kv = _kv(kv, d)
+    kv = _kv(kv, d, cur)
     qp, ldq = _rows(q, n, d.H * d.d, io, cur, "q")
     op, ldo = _rows(o, n, d.H * d.d, io, cur, "o")
     ws, nb = _space(workspace, cur, lambda: gdnq_attn_workspace(d, kv, n))
@@ -250,7 +261,7 @@ def gdnq_kv_evict(desc, kv, budget, sink, recent, slots, n, workspace=None, stre
     d = _desc(desc)
     cur, st = _begin(stream)
     _, _, i32 = _layer._types(d)
-    kv = _kv(kv, d)
+    kv = _kv(kv, d, cur)
     ws, nb = _space(workspace, cur, lambda: gdnq_kv_evict_workspace(d, kv, budget, n))
     rc = lib.gdnq_kv_evict(d, kv, budget, sink, recent, _flat(slots, n, i32, cur, "slots"), n, ws, nb, st)
     if rc:

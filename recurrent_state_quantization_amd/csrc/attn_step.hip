@@ -168,6 +168,7 @@ __device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh, 
     const int t = (int)__builtin_amdgcn_workitem_id_x();
     const int per = (A.c.n + NT - 1) / NT, lo = min(t * per, A.c.n), hi = min(lo + per, A.c.n);
     u64 mine = 0;
+#pragma unroll 4
     for (int i = lo; i < hi; i++) mine += (unsigned)entry_of<ROWS>(A, i).units;
     const u64 before = sum_before(mine, part, sh.at.all) * (unsigned)A.P;
     if (b == 0 && A.w.before) {
@@ -743,13 +744,14 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
         for (int tile = 0; tile < A.nt; tile++) {
             const int heads = min(16, A.G - tile * 16);
             // eight heads at a time: of the first ones before the maximum and the sum are known
-            const float *from =
-                A.w.scores + (in ? ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off : 0);
+            const size_t first = in ? ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off : 0;
+            const float *from = A.w.scores + first;
             float4 s[8];
             auto load = [&](int x0) {
 #pragma unroll
                 for (int x = 0; x < 8; x++)
-                    if (x0 + x < heads && in) s[x] = *reinterpret_cast<const float4 *>(from + ((size_t)(x0 + x) << A.shift));
+                    if (x0 + x < heads && in)
+                        s[x] = *reinterpret_cast<const float4 *>(from + ((size_t)(x0 + x) << A.shift));
             };
             load(0);
             if (A.nt > 1 || !known) {   // the pair's maximum and sum

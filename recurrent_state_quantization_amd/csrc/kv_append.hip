@@ -6,9 +6,9 @@
 // their (cos, sin) pairs and places are formed once in LDS and serve all heads,
 // whose pieces it deals out over its threads in one order: queries, keys, values.
 // Bound by HBM: 20011 tokens of 13 prompts, 32 query and 8 cache heads of 128,
-// 88 us (5.6 TB/s; a large copy reaches 4.9).  Of long calls the queries go past
-// the caches, both ways; keys and values do not, which are read next (and took
-// 98 us past them).
+// 99 us (5.0 TB/s, the rate of a large copy), 88 where a part of the rows is still
+// in the memory's cache.  Of long calls the queries go past the caches, both ways
+// (111 us through them); keys and values do not: they are read next.
 #include "attn_launchers.hpp"
 #include "paged.hpp"
 #include "rotate.hpp"
@@ -115,8 +115,8 @@ hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, co
     A.pieces = ((c.q ? d.H : 0) + d.hk) * A.p.ni + d.hk * A.nv;
     A.byPieces = make_divisor((unsigned)A.pieces);
     A.byNv = make_divisor((unsigned)A.nv);
-    // four tokens of a prompt: their rows of a head lie together (20011 tokens of 32 and 8 heads of 128
-    // 95 us with one token, 88 with four, 115 with eight)
+    // four tokens of a prompt: their rows of a head lie together (the same call 95 us with one token where
+    // four take 88, 115 with eight; from memory 98, 99)
     A.rows = c.cu && c.T >= 1024 ? 2 : 0;
     const dim3 grid = grid_of(c.cu ? (unsigned long long)(c.T >> A.rows) + c.n : c.n, NT);
     A.nx = grid.x;
@@ -127,8 +127,8 @@ hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, co
                 return with_bool(stream, [&](auto o) {
                     constexpr bool B = decltype(b)::value;
                     constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
-                    hipLaunchKernelGGL((kv_append_kernel<B, V, decltype(n)::value, decltype(o)::value && V != 1>),
-                                       grid, dim3(NT), 0, st, A);
+                    constexpr bool N = decltype(n)::value, S = decltype(o)::value && V != 1;
+                    hipLaunchKernelGGL((kv_append_kernel<B, V, N, S>), grid, dim3(NT), 0, st, A);
                     return hipGetLastError();
                 });
             });

@@ -50,8 +50,9 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs A)
         const int h = (int)div_by((unsigned)in_row, A.p.byNi);
         if (h >= nh) continue;
         const size_t at = (size_t)(h0 + h) * A.d;
-        turn_piece<BF16, V, INTER, STREAM>(A.c.x, (size_t)(r0 + r) * A.c.ldx + at, A.c.y, (size_t)(r0 + r) * A.c.ldy + at,
-                                   in_row - h * A.p.ni, cs + r * pairs, A.p);
+        const size_t row = (size_t)(r0 + r);
+        turn_piece<BF16, V, INTER, STREAM>(A.c.x, row * A.c.ldx + at, A.c.y, row * A.c.ldy + at, in_row - h * A.p.ni,
+                                           cs + r * pairs, A.p);
     }
 }
 
@@ -64,9 +65,9 @@ hipError_t launch_rope(const gdnq_rope_desc &d, const RopeCall &c, hipStream_t s
     const bool wide = wide_pieces(d.d, d.rot, inter, es) && wide_rows(c.x, c.ldx, es) && wide_rows(c.y, c.ldy, es);
     RopeArgs A{c, head_pieces(d.d, d.rot, inter, wide ? 16 / es : 1), d.d, 1, c.H, d.amp,
                (d.flags & GDNQ_ROPE_INVERSE) != 0, {}, {}, {}, 0};
-    // a workgroup's pieces: one or two a thread (three rows of 40 heads of 128 in bf16 instead of
-    // one: 124 us instead of 113)
-    A.heads = (long long)c.rows * c.H * A.p.ni >= 256 * 1024 ? c.H : std::min(c.H, std::max(1, 256 / A.p.ni));
+    // Whole rows, some 512 pieces in a workgroup (three rows of 40 heads of 128 in bf16 instead of one:
+    // 124 us instead of 113), or, of few rows, the heads that give each thread a piece.
+    A.heads = c.rows >= 512 ? c.H : std::min(c.H, std::max(1, 256 / A.p.ni));
     A.rows = A.heads < c.H ? 1 : std::max(1, std::min(512 / (c.H * A.p.ni), MAX_CS / (d.rot / 2)));
     A.byRow = make_divisor((unsigned)(A.heads * A.p.ni));
     A.byPairs = make_divisor((unsigned)(d.rot / 2));
@@ -81,8 +82,8 @@ hipError_t launch_rope(const gdnq_rope_desc &d, const RopeCall &c, hipStream_t s
                 return with_bool(stream, [&](auto o) {
                     constexpr bool B = decltype(b)::value;
                     constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
-                    hipLaunchKernelGGL((rope_kernel<B, V, decltype(n)::value, decltype(o)::value && V != 1>), grid,
-                                       dim3(256), 0, st, A);
+                    constexpr bool N = decltype(n)::value, S = decltype(o)::value && V != 1;
+                    hipLaunchKernelGGL((rope_kernel<B, V, N, S>), grid, dim3(256), 0, st, A);
                     return hipGetLastError();
                 });
             });

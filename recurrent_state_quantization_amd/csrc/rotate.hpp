@@ -84,7 +84,8 @@ __device__ __forceinline__ void turn_piece(const void *x, size_t xo, void *y, si
     } else {
         const int ja = INTER ? 2 * it : it * V, jb = INTER ? 2 * it + 1 : p.rot / 2 + it * V;
         float a[V], b[V];
-        const typename P::raw ra = P::template load_once<STREAM>(x, xo + ja), rb = P::template load_once<STREAM>(x, xo + jb);
+        const typename P::raw ra = P::template load_once<STREAM>(x, xo + ja);
+        const typename P::raw rb = P::template load_once<STREAM>(x, xo + jb);
         P::widen(ra, a);
         P::widen(rb, b);
 #pragma unroll

@@ -193,3 +193,26 @@ def test_repeated_calls_agree():
         call(C, 16, q, o)
         seen.append((o.clone(), C.accd.clone()))
     assert all(same(a, seen[0][0]) and same(b, seen[0][1]) for a, b in seen)
+
+
+def test_a_marshalled_cache_says_what_it_is():
+    """A cache marshalled once keeps its tensors, and is refused where the descriptor is another's."""
+    torch = torch_cuda()
+    g = lib()
+    say("attention cache of another descriptor")
+    rng = np.random.default_rng(19)
+    C = Cache(rng, [20], 2, 64, 16, "bf16", extra_pages=0)
+    kv = C.kv().c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+    q = torch.zeros(1, 8 * 64, dtype=torch.bfloat16, device="cuda")
+    for other in (dict(H=4, hk=1), dict(H=8, hk=4), dict(H=4, hk=2, page=32), dict(H=4, hk=2, d=128),
+                  dict(H=4, hk=2, io_dtype=g.IO_F32)):
+        with pytest.raises(g.GdnqError, match="kv is a cache of"):
+            g.gdnq_attn_step(g.AttnDesc(**{**dict(d=64, page=16), **other}), kv, q, q.clone(), C.slotsd, 1, None)
+    with pytest.raises(g.GdnqError, match="shape and strides"):
+        C.kv(v=C.vd.transpose(1, 2).contiguous().transpose(1, 2)).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+    with pytest.raises(g.GdnqError, match="must be"):
+        C.kv(k=C.kd[..., :32]).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+    with pytest.raises(g.GdnqError, match="acc has"):
+        C.kv(acc=C.accd[:1]).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+    with pytest.raises(g.GdnqError, match="lens is"):
+        C.kv(lens=C.lensd.long()).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
