@@ -38,14 +38,15 @@ namespace {
 constexpr float LOG2E = 1.44269504f, LOWEST = -3.4028234e38f;
 constexpr int NT = 256, NW = NT / 64;
 constexpr int SHARES = 512;   // workgroups at most: two for each compute unit
+constexpr int JOIN_HEADS = 16;     // workgroups at most that join a pair's heads
 constexpr int SUM_ROWS = NT * 4;   // rows of which a workgroup adds up the weights at a time
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned long long u64;
 
-// Where a share begins: entry, pair (cache head and 16 of its query heads), unit of
-// the pair, and the pair's units; and the units of all entries (0: the share has
+// Where a share begins: entry, pair (cache head and up to 64 of its query heads),
+// unit of the pair, and the pair's units; and the units of all entries (0: the share has
 // none).
 struct Start {
     int i, p, u, units;
@@ -55,10 +56,10 @@ struct Start {
 // The workspace's parts.
 struct Space {
     Start *start;       // [shares], for the second kernel
-    float *part_ml;     // [2 shares][16][2]: maximum and sum of a share's first and last piece
+    float *part_ml;     // [2 shares][16 tw][2]: maximum and sum of a share's first and last piece
     float *part_o;      // [2 shares][gt][D]
     u64 *before;        // [n]: units of the entries before, for the sums of weights, as are
-    float *whole_ml;    // [n P][16][2]
+    float *whole_ml;    // [n P][16 tw][2]
     float *scores;      // [n_pages][hk][G][page], and four more
     size_t spare;       // where these are, for rows on no page
 };
@@ -66,12 +67,15 @@ struct Space {
 struct StepArgs {
     AttnCall c;
     Space w;
-    int H, hk, G, gt, nt, P;   // query heads per cache head, per pair; pairs per cache head, per entry
+    int H, hk, G;              // query heads per cache head,
+    int gt, nt, P;             // per pair; pairs per cache head, per entry
+    int tw;                    // groups of 16 heads in a pair, each with its own waves
+    int nt16;                  // groups of 16 heads per cache head
     int shift, window;
     int shares, splits;        // 0: a wave for each pair; workgroups for the sums of an entry and cache head
     float scale2, decay;       // scale log2(e): weights are powers of two
     bool wide_q, wide_o;
-    Divisor bySplits, byHk, byP;
+    Divisor bySplits, byHk, byGroups;
     unsigned nx;               // width of the grid, where it is not the shares
 };
 
@@ -249,12 +253,17 @@ __device__ __forceinline__ float across_rows_sum(float x)
     return a + b;
 }
 
-// 16 bytes that are read once: kept out of the caches' way (64 requests to 32768
-// rows 410 -> 366 us, 5.8 -> 6.5 TB/s).
-__device__ __forceinline__ uint4 stream16(const char *p)
+// 16 bytes.  What is read once is kept out of the caches' way (64 requests to 32768
+// rows 410 -> 366 us, 5.8 -> 6.5 TB/s); what several waves read (AGAIN) is not (32
+// requests to 20000 rows, 64 query heads to a cache head, 145 -> 106 us).
+template <bool AGAIN>
+__device__ __forceinline__ uint4 read16(const char *p)
 {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-    const u32x4 x = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+    u32x4 x;
+    if constexpr (AGAIN) x = *q;
+    else x = __builtin_nontemporal_load(q);
     return make_uint4(x.x, x.y, x.z, x.w);
 }
 
@@ -264,8 +273,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
     return __builtin_bit_cast(uint32_t, (bf16x2{(__bf16)a, (__bf16)b}));
 }
 
-// One wave's steps over a piece, STRIDE apart.  Lane = (head or row or column n = lane & 15, group g = lane >> 4).
-template <bool BF16, int D, bool SUMS, int STRIDE>
+// One wave's steps over a piece, `stride` apart.  Lane = (head or row or column n = lane & 15, group g = lane >> 4).
+template <bool BF16, int D, bool SUMS, bool WIDE>
 struct Steps {
     using X = Geo<BF16, D>;
     static constexpr int J = X::J;
@@ -273,6 +282,7 @@ struct Steps {
     const StepArgs &A;
     const Entry &e;
     int h, n, g;
+    const int stride;
     size_t head;                 // of the cache, in elements
     uint4 q[X::KP], k[J][X::KP];
     uint4 v[J * 4][X::VP];       // row 16 j + 4 g + i at 4 j + i
@@ -284,7 +294,8 @@ struct Steps {
     bool ok[J];                  // or whose page does not exist (of this lane's rows of V and scores)
     int at_v[J];                 // (with SUMS) their pages
 
-    __device__ __forceinline__ Steps(const StepArgs &A_, const Entry &e_, int h_) : A(A_), e(e_), h(h_)
+    __device__ __forceinline__ Steps(const StepArgs &A_, const Entry &e_, int h_, int stride_)
+        : A(A_), e(e_), h(h_), stride(stride_)
     {
         const int lane = (int)(__builtin_amdgcn_workitem_id_x() & 63u);
         n = lane & 15;
@@ -333,7 +344,7 @@ struct Steps {
         for (int j = 0; j < J; j++) {
             const char *p = at(A.c.kv.k, there(page_k[j]) ? page_k[j] : 0, t * X::ROWS + 16 * j + n) + g * 16;
 #pragma unroll
-            for (int c = 0; c < X::KP; c++) k[j][c] = stream16(p + c * 64);
+            for (int c = 0; c < X::KP; c++) k[j][c] = read16<WIDE>(p + c * 64);
         }
     }
 
@@ -352,7 +363,7 @@ struct Steps {
 #pragma unroll
                 for (int c = 0; c < X::VP; c++) {
                     if constexpr (X::VE * X::ES == 16)
-                        v[4 * j + i][c] = stream16(p + c * 256);
+                        v[4 * j + i][c] = read16<WIDE>(p + c * 256);
                     else {
                         const uint2 x = load_nt8(reinterpret_cast<const int8_t *>(p));
                         v[4 * j + i][c] = make_uint4(x.x, x.y, 0, 0);
@@ -434,14 +445,14 @@ struct Steps {
     __device__ __forceinline__ void step(int t)
     {
         float s[4 * J], top = LOWEST;
-        if constexpr (MORE) load_pages(t + 2 * STRIDE, then_k, then_v);
+        if constexpr (MORE) load_pages(t + 2 * stride, then_k, then_v);
 #pragma unroll
         for (int j = 0; j < J; j++) {
             const f32x4 x = scores(j);
 #pragma unroll
             for (int i = 0; i < 4; i++) s[4 * j + i] = x[i] * A.scale2;
         }
-        if constexpr (MORE) load_k(t + STRIDE);
+        if constexpr (MORE) load_k(t + stride);
         float4 raw[J];
         size_t to[J];
         if constexpr (SUMS) {
@@ -485,7 +496,7 @@ struct Steps {
             for (int w = 0; w < X::VE; w++) o[c][w] *= f;
         add_values(s);
         if constexpr (MORE) {
-            load_v(t + STRIDE);
+            load_v(t + stride);
 #pragma unroll
             for (int j = 0; j < J; j++) {
                 page_k[j] = then_k[j];
@@ -498,7 +509,8 @@ struct Steps {
         }
     }
 
-    __device__ __forceinline__ void run(int t, int end)
+    // The steps from t on below `end`, for `heads` query heads from hq on (of none, nothing).
+    __device__ __forceinline__ void run(int i, int hq, int heads, int t, int end)
     {
         m = LOWEST;
         l = 0.0f;
@@ -506,9 +518,11 @@ struct Steps {
         for (int c = 0; c < X::VP; c++)
 #pragma unroll
             for (int w = 0; w < X::VE; w++) o[c][w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (t >= end) return;
+        if (t >= end || heads <= 0) return;
+        sum_head = hq - h * A.G + n % heads;
+        load_q(i, hq, heads);
         load_pages(t, page_k, page_v);
-        load_pages(t + STRIDE, then_k, then_v);
+        load_pages(t + stride, then_k, then_v);
         load_k(t);
         load_v(t);
 #pragma unroll
@@ -516,7 +530,7 @@ struct Steps {
             page_k[j] = then_k[j];
             page_v[j] = then_v[j];
         }
-        for (; t + STRIDE < end; t += STRIDE) step<true>(t);
+        for (; t + stride < end; t += stride) step<true>(t);
         step<false>(t);
         l = across_rows_sum(l);
     }
@@ -524,9 +538,10 @@ struct Steps {
     int sum_head;   // (with SUMS) the lane's head within the cache head's
 };
 
-template <bool BF16, int D, bool SUMS>
+template <bool BF16, int D, bool SUMS, bool WIDE>
 __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
 {
+    const int tw = WIDE ? A.tw : 1;
     using X = Geo<BF16, D>;
     constexpr int DC = D < 128 ? D : 128;             // columns joined at a time
     constexpr int PC = DC / (16 * X::VE);             // in pieces of a lane
@@ -541,11 +556,12 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
     if (!some) return;
     u64 done = sh.x;
     for_pieces<X::ROWS>(A, sh, first, [&](int i, const Entry &e, int p, int u, int ue) {
-        const int h = p / A.nt, tile = p - h * A.nt, heads = min(16, A.G - tile * 16), hq = h * A.G + tile * 16;
-        Steps<BF16, D, SUMS, NW> st(A, e, h);
-        st.sum_head = tile * 16 + st.n % heads;
-        st.load_q(i, hq, heads);
-        st.run(e.t0 + u * NW + w, min(e.t0 + ue * NW, e.t1));
+        // wave w: every tw-th of the pair's groups of 16 heads, and of the steps those of its group's waves
+        const int h = p / A.nt, first_head = (p - h * A.nt) * A.gt, heads = min(A.gt, A.G - first_head);
+        const int hq = h * A.G + first_head, group = w & (tw - 1), waves = NW / tw;
+        const int mine = min(16, heads - 16 * group);
+        Steps<BF16, D, SUMS, WIDE> st(A, e, h, waves);
+        st.run(i, hq + 16 * group, mine, e.t0 + u * NW + w / tw, min(e.t0 + ue * NW, e.t1));
         const bool whole = u == 0 && ue == e.units;
         const size_t slot = 2 * (size_t)b + (done != sh.x);
         done += (unsigned)(ue - u);
@@ -557,7 +573,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
 #pragma unroll
         for (int c0 = 0; c0 < X::VP; c0 += PC) {
             if (c0) __syncthreads();
-            if (st.n < heads)
+            if (st.n < mine)
 #pragma unroll
                 for (int c = 0; c < PC; c++)
 #pragma unroll
@@ -570,15 +586,16 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
                                             st.o[c0 + c][x + 3][r]);
             __syncthreads();
             for (int x = t; x < heads * DC; x += NT) {
-                const int hd = x / DC, col = x - hd * DC;
-                float M = mj[0][hd], L = 0.0f, y = 0.0f;
+                const int hd = x / DC, col = x - hd * DC, n = hd & 15;
+                float M = LOWEST, L = 0.0f, y = 0.0f;
+                const int k0 = WIDE ? hd >> 4 : 0;   // its group's waves
 #pragma unroll
-                for (int k = 1; k < NW; k++) M = fmaxf(M, mj[k][hd]);
+                for (int k = k0; k < NW; k += tw) M = fmaxf(M, mj[k][n]);
 #pragma unroll
-                for (int k = 0; k < NW; k++) {
-                    const float f = __builtin_amdgcn_exp2f(mj[k][hd] - M);
-                    L = fmaf(lj[k][hd], f, L);
-                    y = fmaf(oj[k][hd][col], f, y);
+                for (int k = k0; k < NW; k += tw) {
+                    const float f = __builtin_amdgcn_exp2f(mj[k][n] - M);
+                    L = fmaf(lj[k][n], f, L);
+                    y = fmaf(oj[k][n][col], f, y);
                 }
                 const int at = c0 / PC * DC + col;
                 if (whole)
@@ -586,7 +603,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
                 else
                     A.w.part_o[(slot * A.gt + hd) * D + at] = y;
                 if (c0 == 0 && col == 0 && (SUMS || !whole)) {
-                    float *ml = whole ? A.w.whole_ml + ((size_t)i * A.P + p) * 32 : A.w.part_ml + slot * 32;
+                    float *ml = whole ? A.w.whole_ml + ((size_t)i * A.P + p) * 32 * tw : A.w.part_ml + slot * 32 * tw;
                     ml[2 * hd] = M;
                     ml[2 * hd + 1] = L;
                 }
@@ -595,25 +612,26 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
     });
 }
 
-// Short caches: a wave for each pair of an entry, without shares, workspace or
-// join.
+// Short caches: a wave for each group of 16 heads of an entry's cache heads,
+// without shares, pieces or join.
 template <bool BF16, int D, bool SUMS>
 __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_short_kernel(StepArgs A)
 {
     using X = Geo<BF16, D>;
     const int w = __builtin_amdgcn_readfirstlane((int)__builtin_amdgcn_workitem_id_x() >> 6);
-    const unsigned id = block_id(A.nx) * NW + (unsigned)w, i = div_by(id, A.byP), p = id - i * (unsigned)A.P;
+    const int groups = A.hk * A.nt16;
+    const unsigned id = block_id(A.nx) * NW + (unsigned)w, i = div_by(id, A.byGroups), p = id - i * (unsigned)groups;
     if (i >= (unsigned)A.c.n) return;
     const Entry e = entry_of<X::ROWS>(A, (int)i);
     if (e.units == 0) return;
-    const int h = (int)p / A.nt, tile = (int)p - h * A.nt, heads = min(16, A.G - tile * 16), hq = h * A.G + tile * 16;
-    Steps<BF16, D, SUMS, 1> st(A, e, h);
-    st.sum_head = tile * 16 + st.n % heads;
-    st.load_q((int)i, hq, heads);
-    st.run(e.t0, e.t1);
+    const int h = (int)p / A.nt16, group = (int)p - h * A.nt16, heads = min(16, A.G - group * 16);
+    const int hq = h * A.G + group * 16;
+    Steps<BF16, D, SUMS, false> st(A, e, h, 1);
+    st.run((int)i, hq, heads, e.t0, e.t1);
     if (st.n >= heads) return;
     if (SUMS && st.g == 0) {
-        float *ml = A.w.whole_ml + (size_t)id * 32 + 2 * st.n;
+        const size_t pair = ((size_t)i * A.hk + h) * A.nt + group / A.tw;
+        float *ml = A.w.whole_ml + (pair * A.tw + group % A.tw) * 32 + 2 * st.n;
         ml[0] = st.m;
         ml[1] = st.l;
     }
@@ -654,71 +672,74 @@ struct Pieces {
     __device__ __forceinline__ size_t slot(int b) const { return 2 * (size_t)b + (b == b0 && inside); }
 };
 
-// Joins the pieces of the pairs that lie in several shares: workgroup (b, head)
-// that of the pair which share b begins inside of, if no share before it does so
-// too.
+// Joins the pieces of the pairs that lie in several shares: workgroups (b, first),
+// for every JOIN_HEADS-th head, that of the pair which share b begins inside of, if
+// no share before it does so too.
 template <bool BF16, int D>
-__device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, int b, int hd)
+__device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, int b, int first)
 {
     constexpr int COLS = D / 4, PARTS = NT / COLS;   // threads on four columns each
     __shared__ float f[SHARES + 1], red[2][NW];
     __shared__ float4 oj[PARTS][COLS];
-    const int t = (int)__builtin_amdgcn_workitem_id_x();
+    const int t = (int)__builtin_amdgcn_workitem_id_x(), col = t % COLS, part = t / COLS;
     if (b == 0 || sh.at.u == 0) return;
     const u64 begin = sh.x - (unsigned)sh.at.u;
     const Pieces pc(sh.at.all, begin, sh.at.units);
     if (pc.b0 != b - 1) return;
-    const int h = sh.at.p / A.nt, tile = sh.at.p - h * A.nt;
-    if (hd >= min(16, A.G - tile * 16)) return;
-    const int np = pc.b1 - pc.b0 + 1;
-    float M = LOWEST;
-    for (int k = t; k < np; k += NT) {
-        f[k] = A.w.part_ml[pc.slot(pc.b0 + k) * 32 + 2 * hd];
-        M = fmaxf(M, f[k]);
-    }
-    M = fmaxf(M, __shfl_xor(M, 1));
-    M = fmaxf(M, __shfl_xor(M, 2));
-    M = fmaxf(M, __shfl_xor(M, 4));
-    M = fmaxf(M, __shfl_xor(M, 8));
-    M = across_rows_max(M);
-    if ((t & 63) == 0) red[0][t >> 6] = M;
-    __syncthreads();
+    const int h = sh.at.p / A.nt, first_head = (sh.at.p - h * A.nt) * A.gt, heads = min(A.gt, A.G - first_head);
+    const int np = pc.b1 - pc.b0 + 1, stride = 32 * A.tw;
+    for (int hd = first; hd < heads; hd += JOIN_HEADS) {
+        const float *ml = A.w.part_ml + 2 * hd;
+        if (hd != first) __syncthreads();   // the last head's sums have been read
+        float M = LOWEST;
+        for (int k = t; k < np; k += NT) {
+            f[k] = ml[pc.slot(pc.b0 + k) * stride];
+            M = fmaxf(M, f[k]);
+        }
+        M = fmaxf(M, __shfl_xor(M, 1));
+        M = fmaxf(M, __shfl_xor(M, 2));
+        M = fmaxf(M, __shfl_xor(M, 4));
+        M = fmaxf(M, __shfl_xor(M, 8));
+        M = across_rows_max(M);
+        if ((t & 63) == 0) red[0][t >> 6] = M;
+        __syncthreads();
 #pragma unroll
-    for (int k = 0; k < NW; k++) M = fmaxf(M, red[0][k]);
-    float L = 0.0f;
-    for (int k = t; k < np; k += NT) {
-        f[k] = __builtin_amdgcn_exp2f(f[k] - M);
-        L = fmaf(A.w.part_ml[pc.slot(pc.b0 + k) * 32 + 2 * hd + 1], f[k], L);
-    }
-    L = lanes_sum<64>(L);
-    if ((t & 63) == 0) red[1][t >> 6] = L;
-    __syncthreads();
-    L = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    const int col = t % COLS, part = t / COLS;
-    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int k = 0; k < NW; k++) M = fmaxf(M, red[0][k]);
+        float L = 0.0f;
+        for (int k = t; k < np; k += NT) {
+            f[k] = __builtin_amdgcn_exp2f(f[k] - M);
+            L = fmaf(ml[pc.slot(pc.b0 + k) * stride + 1], f[k], L);
+        }
+        L = lanes_sum<64>(L);
+        if ((t & 63) == 0) red[1][t >> 6] = L;
+        __syncthreads();
+        L = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+        float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int k = part; k < np; k += PARTS) {
-        const float4 x =
-            *reinterpret_cast<const float4 *>(A.w.part_o + (pc.slot(pc.b0 + k) * A.gt + hd) * D + 4 * col);
-        y.x = fmaf(x.x, f[k], y.x);
-        y.y = fmaf(x.y, f[k], y.y);
-        y.z = fmaf(x.z, f[k], y.z);
-        y.w = fmaf(x.w, f[k], y.w);
-    }
-    oj[part][col] = y;
-    __syncthreads();
-    if (t >= COLS) return;
+        for (int k = part; k < np; k += PARTS) {
+            const float4 x =
+                *reinterpret_cast<const float4 *>(A.w.part_o + (pc.slot(pc.b0 + k) * A.gt + hd) * D + 4 * col);
+            y.x = fmaf(x.x, f[k], y.x);
+            y.y = fmaf(x.y, f[k], y.y);
+            y.z = fmaf(x.z, f[k], y.z);
+            y.w = fmaf(x.w, f[k], y.w);
+        }
+        oj[part][col] = y;
+        __syncthreads();
+        if (t < COLS) {
 #pragma unroll
-    for (int k = 1; k < PARTS; k++) {
-        const float4 x = oj[k][t];
-        y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+            for (int k = 1; k < PARTS; k++) {
+                const float4 x = oj[k][t];
+                y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+            }
+            const float r = L > 0.0f ? 1.0f / L : 0.0f;
+            const size_t to = (size_t)sh.at.i * A.c.ldo + (size_t)(h * A.G + first_head + hd) * D + 4 * t;
+            store1<BF16>(A.c.o, to, y.x * r);
+            store1<BF16>(A.c.o, to + 1, y.y * r);
+            store1<BF16>(A.c.o, to + 2, y.z * r);
+            store1<BF16>(A.c.o, to + 3, y.w * r);
+        }
     }
-    const float r = L > 0.0f ? 1.0f / L : 0.0f;
-    const size_t to = (size_t)sh.at.i * A.c.ldo + (size_t)(h * A.G + tile * 16 + hd) * D + 4 * t;
-    store1<BF16>(A.c.o, to, y.x * r);
-    store1<BF16>(A.c.o, to + 1, y.y * r);
-    store1<BF16>(A.c.o, to + 2, y.z * r);
-    store1<BF16>(A.c.o, to + 3, y.w * r);
 }
 
 // acc of an entry's rows in a cache head, from the stored scores and the pairs'
@@ -727,14 +748,15 @@ __device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, 
 template <int ROWS>
 __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
 {
-    __shared__ float M[16], R[16], mj[NW][16], lj[NW][16];
+    __shared__ float M[64], R[64], mj[NW][16], lj[NW][16];
     const int t = (int)__builtin_amdgcn_workitem_id_x(), n = t & 15, k0 = t >> 4;
     const unsigned ih = div_by(id, A.bySplits);
-    const int which = (int)(id - ih * (unsigned)A.splits), i = (int)div_by(ih, A.byHk), h = (int)ih - i * A.hk, p = h * A.nt;
+    const int which = (int)(id - ih * (unsigned)A.splits), i = (int)div_by(ih, A.byHk), h = (int)ih - i * A.hk;
+    const int p = h * A.nt;
     const u64 all = A.shares ? A.w.start[0].all : 0, before = A.shares ? A.w.before[i] : 0;
     const Entry e = entry_of<ROWS>(A, i);
     if (e.units == 0) return;
-    const int lo = e.t0 * ROWS, hi = e.s.len;
+    const int lo = e.t0 * ROWS, hi = e.s.len, stride = 32 * A.tw;
     bool known = false;   // M and R are the pair's
     for (int r0 = lo + which * SUM_ROWS; r0 < hi; r0 += A.splits * SUM_ROWS) {
         const int r = r0 + 4 * t, off = r & ((1 << A.shift) - 1);
@@ -742,9 +764,9 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
         const bool in = page >= 0 && page < A.c.kv.n_pages;
         float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int tile = 0; tile < A.nt; tile++) {
-            const int heads = min(16, A.G - tile * 16);
+            const int heads = min(A.gt, A.G - tile * A.gt);
             // eight heads at a time: of the first ones before the maximum and the sum are known
-            const size_t first = in ? ((((size_t)page * A.hk + h) * A.G + tile * 16) << A.shift) + off : 0;
+            const size_t first = in ? ((((size_t)page * A.hk + h) * A.G + tile * A.gt) << A.shift) + off : 0;
             const float *from = A.w.scores + first;
             float4 s[8];
             auto load = [&](int x0) {
@@ -760,36 +782,38 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
                 __syncthreads();
                 if (pc.b0 == pc.b1) {
                     if (t < heads) {
-                        const float *ml = A.w.whole_ml + ((size_t)i * A.P + p + tile) * 32 + 2 * t;
+                        const float *ml = A.w.whole_ml + ((size_t)i * A.P + p + tile) * stride + 2 * t;
                         M[t] = ml[0];
                         R[t] = ml[1] > 0.0f ? 1.0f / ml[1] : 0.0f;
                     }
-                } else {
-                    float m = LOWEST, l = 0.0f;
-                    if (n < heads)
-                        for (int b = pc.b0 + k0; b <= pc.b1; b += 16) {
-                            const float *ml = A.w.part_ml + pc.slot(b) * 32 + 2 * n;
-                            const float mn = fmaxf(m, ml[0]);
-                            l = l * __builtin_amdgcn_exp2f(m - mn) + ml[1] * __builtin_amdgcn_exp2f(ml[0] - mn);
-                            m = mn;
+                } else
+                    for (int g0 = 0; g0 < heads; g0 += 16) {
+                        float m = LOWEST, l = 0.0f;
+                        if (g0 + n < heads)
+                            for (int b = pc.b0 + k0; b <= pc.b1; b += 16) {
+                                const float *ml = A.w.part_ml + pc.slot(b) * stride + 2 * (g0 + n);
+                                const float mn = fmaxf(m, ml[0]);
+                                l = l * __builtin_amdgcn_exp2f(m - mn) + ml[1] * __builtin_amdgcn_exp2f(ml[0] - mn);
+                                m = mn;
+                            }
+                        const float mw = across_rows_max(m);
+                        const float lw = across_rows_sum(l * __builtin_amdgcn_exp2f(m - mw));
+                        if ((t & 63) < 16) {
+                            mj[t >> 6][n] = mw;
+                            lj[t >> 6][n] = lw;
                         }
-                    const float mw = across_rows_max(m);
-                    const float lw = across_rows_sum(l * __builtin_amdgcn_exp2f(m - mw));
-                    if ((t & 63) < 16) {
-                        mj[t >> 6][n] = mw;
-                        lj[t >> 6][n] = lw;
-                    }
-                    __syncthreads();
-                    if (t < 16) {
-                        float mm = mj[0][t], ll = 0.0f;
+                        __syncthreads();
+                        if (t < 16) {
+                            float mm = mj[0][t], ll = 0.0f;
 #pragma unroll
-                        for (int k = 1; k < NW; k++) mm = fmaxf(mm, mj[k][t]);
+                            for (int k = 1; k < NW; k++) mm = fmaxf(mm, mj[k][t]);
 #pragma unroll
-                        for (int k = 0; k < NW; k++) ll = fmaf(lj[k][t], __builtin_amdgcn_exp2f(mj[k][t] - mm), ll);
-                        M[t] = mm;
-                        R[t] = ll > 0.0f ? 1.0f / ll : 0.0f;
+                            for (int k = 0; k < NW; k++) ll = fmaf(lj[k][t], __builtin_amdgcn_exp2f(mj[k][t] - mm), ll);
+                            M[g0 + t] = mm;
+                            R[g0 + t] = ll > 0.0f ? 1.0f / ll : 0.0f;
+                        }
+                        __syncthreads();
                     }
-                }
                 __syncthreads();
                 known = true;
             }
@@ -836,20 +860,20 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(StepArgs A)
         }
         id -= sums;
     }
-    const int b = (int)(id / (unsigned)A.gt), hd = (int)id - b * A.gt;
+    const int joins = min(A.gt, JOIN_HEADS), b = (int)(id / (unsigned)joins), first = (int)id - b * joins;
     if (b >= A.shares) return;
     Share sh{};
     sh.at = A.w.start[b];
     if (sh.at.all == 0) return;
     sh.bounds(b);
-    join_pieces<BF16, D>(A, sh, b, hd);
+    join_pieces<BF16, D>(A, sh, b, first);
 }
 
 size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
 // How a call is dealt out, and its workspace.
 struct Plan {
-    int G, gt, nt, P, shares, splits;
+    int G, tw, gt, nt, nt16, P, shares, splits;
     bool brief, join, sums;   // brief: the kernel of short caches (the workspace has room for shares
                               // all the same: it does not shrink with more entries)
     size_t start, part_ml, part_o, before, whole_ml, scores, bytes;   // offsets
@@ -858,11 +882,18 @@ struct Plan {
     {
         const int rows = d.io_dtype == GDNQ_IO_BF16 ? 32 : 16;
         G = d.H / d.hk;
-        gt = std::min(G, 16);
-        nt = (G + 15) / 16;
-        P = d.hk * nt;
         const long long steps = (long long)kv.max_pages * d.page / rows + 2;   // one more at each end of a window
         const long long units = (steps + NW - 1) / NW;
+        nt16 = (G + 15) / 16;
+        // More than 16 query heads to a cache head: two or four groups of 16 in a workgroup, which share
+        // the rows in the caches, or a workgroup for each, where there are not several units for each
+        // share: its piece of 64 heads is half as large as a unit (32 requests to 20000 rows, 64 heads,
+        // 106 us against 156; one of 30000, 128 heads, 48 against 30).
+        const bool wide = nt16 > 1 && (long long)n * d.hk * std::min<long long>(units, SHARES) >= 4 * SHARES;
+        tw = !wide ? 1 : nt16 == 2 ? 2 : 4;
+        gt = std::min(G, 16 * tw);
+        nt = (nt16 + tw - 1) / tw;
+        P = d.hk * nt;
         shares = (int)std::min<long long>(SHARES, (long long)n * P * std::min<long long>(units, SHARES));
         join = units > 1;
         sums = kv.acc != nullptr;
@@ -870,17 +901,17 @@ struct Plan {
         // 128 rows 8.9 and 8.8, of 256 14.5 and 10.4; 32 entries to 256 16.3 and 14.1; 128 to 128 11.7
         // and 17.2, to 256 19.6 and 27.5, to 512 35 and 41, to 1024 66 and 62; 2000 to 64 80 and 132,
         // to 512 409 and 480.
-        brief = steps - 2 <= 4 || (steps - 2 <= 16 && (long long)n * P >= 1024);
+        brief = steps - 2 <= 4 || (steps - 2 <= 16 && (long long)n * d.hk * nt16 >= 1024);
         // enough workgroups to fill the compute units, and none without rows
         const long long parts = ((long long)kv.max_pages * d.page + SUM_ROWS - 1) / SUM_ROWS;
         splits = (int)std::max(1LL, std::min(parts, 4096 / ((long long)n * d.hk)));
         const size_t u = (size_t)shares;
         start = 0;
         part_ml = up16(join || sums ? u * sizeof(Start) : 0);
-        part_o = part_ml + (join ? u * 2 * 32 * 4 : 0);
+        part_o = part_ml + (join ? u * 2 * 32 * tw * 4 : 0);
         before = part_o + up16(join ? u * 2 * gt * d.d * 4 : 0);
         whole_ml = before + up16(sums ? (size_t)n * 8 : 0);
-        scores = whole_ml + (sums ? (size_t)n * P * 32 * 4 : 0);
+        scores = whole_ml + (sums ? (size_t)n * P * 32 * tw * 4 : 0);
         bytes = scores + (sums ? (size_t)kv.n_pages * d.page * d.H * 4 + 16 : 0);
     }
 };
@@ -907,21 +938,24 @@ hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStrea
         w.scores = reinterpret_cast<float *>(ws + p.scores);
         w.spare = (size_t)c.kv.n_pages * d.page * d.H;
     }
-    const unsigned long long pairs = (unsigned long long)c.n * p.P;
-    const dim3 waves = grid_of((pairs + NW - 1) / NW, NT);
-    const unsigned long long second =
-        (p.join ? (unsigned long long)shares * p.gt : 0) + (p.sums ? (unsigned long long)c.n * d.hk * p.splits : 0);
+    const unsigned long long groups = (unsigned long long)c.n * d.hk * p.nt16;
+    const dim3 waves = grid_of((groups + NW - 1) / NW, NT);
+    const unsigned long long second = (p.join ? (unsigned long long)shares * std::min(p.gt, JOIN_HEADS) : 0) +
+                                      (p.sums ? (unsigned long long)c.n * d.hk * p.splits : 0);
     const dim3 joins = second ? grid_of(second, NT) : dim3(0);
-    StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, __builtin_ctz((unsigned)d.page), d.window, shares, p.splits,
-               d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es), wide_rows(c.o, c.ldo, es),
-               make_divisor((unsigned)p.splits), make_divisor((unsigned)d.hk), make_divisor((unsigned)p.P), 0};
+    StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, p.tw, p.nt16, __builtin_ctz((unsigned)d.page), d.window, shares,
+               p.splits, d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es), wide_rows(c.o, c.ldo, es),
+               make_divisor((unsigned)p.splits), make_divisor((unsigned)d.hk),
+               make_divisor((unsigned)(d.hk * p.nt16)), 0};
     return with_bool(d.io_dtype == GDNQ_IO_BF16, [&](auto bf) {
         return with_bool(p.sums, [&](auto sm) {
             auto go = [&](auto dd) {
                 constexpr bool B = decltype(bf)::value, S = decltype(sm)::value;
                 constexpr int D = decltype(dd)::value;
-                if (shares)
-                    hipLaunchKernelGGL((attn_kernel<B, D, S>), dim3((unsigned)shares), dim3(NT), 0, st, A);
+                if (shares && p.tw > 1)
+                    hipLaunchKernelGGL((attn_kernel<B, D, S, true>), dim3((unsigned)shares), dim3(NT), 0, st, A);
+                else if (shares)
+                    hipLaunchKernelGGL((attn_kernel<B, D, S, false>), dim3((unsigned)shares), dim3(NT), 0, st, A);
                 else {
                     A.nx = waves.x;
                     hipLaunchKernelGGL((attn_short_kernel<B, D, S>), waves, dim3(NT), 0, st, A);

@@ -74,6 +74,9 @@ CASES = [
     ("bf16", 8, 1, 128, 16, [4097, 9000, 20], 0, "hr", 0),
     ("f32", 4, 2, 64, 16, [5000], 0, "hr", 0),
     ("bf16", 4, 2, 64, 8, [9] * 300 + [2000, 1], 0, "hr", 0),
+    # many query heads to a cache head
+    ("bf16", 64, 1, 128, 64, [3000, 1, 0, 777, 130], 0, "hr", 0),
+    ("bf16", 40, 1, 64, 8, [2000, 33], 500, "rh", 3),
     # many short caches
     ("bf16", 16, 8, 128, 16, [(37 * i) % 513 for i in range(130)], 0, "hr", 0),
     ("bf16", 6, 2, 64, 8, [(11 * i) % 300 for i in range(515)], 0, "rh", 1),
@@ -99,6 +102,39 @@ def test_step(case, sums):
     call(C, H, qd, od, window=window, sums=sums)
     check(C, H, q, od.cpu(), None if not sums else C.accd.cpu(), window=window)
     assert same(C.kd, C.k) and same(C.vd, C.v) and (not sums or same(C.posd, C.pos))
+    obuf[:, off:off + H * d] = before[:, off:off + H * d]
+    assert torch.equal(obuf, before)
+
+
+WIDE = [
+    # io, H, hk, d, page, lens, window, layout, offset of the rows: caches that may hold 131072 rows
+    ("bf16", 64, 1, 128, 64, [3000, 1, 0, 777, 130], 0, "hr", 0),
+    ("bf16", 40, 1, 64, 8, [2000, 33, 5, 0], 500, "rh", 3),
+    ("bf16", 32, 1, 128, 16, [1, 128, 129, 5000], 0, "hr", 0),
+    ("f32", 66, 2, 64, 16, [700, 64, 65], 0, "hr", 0),
+    ("bf16", 130, 2, 64, 32, [400, 90, 2500], 100, "hr", 0),
+    ("bf16", 100, 1, 256, 32, [600, 5, 2000, 1], 0, "pad", 8),
+    ("f32", 32, 1, 256, 16, [300, 1000, 2, 64], 0, "hr", 0),
+    ("f32", 17, 1, 128, 64, [300, 1000, 2, 64], 70, "rh", 0),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[f"{c[0]}-{c[1]}x{c[2]}-d{c[3]}-p{c[4]}-n{len(c[5])}-w{c[6]}" for c in WIDE])
+@pytest.mark.parametrize("sums", [False, True])
+def test_many_query_heads(case, sums):
+    """More than 16 query heads to a cache head in tables wide enough for several
+    groups of 16 to share a workgroup."""
+    torch = torch_cuda()
+    io, H, hk, d, page, lens, window, layout, off = case
+    say("attention, many query heads", case, sums)
+    rng = np.random.default_rng(d + page + len(lens) + H)
+    C = Cache(rng, lens, hk, d, page, io, layout, sums=sums, max_pages=131072 // page)
+    q = rand(rng, (len(lens), H * d), io, 2.0)
+    qd, _ = strided(q, off, 8)
+    od, obuf = strided(torch.full_like(q, 0.25), off, 8)
+    before = obuf.clone()
+    call(C, H, qd, od, window=window, sums=sums)
+    check(C, H, q, od.cpu(), None if not sums else C.accd.cpu(), window=window)
     obuf[:, off:off + H * d] = before[:, off:off + H * d]
     assert torch.equal(obuf, before)
 
