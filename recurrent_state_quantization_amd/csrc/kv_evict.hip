@@ -230,15 +230,19 @@ __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
     } else {
         int shift = lo == hi ? 0 : max(0, 32 - BITS - __clz((int)(hi - lo)));
         for (;;) {
+            int same = 0;   // of `lo` itself, say rows that never had any weight, there may be many
             for (int round = 0; round < rounds; round++) {
                 again(round);
                 each(round, [&](int k) {
                     // numbers below `lo`, where there are some, are 2^24 from its other side, and shift is
                     // at most 12 then
                     const unsigned d = (key[k] - lo) >> shift;
-                    if (d < BINS && key[k] != STAYS) atomicAdd(&hist[d], 1);
+                    same += key[k] == lo;
+                    if (d < BINS && key[k] != STAYS && key[k] != lo) atomicAdd(&hist[d], 1);
                 });
             }
+            same = lanes_before(same);
+            if (lane == 63) atomicAdd(&hist[0], same);
             __syncthreads();
             int cnt[BT], sum = 0;
 #pragma unroll
