@@ -166,8 +166,9 @@ int gdnq_attn_workspace(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32_t n
  *   w_r = softmax_r(scale q . k_r),   o = sum_r w_r v_r.
  *   q, o  device io_dtype [n, H*d].  An entry without rows gives zeros.
  * With kv->acc, for every row that was attended: acc = acc_decay acc + the sum
- * of w_r over the query heads of its cache head.  Entries whose pages are
- * shared must then not be in the same call.
+ * of w_r over the query heads of its cache head.  Entries that attend to rows of
+ * one page must then not be in the same call.  (Pages that lie before every
+ * row of a window are not attended to: their table entries may be anything.)
  * workspace: device, 16-byte aligned, at least gdnq_attn_workspace bytes, free
  * for other use once the call has run; calls that may run at the same time need
  * one each.  n == 0 is a no-op.

@@ -117,6 +117,8 @@ class Kv:
         ldr = st[2] if d.page > 1 else d.d
         ldh = st[1] if hk > 1 else max(ldr * d.page, d.d)
         ldp = st[0] if n > 1 else max(ldh * hk, ldr * d.page)
+        if min(ldr, ldh, ldp) < d.d:   # three of zero would read as the default layout
+            _bad(f"the rows of k overlap (strides {st})")
         kv = _Kv(self.k.data_ptr(), self.v.data_ptr(), _flat(self.acc, n * hk * d.page, f32, cur, "acc"),
                  _flat(self.pos, n * hk * d.page, i32, cur, "pos"), _flat(self.table, slots * width, i32, cur, "table"),
                  _flat(self.lens, slots, i32, cur, "lens"),

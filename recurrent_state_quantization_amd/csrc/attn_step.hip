@@ -7,7 +7,7 @@
 // Keys and values are read once, 4 d H rows operations against them: bound by
 // HBM, so the kernel is made of loads in flight.  The query heads of a cache
 // head are the columns of a matrix product (16 at a time, the missing ones
-// zeros), so a row is read once for all of them:
+// repeats), so a row is read once for all of them:
 //
 //   S [rows x heads] = K Q^T,  then  O^T [d x heads] += V^T W^T
 //
@@ -87,7 +87,6 @@ struct Geo {
     static constexpr int VW = D / 16;                          // values of a value row in a lane,
     static constexpr int VP = VW * ES > 16 ? VW * ES / 16 : 1; // in pieces
     static constexpr int VE = VW / VP;                         // of 16 bytes (8 for 64 bf16)
-    static constexpr int UNIT = NW * ROWS;                     // rows of a unit
 };
 
 // Rows [first, len) of an entry, in steps [t0, t1) and units.
@@ -459,8 +458,10 @@ struct Steps {
 #pragma unroll
             for (int j = 0; j < J; j++) {
                 raw[j] = make_float4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
-                const int off = (t * X::ROWS + 16 * j + 4 * g) & ((1 << A.shift) - 1);
-                to[j] = ok[j] ? ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head) << A.shift) + off : A.w.spare;
+                // rows before a window or behind the last may lie on pages that are another entry's by now
+                const int r = t * X::ROWS + 16 * j + 4 * g, off = r & ((1 << A.shift) - 1);
+                const bool mine = ok[j] && r + 3 >= e.first && r < e.s.len;
+                to[j] = mine ? ((((size_t)at_v[j] * A.hk + h) * A.G + sum_head) << A.shift) + off : A.w.spare;
             }
         }
         if (edge) {
@@ -541,8 +542,8 @@ struct Steps {
 template <bool BF16, int D, bool SUMS, bool WIDE>
 __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
 {
-    const int tw = WIDE ? A.tw : 1;
     using X = Geo<BF16, D>;
+    const int tw = WIDE ? A.tw : 1;
     constexpr int DC = D < 128 ? D : 128;             // columns joined at a time
     constexpr int PC = DC / (16 * X::VE);             // in pieces of a lane
     __shared__ float mj[NW][16], lj[NW][16];

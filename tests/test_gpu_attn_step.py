@@ -215,6 +215,28 @@ def test_shared_pages():
     check(C, 4, q, o.cpu(), None)
 
 
+@pytest.mark.parametrize("io,page", [("bf16", 8), ("bf16", 16), ("f32", 8), ("bf16", 64)])
+def test_pages_before_a_window(io, page):
+    """Table entries before a window are stale: pages of other entries by now, or
+    none.  Nothing of them counts, and the others' sums are theirs alone."""
+    torch = torch_cuda()
+    say("attention, stale pages before a window", io, page)
+    rng = np.random.default_rng(page)
+    lens, window = [200 + 7 * i for i in range(24)], 45
+    C = Cache(rng, lens, 2, 64, page, io)
+    live = [set(C.table[C.slots[i], (n - window) // page:-(-n // page)].tolist()) for i, n in enumerate(lens)]
+    for i, n in enumerate(lens):
+        others = [p for j in range(24) if j != i for p in live[j]] + [-3, C.n_pages]
+        C.table[C.slots[i], :(n - window) // page] = rng.choice(others, (n - window) // page)
+    C.tabled = up(C.table)
+    q = rand(rng, (24, 8 * 64), io, 2.0)
+    for _ in range(3):
+        C.accd.copy_(C.acc)
+        o = torch.zeros(24, 8 * 64, dtype=q.dtype, device="cuda")
+        call(C, 8, q.cuda(), o, window=window)
+        check(C, 8, q, o.cpu(), C.accd.cpu(), window=window)
+
+
 def test_repeated_calls_agree():
     """The same call gives the same bits, whatever the workspace held."""
     torch = torch_cuda()
@@ -248,6 +270,9 @@ def test_a_marshalled_cache_says_what_it_is():
         C.kv(v=C.vd.transpose(1, 2).contiguous().transpose(1, 2)).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
     with pytest.raises(g.GdnqError, match="must be"):
         C.kv(k=C.kd[..., :32]).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+    with pytest.raises(g.GdnqError, match="overlap"):
+        one = C.kd[:1, :1, :1].expand(C.kd.shape)
+        C.kv(k=one, v=one).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
     with pytest.raises(g.GdnqError, match="acc has"):
         C.kv(acc=C.accd[:1]).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
     with pytest.raises(g.GdnqError, match="lens is"):
