@@ -37,7 +37,8 @@ namespace {
 
 constexpr float LOG2E = 1.44269504f, LOWEST = -3.4028234e38f;
 constexpr int NT = 256, NW = NT / 64;
-constexpr int SHARES = 512;   // workgroups at most: two for each compute unit
+constexpr int SHARES = 512;   // workgroups at most: two for each compute unit; half as many for heads of
+                              // 256, whose registers leave room for one
 constexpr int JOIN_HEADS = 16;     // workgroups at most that join a pair's heads
 constexpr int SUM_ROWS = NT * 4;   // rows of which a workgroup adds up the weights at a time
 
@@ -73,6 +74,7 @@ struct StepArgs {
     int nt16;                  // groups of 16 heads per cache head
     int shift, window;
     int shares, splits;        // 0: a wave for each pair; workgroups for the sums of an entry and cache head
+    int lg;                    // log2 of the most shares
     float scale2, decay;       // scale log2(e): weights are powers of two
     bool wide_q, wide_o;
     Divisor bySplits, byHk, byGroups;
@@ -114,18 +116,24 @@ __device__ __forceinline__ Entry entry_of(const StepArgs &A, int i)
     return slot_rows(A.c.kv, A.c.slots, i, A.shift, s) ? entry_of<ROWS>(A, s) : Entry{};
 }
 
-// The shares of `all` units: one unit each, or SHARES of them.  (A call has fewer
-// workgroups than SHARES only where its units cannot be more than these.)
-__device__ __forceinline__ int shares_of(u64 all) { return (int)min((u64)SHARES, all); }
-// First unit of share b; the share that holds unit x.
-__device__ __forceinline__ u64 share_begin(u64 all, int b)
-{
-    return all <= SHARES ? (u64)(unsigned)b : all * (unsigned)b / SHARES;
-}
-__device__ __forceinline__ int share_of(u64 all, u64 x)
-{
-    return all <= SHARES ? (int)x : (int)(((x + 1) * SHARES - 1) / all);
-}
+// `all` units in shares: one unit each, or 2^lg shares.  (A call has fewer workgroups
+// than that only where its units cannot be more than these.)
+struct Deal {
+    u64 all;
+    int lg;
+
+    __device__ __forceinline__ bool single() const { return all <= (1ull << lg); }
+    __device__ __forceinline__ int shares() const { return single() ? (int)all : 1 << lg; }
+    // first unit of share b; the share that holds unit x
+    __device__ __forceinline__ u64 begin(int b) const
+    {
+        return single() ? (u64)(unsigned)b : (all * (unsigned)b) >> lg;
+    }
+    __device__ __forceinline__ int holds(u64 x) const
+    {
+        return single() ? (int)x : (int)((((x + 1) << lg) - 1) / all);
+    }
+};
 
 // Sum over the lower threads, and over all, of the workgroup.
 __device__ __forceinline__ u64 sum_before(u64 x, u64 *part, u64 &all)
@@ -154,10 +162,11 @@ struct Share {
     u64 x, end;
     Start at;
 
-    __device__ __forceinline__ void bounds(int b)
+    __device__ __forceinline__ void bounds(int lg, int b)
     {
-        x = share_begin(at.all, b);
-        end = share_begin(at.all, b + 1);
+        const Deal d{at.all, lg};
+        x = d.begin(b);
+        end = d.begin(b + 1);
     }
 };
 
@@ -183,11 +192,11 @@ __device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh, 
     }
     sh.at.all *= (unsigned)A.P;
     mine *= (unsigned)A.P;
-    if (b >= shares_of(sh.at.all)) {
+    if (b >= Deal{sh.at.all, A.lg}.shares()) {
         sh.at.all = 0;
         return false;
     }
-    sh.bounds(b);
+    sh.bounds(A.lg, b);
     if (sh.x >= before && sh.x < before + mine) {
         int i = lo;
         u64 x = sh.x - before;
@@ -663,11 +672,11 @@ struct Pieces {
     bool inside;   // it begins inside share b0
 
     __device__ __forceinline__ Pieces(int f, int l, bool in) : b0(f), b1(l), inside(in) {}
-    __device__ __forceinline__ Pieces(u64 all, u64 begin, int units)
+    __device__ __forceinline__ Pieces(const Deal &d, u64 begin, int units)
     {
-        b0 = share_of(all, begin);
-        b1 = share_of(all, begin + (unsigned)units - 1);
-        inside = share_begin(all, b0) != begin;
+        b0 = d.holds(begin);
+        b1 = d.holds(begin + (unsigned)units - 1);
+        inside = d.begin(b0) != begin;
     }
 
     __device__ __forceinline__ size_t slot(int b) const { return 2 * (size_t)b + (b == b0 && inside); }
@@ -685,7 +694,7 @@ __device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, 
     const int t = (int)__builtin_amdgcn_workitem_id_x(), col = t % COLS, part = t / COLS;
     if (b == 0 || sh.at.u == 0) return;
     const u64 begin = sh.x - (unsigned)sh.at.u;
-    const Pieces pc(sh.at.all, begin, sh.at.units);
+    const Pieces pc(Deal{sh.at.all, A.lg}, begin, sh.at.units);
     if (pc.b0 != b - 1) return;
     const int h = sh.at.p / A.nt, first_head = (sh.at.p - h * A.nt) * A.gt, heads = min(A.gt, A.G - first_head);
     const int np = pc.b1 - pc.b0 + 1, stride = 32 * A.tw;
@@ -779,7 +788,7 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
             load(0);
             if (A.nt > 1 || !known) {   // the pair's maximum and sum
                 Pieces pc{0, 0, false};
-                if (A.shares) pc = Pieces(all, before + (u64)(p + tile) * (unsigned)e.units, e.units);
+                if (A.shares) pc = Pieces(Deal{all, A.lg}, before + (u64)(p + tile) * (unsigned)e.units, e.units);
                 __syncthreads();
                 if (pc.b0 == pc.b1) {
                     if (t < heads) {
@@ -866,7 +875,7 @@ __global__ __launch_bounds__(NT) void attn_join_kernel(StepArgs A)
     Share sh{};
     sh.at = A.w.start[b];
     if (sh.at.all == 0) return;
-    sh.bounds(b);
+    sh.bounds(A.lg, b);
     join_pieces<BF16, D>(A, sh, b, first);
 }
 
@@ -874,7 +883,7 @@ size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
 // How a call is dealt out, and its workspace.
 struct Plan {
-    int G, tw, gt, nt, nt16, P, shares, splits;
+    int G, tw, gt, nt, nt16, P, lg, shares, splits;
     bool brief, join, sums;   // brief: the kernel of short caches (the workspace has room for shares
                               // all the same: it does not shrink with more entries)
     size_t start, part_ml, part_o, before, whole_ml, scores, bytes;   // offsets
@@ -883,19 +892,24 @@ struct Plan {
     {
         const int rows = d.io_dtype == GDNQ_IO_BF16 ? 32 : 16;
         G = d.H / d.hk;
-        const long long steps = (long long)kv.max_pages * d.page / rows + 2;   // one more at each end of a window
+        const long long held = (long long)kv.max_pages * d.page;
+        const long long most = d.window ? std::min<long long>(held, d.window) : held;   // rows attended to
+        const long long steps = most / rows + 2;   // one more at each end of a window
         const long long units = (steps + NW - 1) / NW;
+        lg = d.d == 256 ? 8 : 9;
+        static_assert(SHARES == 1 << 9, "");
+        const long long cap = 1LL << lg, few = std::min(units, cap);
         nt16 = (G + 15) / 16;
         // More than 16 query heads to a cache head: two or four groups of 16 in a workgroup, which share
         // the rows in the caches, or a workgroup for each, where there are not several units for each
         // share: its piece of 64 heads is half as large as a unit (32 requests to 20000 rows, 64 heads,
         // 106 us against 156; one of 30000, 128 heads, 48 against 30).
-        const bool wide = nt16 > 1 && (long long)n * d.hk * std::min<long long>(units, SHARES) >= 4 * SHARES;
+        const bool wide = nt16 > 1 && (long long)n * d.hk * few >= 4 * cap;
         tw = !wide ? 1 : nt16 == 2 ? 2 : 4;
         gt = std::min(G, 16 * tw);
         nt = (nt16 + tw - 1) / tw;
         P = d.hk * nt;
-        shares = (int)std::min<long long>(SHARES, (long long)n * P * std::min<long long>(units, SHARES));
+        shares = (int)std::min(cap, (long long)n * P * few);
         join = units > 1;
         sums = kv.acc != nullptr;
         // A wave for each pair, or shares.  8 heads of 128 in bf16, us, waves and shares: one entry of
@@ -904,7 +918,7 @@ struct Plan {
         // to 512 409 and 480.
         brief = steps - 2 <= 4 || (steps - 2 <= 16 && (long long)n * d.hk * nt16 >= 1024);
         // enough workgroups to fill the compute units, and none without rows
-        const long long parts = ((long long)kv.max_pages * d.page + SUM_ROWS - 1) / SUM_ROWS;
+        const long long parts = (most + SUM_ROWS - 1) / SUM_ROWS;
         splits = (int)std::max(1LL, std::min(parts, 4096 / ((long long)n * d.hk)));
         const size_t u = (size_t)shares;
         start = 0;
@@ -945,7 +959,7 @@ hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStrea
                                       (p.sums ? (unsigned long long)c.n * d.hk * p.splits : 0);
     const dim3 joins = second ? grid_of(second, NT) : dim3(0);
     StepArgs A{c, w, d.H, d.hk, p.G, p.gt, p.nt, p.P, p.tw, p.nt16, __builtin_ctz((unsigned)d.page), d.window, shares,
-               p.splits, d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es), wide_rows(c.o, c.ldo, es),
+               p.splits, p.lg, d.scale * LOG2E, d.acc_decay, wide_rows(c.q, c.ldq, es), wide_rows(c.o, c.ldo, es),
                make_divisor((unsigned)p.splits), make_divisor((unsigned)d.hk),
                make_divisor((unsigned)(d.hk * p.nt16)), 0};
     return with_bool(d.io_dtype == GDNQ_IO_BF16, [&](auto bf) {
