@@ -30,10 +30,10 @@ struct AppendArgs {
     unsigned nx;      // width of the grid
 };
 
-template <bool BF16, int V, bool INTER, bool STREAM>
+template <bool BF16, bool INTER, bool STREAM>
 __global__ __launch_bounds__(NT) void kv_append_kernel(AppendArgs A)
 {
-    using P = Pack<BF16, V>;
+    constexpr int V = Row16<BF16, STREAM>::V;
     __shared__ float2 cs[MAX_ROWS][128];
     __shared__ int page[MAX_ROWS], at[MAX_ROWS], position[MAX_ROWS];
     const int t = (int)__builtin_amdgcn_workitem_id_x();
@@ -78,19 +78,19 @@ __global__ __launch_bounds__(NT) void kv_append_kernel(AppendArgs A)
         const size_t row = (size_t)(tok + r);
         if (query) {
             const int h = (int)div_by((unsigned)x, A.p.byNi);
-            turn_piece<BF16, V, INTER, STREAM>(c.q, row * c.ldq + (size_t)h * A.d, c.q_out,
+            turn_piece<BF16, INTER, STREAM>(c.q, row * c.ldq + (size_t)h * A.d, c.q_out,
                                                row * c.ldqo + (size_t)h * A.d, x - h * A.p.ni, cs[r], A.p);
             continue;
         }
         if (page[r] < 0 || page[r] >= c.kv.n_pages) continue;
         if (key) {
             const int y = x - nq, h = (int)div_by((unsigned)y, A.p.byNi);
-            turn_piece<BF16, V, INTER, false>(c.k, row * c.ldk + (size_t)h * A.d, c.kv.k,
+            turn_piece<BF16, INTER, false>(c.k, row * c.ldk + (size_t)h * A.d, c.kv.k,
                                               row_at(c.kv, page[r], h, at[r]), y - h * A.p.ni, cs[r], A.p);
         } else {
             const int y = x - nq - nk, h = (int)div_by((unsigned)y, A.byNv), j = (y - h * A.nv) * V;
-            P::template store_once<false>(c.kv.v, row_at(c.kv, page[r], h, at[r]) + j,
-                                           P::template load_once<STREAM>(c.v, row * c.ldv + (size_t)h * A.d + j));
+            const uint4 v = Row16<BF16, STREAM>::load(c.v, row * c.ldv + (size_t)h * A.d + j);
+            Row16<BF16, false>::store(c.kv.v, row_at(c.kv, page[r], h, at[r]) + j, v);
         }
     }
     for (int i = t; i < nr * A.hk; i += NT) {
@@ -107,11 +107,8 @@ hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, co
 {
     const bool bf16 = d.io_dtype == GDNQ_IO_BF16, inter = r && (r->flags & GDNQ_ROPE_INTERLEAVED);
     const int es = bf16 ? 2 : 4, rot = r ? r->rot : 0;
-    const bool wide = wide_pieces(d.d, rot, inter, es) && wide_rows(c.k, c.ldk, es) && wide_rows(c.v, c.ldv, es) &&
-                      (!c.q || (wide_rows(c.q, c.ldq, es) && wide_rows(c.q_out, c.ldqo, es)));
-    const int v = wide ? 16 / es : 1;
-    AppendArgs A{c, head_pieces(d.d, rot, inter, v), d.H, d.hk, d.d, __builtin_ctz((unsigned)d.page), 0, d.d / v, 0,
-                 r ? r->amp : 1.0f, r != nullptr, r && (r->flags & GDNQ_ROPE_INVERSE), {}, {}, 0};
+    AppendArgs A{c, head_pieces(d.d, rot, inter, bf16), d.H, d.hk, d.d, __builtin_ctz((unsigned)d.page), 0,
+                 d.d / (16 / es), 0, r ? r->amp : 1.0f, r != nullptr, r && (r->flags & GDNQ_ROPE_INVERSE), {}, {}, 0};
     A.pieces = ((c.q ? d.H : 0) + d.hk) * A.p.ni + d.hk * A.nv;
     A.byPieces = make_divisor((unsigned)A.pieces);
     A.byNv = make_divisor((unsigned)A.nv);
@@ -120,17 +117,16 @@ hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, co
     A.rows = c.cu && c.T >= 1024 ? 2 : 0;
     const dim3 grid = grid_of(c.cu ? (unsigned long long)(c.T >> A.rows) + c.n : c.n, NT);
     A.nx = grid.x;
-    const bool stream = streams(2ull * c.T * ((c.q ? d.H : 0) + 2 * d.hk) * d.d * es);
+    // rows off 16 bytes share cache lines between lanes: 128 us through the caches, 211 past them
+    const bool stream = streams(2ull * c.T * ((c.q ? d.H : 0) + 2 * d.hk) * d.d * es) && wide_rows(c.k, c.ldk, es) &&
+                        wide_rows(c.v, c.ldv, es) &&
+                        (!c.q || (wide_rows(c.q, c.ldq, es) && wide_rows(c.q_out, c.ldqo, es)));
     return with_bool(bf16, [&](auto b) {
-        return with_bool(wide, [&](auto w) {
-            return with_bool(inter, [&](auto n) {
-                return with_bool(stream, [&](auto o) {
-                    constexpr bool B = decltype(b)::value;
-                    constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
-                    constexpr bool N = decltype(n)::value, S = decltype(o)::value && V != 1;
-                    hipLaunchKernelGGL((kv_append_kernel<B, V, N, S>), grid, dim3(NT), 0, st, A);
-                    return hipGetLastError();
-                });
+        return with_bool(inter, [&](auto n) {
+            return with_bool(stream, [&](auto o) {
+                constexpr bool B = decltype(b)::value, N = decltype(n)::value, S = decltype(o)::value;
+                hipLaunchKernelGGL((kv_append_kernel<B, N, S>), grid, dim3(NT), 0, st, A);
+                return hipGetLastError();
             });
         });
     });

@@ -25,7 +25,7 @@ struct RopeArgs {
     unsigned nx;              // width of the grid
 };
 
-template <bool BF16, int V, bool INTER, bool STREAM>
+template <bool BF16, bool INTER, bool STREAM>
 __global__ __launch_bounds__(256) void rope_kernel(RopeArgs A)
 {
     __shared__ float2 cs[MAX_CS];
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void rope_kernel(RopeArgs A)
         if (h >= nh) continue;
         const size_t at = (size_t)(h0 + h) * A.d;
         const size_t row = (size_t)(r0 + r);
-        turn_piece<BF16, V, INTER, STREAM>(A.c.x, row * A.c.ldx + at, A.c.y, row * A.c.ldy + at, in_row - h * A.p.ni,
+        turn_piece<BF16, INTER, STREAM>(A.c.x, row * A.c.ldx + at, A.c.y, row * A.c.ldy + at, in_row - h * A.p.ni,
                                            cs + r * pairs, A.p);
     }
 }
@@ -62,8 +62,7 @@ hipError_t launch_rope(const gdnq_rope_desc &d, const RopeCall &c, hipStream_t s
 {
     const bool bf16 = d.io_dtype == GDNQ_IO_BF16, inter = d.flags & GDNQ_ROPE_INTERLEAVED;
     const int es = bf16 ? 2 : 4;
-    const bool wide = wide_pieces(d.d, d.rot, inter, es) && wide_rows(c.x, c.ldx, es) && wide_rows(c.y, c.ldy, es);
-    RopeArgs A{c, head_pieces(d.d, d.rot, inter, wide ? 16 / es : 1), d.d, 1, c.H, d.amp,
+    RopeArgs A{c, head_pieces(d.d, d.rot, inter, bf16), d.d, 1, c.H, d.amp,
                (d.flags & GDNQ_ROPE_INVERSE) != 0, {}, {}, {}, 0};
     // Whole rows, some 512 pieces in a workgroup (three rows of 40 heads of 128 in bf16 instead of one:
     // 124 us instead of 113), or, of few rows, the heads that give each thread a piece.
@@ -75,17 +74,15 @@ hipError_t launch_rope(const gdnq_rope_desc &d, const RopeCall &c, hipStream_t s
     A.bySplit = make_divisor(split);
     const dim3 grid = grid_of((unsigned long long)((c.rows + A.rows - 1) / A.rows) * split, 256);
     A.nx = grid.x;
-    const bool stream = streams(2ull * c.rows * c.H * d.d * es);
+    // rows off 16 bytes share cache lines between lanes: 140 us through the caches, 150 past them
+    const bool stream = streams(2ull * c.rows * c.H * d.d * es) && wide_rows(c.x, c.ldx, es) &&
+                        wide_rows(c.y, c.ldy, es);
     return with_bool(bf16, [&](auto b) {
-        return with_bool(wide, [&](auto w) {
-            return with_bool(inter, [&](auto n) {
-                return with_bool(stream, [&](auto o) {
-                    constexpr bool B = decltype(b)::value;
-                    constexpr int V = decltype(w)::value ? (B ? 8 : 4) : 1;
-                    constexpr bool N = decltype(n)::value, S = decltype(o)::value && V != 1;
-                    hipLaunchKernelGGL((rope_kernel<B, V, N, S>), grid, dim3(256), 0, st, A);
-                    return hipGetLastError();
-                });
+        return with_bool(inter, [&](auto n) {
+            return with_bool(stream, [&](auto o) {
+                constexpr bool B = decltype(b)::value, N = decltype(n)::value, S = decltype(o)::value;
+                hipLaunchKernelGGL((rope_kernel<B, N, S>), grid, dim3(256), 0, st, A);
+                return hipGetLastError();
             });
         });
     });

@@ -72,28 +72,6 @@ struct Pack {
     {
         *reinterpret_cast<raw *>(reinterpret_cast<elem *>(base) + off) = r;
     }
-
-    // the same for what is not used again soon (STREAM), past the caches
-    typedef uint32_t words __attribute__((ext_vector_type(4)));
-    template <bool STREAM>
-    __device__ __forceinline__ static raw load_once(const void *base, size_t off)
-    {
-        if constexpr (V == 1 || !STREAM) return load(base, off);
-        else {
-            const auto p = reinterpret_cast<const words *>(reinterpret_cast<const elem *>(base) + off);
-            return __builtin_bit_cast(raw, __builtin_nontemporal_load(p));
-        }
-    }
-
-    template <bool STREAM>
-    __device__ __forceinline__ static void store_once(void *base, size_t off, const raw &r)
-    {
-        if constexpr (V == 1 || !STREAM) store(base, off, r);
-        else {
-            const auto p = reinterpret_cast<words *>(reinterpret_cast<elem *>(base) + off);
-            __builtin_nontemporal_store(__builtin_bit_cast(words, r), p);
-        }
-    }
 };
 
 template <bool BF16, int V>

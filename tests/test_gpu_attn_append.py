@@ -117,3 +117,46 @@ def test_in_place_and_bad_lengths():
     pg, off = C.where(0, 17, 20)
     want[pg, :, off] = v[:3].cpu().reshape(3, 2, 64)
     assert same(C.vd, want) and sum(new) == 12
+
+
+@pytest.mark.parametrize("off", [0, 3])
+def test_long_calls(off):
+    """A call whose rows go past the caches, several tokens to a workgroup, gives
+    what calls on its sequences give, bit for bit."""
+    torch = torch_cuda()
+    g = lib()
+    say("append, long call", off)
+    new, H, hk, d, page = [2000, 1, 0, 1501, 6, 700], 32, 8, 128, 16
+    rng = np.random.default_rng(23)
+    got = []
+    T = sum(new)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    x = torch.randn(T, (H + 2 * hk) * d + off, generator=gen, device="cuda").bfloat16()[:, off:]
+    assert 2 * x.numel() * 2 > 64 << 20
+    q, k, v = x[:, :H * d], x[:, H * d:(H + hk) * d], x[:, (H + hk) * d:]
+    rope = g.RopeDesc(d=d, rot=92, flags=g.ROPE_INTERLEAVED)
+    desc, freqs = g.AttnDesc(H=H, hk=hk, d=d, page=page), table_of(rope)
+    C = Cache(rng, [m + 5 for m in new], hk, d, page, "bf16", fill=0.0)
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    for whole in (True, False):
+        kk, vv, acc, pos = C.kd.clone(), C.vd.clone(), C.accd.clone(), C.posd.clone()
+        o = torch.zeros_like(q)
+        kv = g.Kv(kk, vv, C.tabled, C.lensd, acc, pos)
+        if whole:
+            g.gdnq_kv_append(desc, rope, freqs, kv, q, o, k, v, None, C.slotsd, up(cu), len(new), T)
+        else:
+            for i, m in enumerate(new):
+                at = slice(cu[i], cu[i] + m)
+                slot = up(C.slots[i:i + 1])
+                if m:   # up to 900 tokens: one to a workgroup; the lens of a part count what lies behind it
+                    lens = C.lens.copy()
+                    for lo in range(0, m, 900):
+                        n = min(900, m - lo)
+                        lens[C.slots[i]] = C.lens[C.slots[i]] - (m - lo - n)
+                        part = slice(at.start + lo, at.start + lo + n)
+                        kv = g.Kv(kk, vv, C.tabled, up(lens), acc, pos)
+                        g.gdnq_kv_append(desc, rope, freqs, kv, q[part], o[part], k[part], v[part], None, slot,
+                                         up(np.array([0, n], np.int32)), 1, n)
+        got.append((kk, vv, acc, pos, o))
+    assert all(same(a, b) for a, b in zip(*got))

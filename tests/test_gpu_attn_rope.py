@@ -124,3 +124,29 @@ def test_gradient(inter):
         tol = 24 * L.U * 1.25 * (np.abs(f64(gy)).max() * 2 * (2 * np.abs(f64(e)).max() + 1)) * 2
         step = f64(e)[:, c] - f64(x)[:, c]
         assert np.abs(diff.sum(1) - f64(gx)[:, c] * step).max() < tol
+
+
+LONG = [("bf16", 128, 128, 0), ("f32", 66, 34, 0), ("bf16", 128, 92, 3), ("bf16", 64, 20, 8)]
+
+
+@pytest.mark.parametrize("io,d,rot,off", LONG)
+@pytest.mark.parametrize("inter", [False, True])
+def test_long_calls(io, d, rot, off, inter):
+    """A call whose rows go past the caches gives what calls on its parts give, bit for bit."""
+    torch = torch_cuda()
+    g = lib()
+    say("rope, long call", io, d, rot, off, inter)
+    rows, H = 4200, 12 * 1024 // d
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(d)
+    x = torch.randn(rows, H * d + off, generator=gen, device="cuda")
+    x = x.to(torch.bfloat16 if io == "bf16" else torch.float32)[:, off:]
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda") * 977
+    y, z = torch.zeros_like(x), torch.zeros_like(x)
+    assert 2 * x.numel() * x.element_size() > 64 << 20
+    desc = g.RopeDesc(d=d, rot=rot, io_dtype=io_of(io), flags=g.ROPE_INTERLEAVED if inter else 0)
+    t = table_of(desc)
+    g.gdnq_rope(desc, t, x, pos, y, rows, H)
+    for lo in range(0, rows, 700):
+        g.gdnq_rope(desc, t, x[lo:lo + 700], pos[lo:lo + 700], z[lo:lo + 700], 700, H)
+    assert torch.equal(y, z) and not torch.equal(x, y)
