@@ -410,6 +410,9 @@ hipError_t launch_kv_evict(const gdnq_attn_desc &d, const EvictCall &c, hipStrea
     using std::integral_constant;
     if (rows <= 256 * 16) choose(integral_constant<int, 256>{}, integral_constant<int, 16>{}, std::false_type{});
     else if (rows <= 1024 * 16) choose(integral_constant<int, 1024>{}, integral_constant<int, 16>{}, std::false_type{});
+    // 24 rows of a thread are what its registers hold; with 32, 15 of them go to memory (8 prompts of up to
+    // 20000 rows 51 and 53 us), which is still less than to form the numbers again
+    else if (rows <= 1024 * 24) choose(integral_constant<int, 1024>{}, integral_constant<int, 24>{}, std::false_type{});
     else if (rows <= 1024 * 32) choose(integral_constant<int, 1024>{}, integral_constant<int, 32>{}, std::false_type{});
     else choose(integral_constant<int, 1024>{}, integral_constant<int, 16>{}, std::true_type{});
     if (most > FEW) {
