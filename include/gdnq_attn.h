@@ -104,7 +104,7 @@ typedef struct {
     int32_t page;     /* rows per page, a power of two, 8..65536                 */
     int32_t window;   /* attention over the last `window` rows (0: all)          */
     float scale;      /* of the scores, > 0 (0: 1/sqrt(d))                       */
-    float acc_decay;  /* of the sums of weights, 0..1                            */
+    float acc_decay;  /* of the sums of weights, 0..1 (0: replaced unread)       */
 } gdnq_attn_desc;
 
 /*

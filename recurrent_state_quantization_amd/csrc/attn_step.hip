@@ -210,7 +210,7 @@ __device__ __forceinline__ bool find_share(const StepArgs &A, int b, Share &sh, 
         Entry f;
         for (;; i++) {
             f = entry_of<ROWS>(A, i);
-            if (x < (u64)(unsigned)f.units * (unsigned)A.P) break;
+            if (x < (u64)(unsigned)f.units * (unsigned)A.P || i + 1 >= hi) break;
             x -= (u64)(unsigned)f.units * (unsigned)A.P;
         }
         const int p = (int)(x / (unsigned)f.units);
@@ -244,6 +244,7 @@ __device__ __forceinline__ void for_pieces(const StepArgs &A, const Share &sh, E
             p = 0;
             do e = entry_of<ROWS>(A, ++i);   // units are left, so an entry with some follows
             while (e.units == 0 && i + 1 < A.c.n);
+            if (e.units == 0) return;        // (unless the lengths change under the call)
         }
     }
 }
@@ -850,7 +851,7 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
         if (!in) continue;
         float *acc = A.c.kv.acc + sum_at(A.hk, A.shift, page, h, off);
         if (r >= e.first && r + 4 <= e.s.len) {
-            float4 a = *reinterpret_cast<const float4 *>(acc);
+            float4 a = A.decay == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4 *>(acc);
             a.x = fmaf(A.decay, a.x, w[0]);
             a.y = fmaf(A.decay, a.y, w[1]);
             a.z = fmaf(A.decay, a.z, w[2]);
@@ -859,7 +860,8 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
         } else
 #pragma unroll
             for (int x = 0; x < 4; x++)
-                if (r + x >= e.first && r + x < e.s.len) acc[x] = fmaf(A.decay, acc[x], w[x]);
+                if (r + x >= e.first && r + x < e.s.len)
+                    acc[x] = A.decay == 0.0f ? w[x] : fmaf(A.decay, acc[x], w[x]);
     }
 }
 

@@ -173,6 +173,39 @@ def test_scales(io, scale, decay, big):
     check(C, 6, q, o.cpu(), C.accd.cpu(), scale=float(np.float32(scale)), decay=decay)
 
 
+@pytest.mark.parametrize("lens", [[300, 64, 1, 0], [70, 128, 3, 9]])
+def test_sums_replaced(lens):
+    """A decay of 0 replaces the sums without reading them."""
+    torch = torch_cuda()
+    say("attention sums replaced", lens)
+    rng = np.random.default_rng(8)
+    C = Cache(rng, lens, 2, 64, 16, "bf16")
+    q = rand(rng, (4, 6 * 64), "bf16", 2.0)
+    o = torch.zeros(4, 6 * 64, dtype=q.dtype, device="cuda")
+    C.acc.fill_(0.0)
+    C.accd.fill_(float("nan"))
+    call(C, 6, q.cuda(), o, decay=0.0)
+    got = C.accd.cpu()
+    for i in range(4):
+        pg, off = C.where(i)
+        assert not torch.isnan(got[pg, :, off]).any()
+    check(C, 6, q, o.cpu(), torch.where(torch.isnan(got), torch.zeros_like(got), got), decay=0.0)
+
+
+def test_one_slot_twice():
+    """Entries of one slot (two tokens that attend to the same rows)."""
+    torch = torch_cuda()
+    say("attention, one slot twice")
+    rng = np.random.default_rng(14)
+    C = Cache(rng, [500, 40], 2, 64, 16, "bf16", sums=False)
+    C.slots, C.lens_list = C.slots[[0, 1, 0, 0]], [500, 40, 500, 500]
+    C.slotsd = up(C.slots)
+    q = rand(rng, (4, 8 * 64), "bf16", 2.0)
+    o = torch.zeros(4, 8 * 64, dtype=q.dtype, device="cuda")
+    call(C, 8, q.cuda(), o, sums=False)
+    check(C, 8, q, o.cpu(), None)
+
+
 def test_equal_and_low_scores():
     """Equal rows share the weight; scores near the type's lowest value, and among them one high one."""
     torch = torch_cuda()
