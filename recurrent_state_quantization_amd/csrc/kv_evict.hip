@@ -23,6 +23,7 @@ namespace gdnq {
 namespace {
 
 constexpr int FEW = 64;   // moves that the choosing workgroup makes itself
+constexpr int HELD = 1024 * 32;   // rows whose numbers a workgroup holds in registers
 constexpr unsigned STAYS = 0xFFFFFFFFu;   // the number of protected rows, above all others
 
 // A row's numbers before and behind a move.
@@ -36,6 +37,8 @@ struct EvictArgs {
     int pieces;            // 16-byte pieces of a row; ldp, ldh and ldr count such pieces here
     int *count;            // [n hk]: moves left to the second kernel
     Move *moves;           // [n hk][most]
+    unsigned *keys;        // [n hk][rows of a slot]: the rows' numbers, where registers do not hold them
+    int rows;
     Divisor byHk, bySplit;
     unsigned nx;
 };
@@ -80,7 +83,8 @@ __device__ __forceinline__ int lanes_before(int x)
 
 // NT threads of K rows each, four consecutive ones (16 bytes, in one page) of
 // every NT * 4 rows; more rows than NT K (MANY) in several rounds, whose numbers
-// are formed again in every pass.
+// go to the workspace once they are formed (2 entries of 70000 rows down to 30000
+// 153 us; formed again in every pass 181).
 template <int NT, int K, bool MANY>
 __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
 {
@@ -148,11 +152,26 @@ __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
             key[k] = stay ? STAYS : order_of(__uint_as_float(key[k]));
         });
     };
-    auto again = [&](int round) {
+    unsigned *const keys = MANY ? A.keys + (size_t)id * A.rows : nullptr;
+    auto form = [&](int round) {
         if constexpr (MANY) {
             load(round);
             number(round);
+            each(round, [&](int k) {
+                if (k % 4 == 3 && row(round, k - 3) < n)
+                    *reinterpret_cast<uint4 *>(keys + row(round, k - 3)) =
+                        make_uint4(key[k - 3], key[k - 2], key[k - 1], key[k]);
+            });
         }
+    };
+    auto again = [&](int round) {
+        if constexpr (MANY)
+            each(round, [&](int k) {
+                if (k % 4) return;
+                uint4 x = make_uint4(STAYS, STAYS, STAYS, STAYS);
+                if (row(round, k) < n) x = *reinterpret_cast<const uint4 *>(keys + row(round, k));
+                key[k] = x.x; key[k + 1] = x.y; key[k + 2] = x.z; key[k + 3] = x.w;
+            });
     };
 
     if (t == 0) {
@@ -174,13 +193,13 @@ __global__ __launch_bounds__(NT) void kv_evict_kernel(EvictArgs A)
     if (lane == 0) atomicMax(&top, newest);
     __syncthreads();
     newest = top;
-    number(0);
+    if constexpr (!MANY) number(0);
 
     // the range of the rows that are not protected (hi: one more), and how many these are
     unsigned lo = STAYS, hi = 0;
     int free = 0;
     for (int round = 0; round < rounds; round++) {
-        again(round);
+        form(round);
         each(round, [&](int k) {
             lo = min(lo, key[k]);
             hi = max(hi, key[k] + 1);   // 0 of a protected row
@@ -378,12 +397,19 @@ int most_moves(const gdnq_attn_desc &d, const gdnq_kv &kv, int budget)
 
 size_t up16(size_t x) { return (x + 15) / 16 * 16; }
 
+// The moves' part of the workspace, behind which the numbers are.
+size_t moves_bytes(size_t heads, size_t most)
+{
+    return most <= FEW ? 0 : up16(heads * 4) + up16(heads * most * sizeof(Move));
+}
+
 }  // namespace
 
 size_t kv_evict_workspace(const gdnq_attn_desc &d, const gdnq_kv &kv, int budget, int n)
 {
-    const size_t heads = (size_t)n * d.hk, most = (size_t)most_moves(d, kv, budget);
-    return most <= FEW ? 0 : up16(heads * 4) + heads * most * sizeof(Move);
+    const size_t heads = (size_t)n * d.hk, rows = (size_t)kv.max_pages * d.page;
+    const size_t most = (size_t)most_moves(d, kv, budget);
+    return most == 0 ? 0 : moves_bytes(heads, most) + (rows > HELD ? heads * rows * 4 : 0);
 }
 
 hipError_t launch_kv_evict(const gdnq_attn_desc &d, const EvictCall &c, hipStream_t st)
@@ -392,7 +418,7 @@ hipError_t launch_kv_evict(const gdnq_attn_desc &d, const EvictCall &c, hipStrea
     if (most == 0) return hipSuccess;   // no slot holds more than the budget
     const unsigned long long heads = (unsigned long long)c.n * d.hk;
     const int rows = c.kv.max_pages * d.page;
-    EvictArgs A{c, d.hk, __builtin_ctz((unsigned)d.page), most, d.d / per, nullptr, nullptr,
+    EvictArgs A{c, d.hk, __builtin_ctz((unsigned)d.page), most, d.d / per, nullptr, nullptr, nullptr, rows,
                 make_divisor((unsigned)d.hk), {}, 0};
     A.c.kv.ldp /= per;
     A.c.kv.ldh /= per;
@@ -401,6 +427,8 @@ hipError_t launch_kv_evict(const gdnq_attn_desc &d, const EvictCall &c, hipStrea
         A.count = static_cast<int *>(c.ws);
         A.moves = reinterpret_cast<Move *>(static_cast<char *>(c.ws) + up16(heads * 4));
     }
+    if (rows > HELD)
+        A.keys = reinterpret_cast<unsigned *>(static_cast<char *>(c.ws) + moves_bytes(heads, (size_t)most));
     auto choose = [&](auto nt, auto k, auto many) {
         constexpr int NT = decltype(nt)::value;
         const dim3 grid = grid_of(heads, NT);
@@ -413,7 +441,7 @@ hipError_t launch_kv_evict(const gdnq_attn_desc &d, const EvictCall &c, hipStrea
     // 24 rows of a thread are what its registers hold; with 32, 15 of them go to memory (8 prompts of up to
     // 20000 rows 51 and 53 us), which is still less than to form the numbers again
     else if (rows <= 1024 * 24) choose(integral_constant<int, 1024>{}, integral_constant<int, 24>{}, std::false_type{});
-    else if (rows <= 1024 * 32) choose(integral_constant<int, 1024>{}, integral_constant<int, 32>{}, std::false_type{});
+    else if (rows <= HELD) choose(integral_constant<int, 1024>{}, integral_constant<int, 32>{}, std::false_type{});
     else choose(integral_constant<int, 1024>{}, integral_constant<int, 16>{}, std::true_type{});
     if (most > FEW) {
         const int at_once = 256 / A.pieces;

@@ -50,6 +50,9 @@ CASES = [
     ("bf16", 1, 64, 16, [70000], 30000, 1, 1, "hr"),
     ("bf16", 2, 64, 8, [20] * 200, 13, 1, 3, "hr"),
     ("bf16", 1, 64, 8, [33000], 32900, 0, 0, "hr"),
+    ("bf16", 1, 64, 8, [33000], 32999, 3, 50, "hr"),
+    ("bf16", 2, 64, 16, [40003, 36000, 35001], 35000, 4, 50, "rh"),
+    ("f32", 3, 64, 64, [65536, 100], 90, 0, 7, "hr"),
     ("bf16", 1, 64, 32, [20000, 17001], 9000, 4, 100, "hr"),
     ("bf16", 1, 64, 16, [30001, 32768, 5], 2000, 0, 64, "hr"),
 ]
