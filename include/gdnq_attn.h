@@ -113,6 +113,9 @@ typedef struct {
  * consecutive elements at
  *   k + p ldp + h ldh + (r % page) ldr.
  * ldp, ldh and ldr are multiples of 16 bytes; all 0: [n_pages,hk,page,d].
+ * k and v may be one pool, between each other's pages, heads or rows (such as
+ * [n_pages,2,hk,page,d]), where no row of the one shares a byte with one of the
+ * other.
  * acc and pos belong to rows and heads too: [n_pages,hk,page] each.
  *   acc  the attention weight that the row has received, or NULL
  *   pos  the position of its token, or NULL

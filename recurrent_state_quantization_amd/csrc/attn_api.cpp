@@ -122,15 +122,49 @@ int check_sizes(const gdnq_attn_desc &d, const gdnq_kv *cache, gdnq_kv &kv)
     return GDNQ_OK;
 }
 
-// The cache's buffers; `use` of k and v, `more` of acc and pos.
+// n copies of what the next level describes, ld bytes apart (at least as far as one of them reaches).
+struct Level {
+    int64_t n, ld;
+};
+
+// Whether two arrangements of rows of `len` bytes, the second x bytes behind the first, share no byte.
+bool copies_apart(const Level *level, int levels, int64_t x, int64_t len)
+{
+    if (levels == 0) return x >= len || x <= -len;
+    if (level->n == 1) return copies_apart(level + 1, levels - 1, x, len);
+    // a copy reaches only those of the other arrangement that begin at most ld before or behind it
+    const int64_t below = x / level->ld - (x % level->ld < 0);
+    for (int64_t a = below; a <= below + 1; a++)
+        if (a > -level->n && a < level->n && !copies_apart(level + 1, levels - 1, x - a * level->ld, len)) return false;
+    return true;
+}
+
+// Whether no row of k shares a byte with one of v (the two of them in one pool, by pages, heads or rows).
+bool rows_apart(const gdnq_attn_desc &d, const gdnq_kv &kv)
+{
+    const int es = item(d.io_dtype);
+    const Level heads{d.hk, kv.ldh * es}, rows{d.page, kv.ldr * es};
+    const bool outer = d.hk == 1 || kv.ldh >= (d.page - 1) * kv.ldr + d.d;   // heads around rows
+    const Level level[3] = {{kv.n_pages, kv.ldp * es}, outer ? heads : rows, outer ? rows : heads};
+    const int64_t x = reinterpret_cast<intptr_t>(kv.v) - reinterpret_cast<intptr_t>(kv.k);
+    return copies_apart(level, 3, x, (int64_t)d.d * es);
+}
+
+// The cache's buffers and their uses (`use` of k and v).
 int check_cache(const gdnq_attn_desc &d, const gdnq_kv &kv, Use use, Use acc, Use pos, Spans &sp)
 {
     const int es = item(d.io_dtype);
     size_t n = bytes((size_t)(kv.n_pages - 1), (size_t)kv.ldp, es);
     n += bytes((size_t)(d.hk - 1), (size_t)kv.ldh, es) + bytes((size_t)(d.page - 1), (size_t)kv.ldr, es) +
          (size_t)d.d * es;
+    Spans others = sp;
     TRY(flat(sp, kv.k, n, "kv.k", use));
-    TRY(flat(sp, kv.v, n, "kv.v", use));
+    if (use == WRITE && kv.v && gdnq::overlap(Span{kv.k, n, ""}, Span{kv.v, n, ""}) && rows_apart(d, kv)) {
+        TRY(flat(others, kv.v, n, "kv.v", use));
+        sp.s[sp.n] = others.s[others.n - 1];
+        sp.out[sp.n++] = true;
+    } else
+        TRY(flat(sp, kv.v, n, "kv.v", use));
     const size_t m = bytes(kv.n_pages, d.hk, d.page, 4);
     TRY(flat(sp, kv.acc, m, "kv.acc", acc, true));
     TRY(flat(sp, kv.pos, m, "kv.pos", pos, true));

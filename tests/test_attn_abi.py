@@ -349,6 +349,65 @@ def test_append_takes_columns_of_the_same_rows(g):
         assert rc == 3, (rc, m)
 
 
+# keys and values in one pool of 40 pages of 16 rows, 2 heads, 64 bf16 values: ldp, ldh, ldr, and where v is, in
+# elements behind k
+POOLS = {"pages": (4096, 1024, 64, 2048), "heads": (4096, 2048, 64, 1024), "rows": (4096, 2048, 128, 64),
+         "pages of rows of heads": (4096, 64, 128, 2048), "rows of heads": (4096, 64, 256, 128),
+         "heads of rows": (4096, 128, 256, 64), "v first": (4096, 1024, 64, -2048),
+         "gaps": (8192, 64, 256, 4096 + 128), "pages behind": (4096, 1024, 64, 5 * 4096 + 2048)}
+
+
+@pytest.mark.parametrize("pool", POOLS)
+@pytest.mark.parametrize("call", ["append", "evict"])
+def test_one_pool_of_keys_and_values(g, call, pool):
+    """Past the argument checks, to the launch (which fails here, without a GPU)."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("checks only")
+    ldp, ldh, ldr, by = POOLS[pool]
+    at = BASE + (20 << 36)
+    rc, m = CALLS[call](g, kvk=at, kvv=at + 2 * by, kv=dict(ldp=ldp, ldh=ldh, ldr=ldr))
+    assert rc == 3, (rc, m)
+
+
+def _meet(ldp, ldh, ldr, by, d=64, n_pages=40, hk=2, page=16):
+    rows = sorted(p * ldp + h * ldh + r * ldr for p in range(n_pages) for h in range(hk) for r in range(page))
+    both = sorted([(x, 0) for x in rows] + [(x + by, 1) for x in rows])
+    return any(b[0] - a[0] < d for a, b in zip(both, both[1:]))
+
+
+@pytest.mark.parametrize("ld", sorted({p[:3] for p in POOLS.values()}))
+def test_pools_whose_rows_meet(g, ld):
+    """Every distance of v from k, in pieces of 16 bytes: refused where a row of the one
+    meets a row of the other (found row by row), and only there."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("checks only")
+    at, seen = BASE + (20 << 36), set()
+    kv = dict(ldp=ld[0], ldh=ld[1], ldr=ld[2])
+    for by in [*range(-400, 401, 8), *range(ld[0] - 136, ld[0] + 137, 8), *range(ld[0] // 2 - 72, ld[0] // 2 + 73, 8),
+               *range(39 * ld[0] - 72, 40 * ld[0], 1016), *range(-38 * ld[0] - 640, -37 * ld[0], 328)]:
+        rc, m = _evict(g, kvk=at, kvv=at + 2 * by, kv=kv)
+        meet = _meet(*ld, by)
+        assert (rc == 1 and "kv.v overlaps kv.k" in m) if meet else rc == 3, (by, rc, m)
+        seen.add(meet)
+    assert seen == {False, True}
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(acc=BASE + (20 << 36) + 4096), "kv.acc overlaps kv.k"),
+    (dict(acc=BASE + (20 << 36) + 80 * 4096 - 16), "kv.acc overlaps kv.v"),
+    (dict(slots=BASE + (20 << 36) + 80 * 4096 - 16), "kv.v overlaps slots"),
+    (dict(lens=BASE + (20 << 36) + 80 * 4096 - 16), "kv.lens overlaps kv.v"),
+])
+def test_one_pool_beside_others(g, kw, msg):
+    """A pool of both overlaps no other buffer (the last values lie behind the last keys)."""
+    at = BASE + (20 << 36)
+    for call in ("append", "evict"):
+        rc, m = CALLS[call](g, kvk=at, kvv=at + 4096, kv=dict(ldp=4096, ldh=1024, ldr=64), **kw)
+        assert rc == 1 and msg in m, (rc, m)
+
+
 def test_no_ops(g):
     """Calls of nothing touch no pointer."""
     assert _rope(g, rows=0, x=None, y=None)[0] == 0

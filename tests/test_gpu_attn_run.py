@@ -140,6 +140,50 @@ def test_prompts_then_tokens():
                 assert len(p) == m and set(range(max(0, s - A.recent), s)) <= p and set(range(min(A.sink, s))) <= p
 
 
+# a pool of both caches: its shape, made from pages n, heads h, rows r, values d and "2", with keys and values there
+ORDERS = ["n2hrd", "nh2rd", "nhr2d", "nr2hd", "nrh2d", "n2rhd"]
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_one_pool_of_keys_and_values(order, io):
+    """Keys and values between each other's pages, heads or rows give what two pools give, bit for bit."""
+    torch = torch_cuda()
+    say("attention, one pool", order, io)
+    A, B = Layer(5, 31, io), Layer(5, 31, io)
+    C = B.C
+    size = dict(zip("n2hrd", (C.n_pages, 2, B.hk, B.page, B.d)))
+    pool = torch.full([size[x] for x in order], float("nan"), dtype=C.kd.dtype, device="cuda")
+    k, v = (pool.select(order.index("2"), i).permute([order.replace("2", "").index(x) for x in "nhrd"]) for i in (0, 1))
+    k.copy_(C.kd)
+    v.copy_(C.vd)
+    C.kd, C.vd = k, v
+    B.kv = C.kv().c(B.desc)
+    rng = np.random.default_rng(32)
+    width = (A.H + 2 * A.hk) * A.d
+    prompt = [30, 0, 70, 96, 1]
+    cu = up(np.concatenate([[0], np.cumsum(prompt)]).astype(np.int32))
+    x = rand(rng, (sum(prompt), width), io).cuda()
+    tokens = [rand(rng, (5, width), io).cuda() for _ in range(20)]
+    seen = []
+    for M in (A, B):
+        M.C.lensd[M.slot_index] = up(np.array(prompt, np.int32))
+        nq, nk = M.H * M.d, M.hk * M.d
+        y = x.clone()
+        M.g.gdnq_kv_append(M.desc, M.rope, M.freqs, M.kv, y[:, :nq], y[:, :nq], y[:, nq:nq + nk], y[:, nq + nk:], None,
+                           M.C.slotsd, cu, 5, sum(prompt))
+        M.seen.copy_(up(np.array(prompt, np.int32)))
+        M.g.gdnq_kv_evict(M.desc, M.kv, M.budget, M.sink, M.recent, M.C.slotsd, 5, M.ws)
+        M.C.lensd.clamp_(max=M.budget)
+        o = torch.empty(5, nq, dtype=x.dtype, device="cuda")
+        got = [y, *M.state()]
+        for t in tokens:
+            M.token(t.clone(), o)
+            got += [o.clone(), *M.state()]
+        seen.append(got)
+    assert all(same(a, b) for a, b in zip(*seen))
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_graph_replays(io):
     """A token's calls captured once and replayed, with eager work of the same
