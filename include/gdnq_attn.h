@@ -168,6 +168,8 @@ int gdnq_attn_workspace(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32_t n
  * lens of them, or the last `window`; the token's own row is there already):
  *   w_r = softmax_r(scale q . k_r),   o = sum_r w_r v_r.
  *   q, o  device io_dtype [n, H*d].  An entry without rows gives zeros.
+ * NaN in a query, or in a key that is attended to, makes the outputs and sums of
+ * its heads NaN, whatever else is in the call.
  * With kv->acc, for every row that was attended: acc = acc_decay acc + the sum
  * of w_r over the query heads of its cache head.  Entries that attend to rows of
  * one page must then not be in the same call.  (Pages that lie before every

@@ -269,6 +269,10 @@ __device__ __forceinline__ float across_rows_sum(float x)
     return a + b;
 }
 
+// A sum of weights as a divisor: of no rows, where there is nothing to divide, not 0; of others, whose largest
+// weight is 1, as it is.  A NaN stays one: a comparison, compiled for arithmetic without NaN, may make it no rows.
+__device__ __forceinline__ float divisor(float l) { return l + 0x1p-100f; }
+
 // 16 bytes.  What is read once is kept out of the caches' way (64 requests to 32768
 // rows 410 -> 366 us, 5.8 -> 6.5 TB/s); what several waves read (AGAIN) is not (32
 // requests to 20000 rows, 64 query heads to a cache head, 145 -> 106 us).
@@ -617,7 +621,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_kernel(StepArgs A)
                 }
                 const int at = c0 / PC * DC + col;
                 if (whole)
-                    store1<BF16>(A.c.o, (size_t)i * A.c.ldo + (size_t)(hq + hd) * D + at, L > 0.0f ? y / L : 0.0f);
+                    store1<BF16>(A.c.o, (size_t)i * A.c.ldo + (size_t)(hq + hd) * D + at, y / divisor(L));
                 else
                     A.w.part_o[(slot * A.gt + hd) * D + at] = y;
                 if (c0 == 0 && col == 0 && (SUMS || !whole)) {
@@ -653,7 +657,7 @@ __global__ __launch_bounds__(NT, D == 256 ? 1 : 2) void attn_short_kernel(StepAr
         ml[0] = st.m;
         ml[1] = st.l;
     }
-    const float f = st.l > 0.0f ? 1.0f / st.l : 0.0f;
+    const float f = 1.0f / divisor(st.l);
 #pragma unroll
     for (int c = 0; c < X::VP; c++)
 #pragma unroll
@@ -750,7 +754,7 @@ __device__ __forceinline__ void join_pieces(const StepArgs &A, const Share &sh, 
                 const float4 x = oj[k][t];
                 y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
             }
-            const float r = L > 0.0f ? 1.0f / L : 0.0f;
+            const float r = 1.0f / divisor(L);
             const size_t to = (size_t)sh.at.i * A.c.ldo + (size_t)(h * A.G + first_head + hd) * D + 4 * t;
             store1<BF16>(A.c.o, to, y.x * r);
             store1<BF16>(A.c.o, to + 1, y.y * r);
@@ -802,7 +806,7 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
                     if (t < heads) {
                         const float *ml = A.w.whole_ml + ((size_t)i * A.P + p + tile) * stride + 2 * t;
                         M[t] = ml[0];
-                        R[t] = ml[1] > 0.0f ? 1.0f / ml[1] : 0.0f;
+                        R[t] = 1.0f / divisor(ml[1]);
                     }
                 } else
                     for (int g0 = 0; g0 < heads; g0 += 16) {
@@ -828,7 +832,7 @@ __device__ __forceinline__ void add_weights(const StepArgs &A, unsigned id)
 #pragma unroll
                             for (int k = 0; k < NW; k++) ll = fmaf(lj[k][t], __builtin_amdgcn_exp2f(mj[k][t] - mm), ll);
                             M[g0 + t] = mm;
-                            R[g0 + t] = ll > 0.0f ? 1.0f / ll : 0.0f;
+                            R[g0 + t] = 1.0f / divisor(ll);
                         }
                         __syncthreads();
                     }

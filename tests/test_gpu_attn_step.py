@@ -233,6 +233,46 @@ def test_equal_and_low_scores():
     assert np.array_equal(got[2], np.stack([v[2][150]] * 2))
 
 
+SICK = [
+    # rows of the entries, pages of a table, query heads: a wave for each pair, pieces of pairs in several shares,
+    # several pairs in a share, the same with several groups of query heads in a workgroup
+    ("waves", [100, 7, 128], 8, 16), ("pieces", [600, 40], 60, 16), ("whole", [600] + [590] * 520, 40, 16),
+    ("groups", [600] + [590] * 120, 40, 80),
+]
+
+
+@pytest.mark.parametrize("what,lens,width,H", SICK, ids=[c[0] for c in SICK])
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("where", ["key", "query"])
+def test_nan_stays_seen(what, lens, width, H, io, where):
+    """NaN in a key or a query reaches the outputs and sums of its heads, however the
+    call is dealt out, and nothing else."""
+    torch = torch_cuda()
+    say("attention with NaN", what, io, where)
+    rng = np.random.default_rng(23)
+    C = Cache(rng, lens, 2, 64, 16, io, max_pages=width)
+    n, G = len(lens), H // 2
+    q = rand(rng, (n, H * 64), io, 2.0)
+    seen = []
+    for sick in (False, True):
+        if sick and where == "key":
+            pg, off = C.where(0)
+            C.kd[int(pg[70]), 1, int(off[70]), 5] = float("nan")
+        if sick and where == "query":
+            q[0, (G + 3) * 64 + 9] = float("nan")
+        C.accd.copy_(C.acc)
+        o = torch.zeros(n, H * 64, dtype=q.dtype, device="cuda")
+        call(C, H, q.cuda(), o)
+        seen.append((o.reshape(n, H, 64).cpu(), C.accd.cpu()))
+    (o0, a0), (o1, a1) = seen
+    heads = range(G, H) if where == "key" else [G + 3]
+    assert torch.isnan(o1[0, list(heads)]).all() and not torch.isnan(o0).any()
+    pg, off = C.where(0)
+    assert torch.isnan(a1[pg, 1, off]).all() and not torch.isnan(a0[pg, 1, off]).any()
+    o1[0, list(heads)], a1[pg, 1, off] = o0[0, list(heads)], a0[pg, 1, off]
+    assert same(o1, o0) and same(a1, a0)
+
+
 def test_shared_pages():
     """Entries that share the pages of a common beginning."""
     torch = torch_cuda()
