@@ -104,13 +104,13 @@ int check_sizes(const gdnq_attn_desc &d, const gdnq_kv *cache, gdnq_kv &kv)
         kv.ldp = d.hk * kv.ldh;
     }
     const int es = item(d.io_dtype);
-    const int64_t far = (int64_t)1 << 48;   // keeps the sums below in range
+    const int64_t far = (int64_t)1 << 48;
     if (kv.ldp < 0 || kv.ldh < 0 || kv.ldr < 0 || kv.ldp > far || kv.ldh > far || kv.ldr > far)
         return fail(GDNQ_EINVAL, "ldp, ldh and ldr must be in 0..2^48");
     if (kv.ldp * es % 16 || kv.ldh * es % 16 || kv.ldr * es % 16)
         return fail(GDNQ_EINVAL, "ldp, ldh and ldr must be multiples of 16 bytes");
-    // heads around rows, or rows around heads, in pages
-    const int64_t heads = d.hk - 1, rows = d.page - 1;
+    // heads around rows, or rows around heads, in pages; in 128 bits, which no product leaves
+    const __int128 heads = d.hk - 1, rows = d.page - 1;
     if (rows && heads && kv.ldh >= (int64_t)1 << 40 && kv.ldr >= (int64_t)1 << 40)
         return fail(GDNQ_EINVAL, "ldh and ldr are both larger than any page");
     const bool hr = kv.ldr >= d.d && (!heads || kv.ldh >= rows * kv.ldr + d.d);

@@ -337,6 +337,24 @@ def test_workspaces(g):
     assert isinstance(kv, attn._Kv)
 
 
+@pytest.mark.parametrize("desc,kv,msg", [
+    (dict(page=65536), dict(ldp=2 ** 48, ldh=64, ldr=2 ** 48, max_pages=1), "pages overlap"),
+    (dict(page=32768), dict(ldp=2 ** 48, ldh=2 ** 39, ldr=2 ** 48, max_pages=1), "pages overlap"),
+    (dict(page=65536), dict(ldp=2 ** 48, ldh=2 ** 39, ldr=2 ** 48 - 128, max_pages=1), "pages overlap"),
+    (dict(H=2 ** 30, hk=2 ** 30), dict(ldp=2 ** 48, ldh=2 ** 40, ldr=64), "pages overlap"),
+    (dict(H=2 ** 30, hk=2 ** 30), dict(ldp=2 ** 48, ldh=2 ** 34, ldr=2 ** 48), "rows of a page overlap"),
+    (dict(H=2 ** 31 - 1, hk=2 ** 31 - 1, page=8), dict(ldp=2 ** 48, ldh=2 ** 33, ldr=2 ** 39), "rows of a page overlap"),
+])
+def test_far_distances(g, desc, kv, msg):
+    """Distances whose products with the sizes leave 64 bits are refused by what they are."""
+    d = g.AttnDesc(**{**dict(H=6, hk=2, d=64, page=16), **desc}).c()
+    c, out = _cache(_bufs(KV, {}), kv), ctypes.c_size_t()
+    for rc in (g.lib.gdnq_attn_workspace(d, c, 1, ctypes.byref(out)),
+               g.lib.gdnq_kv_evict_workspace(d, c, 64, 1, ctypes.byref(out))):
+        rc, m = _err(g, rc)
+        assert rc == 1 and msg in m, (rc, m)
+
+
 def test_append_takes_columns_of_the_same_rows(g):
     """q turned in place beside k and v: past the argument checks, to the launch
     (which fails here, without a GPU, or would fault on these addresses with one: not run there)."""
