@@ -190,6 +190,20 @@ int check_budget(int32_t budget)
     return GDNQ_OK;
 }
 
+// Sizes that the workspaces are counted with.
+int check_step_sizes(const gdnq_attn_desc &d, const gdnq_kv &kv, int32_t n)
+{
+    TRY(check_grid((unsigned long long)n * d.H, "n*H"));
+    if (kv.acc && bytes(kv.n_pages, d.page, d.H, 4) >= HUGE_SPAN)
+        return fail(GDNQ_EINVAL, "the scores of H heads over the pool's rows are larger than any memory");
+    return GDNQ_OK;
+}
+
+int check_evict_sizes(const gdnq_attn_desc &d, int32_t n)
+{
+    return check_grid((unsigned long long)n * d.hk * 16, "n*hk");
+}
+
 int check_workspace(void *p, size_t got, size_t need, Spans &sp)
 {
     if (got < need) return fail(GDNQ_EINVAL, "workspace of %zu bytes is too small (%zu are needed)", got, need);
@@ -329,6 +343,7 @@ int gdnq_attn_workspace(const gdnq_attn_desc *desc, const gdnq_kv *cache, int32_
     TRY(check_sizes(d, cache, kv));
     TRY(check_entries(n));
     if (!bytes_out) return fail(GDNQ_EINVAL, "bytes_out is NULL");
+    TRY(check_step_sizes(d, kv, n));
     *bytes_out = n == 0 ? 0 : gdnq::attn_workspace(d, kv, n);
     return ok();
 }
@@ -348,7 +363,7 @@ int gdnq_attn_step(const gdnq_attn_desc *desc, const gdnq_kv *cache, const void 
     TRY(check_cache(d, kv, READ, WRITE, READ, sp));
     TRY(rows(sp, q, n, (long long)d.H * d.d, ldq, es, "q"));
     TRY(rows(sp, o, n, (long long)d.H * d.d, ldo, es, "o", WRITE));
-    TRY(check_grid((unsigned long long)n * d.H, "n*H"));
+    TRY(check_step_sizes(d, kv, n));
     TRY(check_workspace(workspace, workspace_bytes, gdnq::attn_workspace(d, kv, n), sp));
     const gdnq::AttnCall c{kv, q, o, slots, ldq, ldo, n, workspace};
     return launched(gdnq::launch_attn_step(d, c, stream_of(stream)));
@@ -364,6 +379,7 @@ int gdnq_kv_evict_workspace(const gdnq_attn_desc *desc, const gdnq_kv *cache, in
     TRY(check_budget(budget));
     TRY(check_entries(n));
     if (!bytes_out) return fail(GDNQ_EINVAL, "bytes_out is NULL");
+    TRY(check_evict_sizes(d, n));
     *bytes_out = n == 0 ? 0 : gdnq::kv_evict_workspace(d, kv, budget, n);
     return ok();
 }
@@ -385,7 +401,7 @@ int gdnq_kv_evict(const gdnq_attn_desc *desc, const gdnq_kv *cache, int32_t budg
     Spans sp;
     TRY(check_slots(kv, slots, n, sp));
     TRY(check_cache(d, kv, WRITE, WRITE, WRITE, sp));
-    TRY(check_grid((unsigned long long)n * d.hk * 16, "n*hk"));
+    TRY(check_evict_sizes(d, n));
     TRY(check_workspace(workspace, workspace_bytes, gdnq::kv_evict_workspace(d, kv, budget, n), sp));
     const gdnq::EvictCall c{kv, slots, budget, sink, recent, n, workspace};
     return launched(gdnq::launch_kv_evict(d, c, stream_of(stream)));

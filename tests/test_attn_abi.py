@@ -355,6 +355,35 @@ def test_far_distances(g, desc, kv, msg):
         assert rc == 1 and msg in m, (rc, m)
 
 
+def test_workspaces_beyond_any_memory(g):
+    """Sizes that 64 bits do not count are refused, by the calls too; none is answered with a small one."""
+    out = ctypes.c_size_t()
+
+    def sizes(desc, kv, n, budget=64):
+        d = g.AttnDesc(**{**dict(H=6, hk=2, d=64, page=16), **desc}).c()
+        c = _cache(_bufs(KV, {}), kv)
+        return (_err(g, g.lib.gdnq_attn_workspace(d, c, n, ctypes.byref(out))), out.value,
+                _err(g, g.lib.gdnq_kv_evict_workspace(d, c, budget, n, ctypes.byref(out))), out.value)
+
+    # 2^31 pages of 2^16 rows, 2^21 heads over one: the scores' bytes are a multiple of 2^64 and a little
+    for desc, pages in ((dict(H=2 ** 20, hk=1, page=65536), 2 ** 31 - 1), (dict(H=2 ** 21, hk=1, page=65536), 2 ** 30),
+                        (dict(H=2 ** 31 - 1, hk=1), 2 ** 31 - 1)):
+        grid = desc["H"] <= 0x7ffffff0   # heads that a grid holds (the first refusal, with sums or without)
+        (rc, m), *_ = sizes(desc, dict(n_pages=pages, max_pages=1), 1)
+        assert rc == 1 and ("larger than any memory" if grid else "n*H") in m, (rc, m)
+        assert sizes(desc, dict(n_pages=pages, max_pages=1, acc=None), 1)[0][0] == (0 if grid else 1)
+    kv = dict(n_pages=2 ** 30, max_pages=1)
+    rc, m = _step(g, desc=dict(H=2 ** 21, hk=1, page=65536), kv=kv, n=1, kvk=1 << 60, kvv=1 << 61, acc=1 << 59)
+    assert rc == 1 and "larger than any memory" in m, (rc, m)
+    # entries and heads that no grid holds
+    (rc, m), _, (rc2, m2), _ = sizes(dict(H=2 ** 16, hk=2 ** 16), {}, 2 ** 15)
+    assert rc == 1 and "n*H" in m and rc2 == 1 and "n*hk" in m2
+    # the largest that one does
+    for desc, n in ((dict(H=2 ** 26, hk=2 ** 26), 1), (dict(H=1, hk=1, d=256), 2 ** 27 - 1)):
+        (rc, m), a, (rc2, m2), b = sizes(desc, dict(max_pages=2 ** 14), n, 2 ** 17)
+        assert rc == 0 and rc2 == 0 and n * desc["H"] * 8 <= a < 2 ** 60 and n * desc["H"] * 2 ** 20 <= b < 2 ** 60
+
+
 def test_append_takes_columns_of_the_same_rows(g):
     """q turned in place beside k and v: past the argument checks, to the launch
     (which fails here, without a GPU, or would fault on these addresses with one: not run there)."""
