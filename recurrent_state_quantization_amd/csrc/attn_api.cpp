@@ -332,6 +332,8 @@ int gdnq_kv_append(const gdnq_attn_desc *desc, const gdnq_rope_desc *rope, const
     }
     TRY(check_grid(((unsigned long long)T + n) * 4, "T"));
     const gdnq::AppendCall c{kv, q, k, v, q_out, table, pos, slots, cu_seqlens, ldq, ldqo, ldk, ldv, n, T};
+    if (!gdnq::kv_append_numbers(d, rope ? &r : nullptr, c))
+        return fail(GDNQ_EINVAL, "too many heads for one row (H=%d, hk=%d)", d.H, d.hk);
     return launched(gdnq::launch_kv_append(d, rope ? &r : nullptr, c, stream_of(stream)));
 }
 

@@ -48,6 +48,8 @@ struct EvictCall {
 };
 
 hipError_t launch_rope(const gdnq_rope_desc &d, const RopeCall &c, hipStream_t st);
+// whether 31 bits number the pieces of a workgroup's rows
+bool kv_append_numbers(const gdnq_attn_desc &d, const gdnq_rope_desc *r, const AppendCall &c);
 hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, const AppendCall &c, hipStream_t st);
 size_t attn_workspace(const gdnq_attn_desc &d, const gdnq_kv &kv, int n);
 hipError_t launch_attn_step(const gdnq_attn_desc &d, const AttnCall &c, hipStream_t st);

@@ -101,20 +101,38 @@ __global__ __launch_bounds__(NT) void kv_append_kernel(AppendArgs A)
     }
 }
 
+// log2 of the tokens of a workgroup: four of a prompt, whose rows of a head lie together (the same call 95 us
+// with one token where four take 88, 115 with eight; from memory 98, 99)
+int log_rows(const AppendCall &c) { return c.cu && c.T >= 1024 ? 2 : 0; }
+
+HeadPieces pieces_of(const gdnq_attn_desc &d, const gdnq_rope_desc *r)
+{
+    const bool inter = r && (r->flags & GDNQ_ROPE_INTERLEAVED);
+    return head_pieces(d.d, r ? r->rot : 0, inter, d.io_dtype == GDNQ_IO_BF16);
+}
+
+long long pieces_of_token(const gdnq_attn_desc &d, const AppendCall &c, int ni, int nv)
+{
+    return ((c.q ? (long long)d.H : 0) + d.hk) * ni + (long long)d.hk * nv;
+}
+
 }  // namespace
+
+bool kv_append_numbers(const gdnq_attn_desc &d, const gdnq_rope_desc *r, const AppendCall &c)
+{
+    const int nv = d.d / (d.io_dtype == GDNQ_IO_BF16 ? 8 : 4);
+    return pieces_of_token(d, c, pieces_of(d, r).ni, nv) <= (0x7FFFFFFF - NT) >> log_rows(c);
+}
 
 hipError_t launch_kv_append(const gdnq_attn_desc &d, const gdnq_rope_desc *r, const AppendCall &c, hipStream_t st)
 {
     const bool bf16 = d.io_dtype == GDNQ_IO_BF16, inter = r && (r->flags & GDNQ_ROPE_INTERLEAVED);
-    const int es = bf16 ? 2 : 4, rot = r ? r->rot : 0;
-    AppendArgs A{c, head_pieces(d.d, rot, inter, bf16), d.H, d.hk, d.d, __builtin_ctz((unsigned)d.page), 0,
+    const int es = bf16 ? 2 : 4;
+    AppendArgs A{c, pieces_of(d, r), d.H, d.hk, d.d, __builtin_ctz((unsigned)d.page), log_rows(c),
                  d.d / (16 / es), 0, r ? r->amp : 1.0f, r != nullptr, r && (r->flags & GDNQ_ROPE_INVERSE), {}, {}, 0};
-    A.pieces = ((c.q ? d.H : 0) + d.hk) * A.p.ni + d.hk * A.nv;
+    A.pieces = (int)pieces_of_token(d, c, A.p.ni, A.nv);
     A.byPieces = make_divisor((unsigned)A.pieces);
     A.byNv = make_divisor((unsigned)A.nv);
-    // four tokens of a prompt: their rows of a head lie together (the same call 95 us with one token where
-    // four take 88, 115 with eight; from memory 98, 99)
-    A.rows = c.cu && c.T >= 1024 ? 2 : 0;
     const dim3 grid = grid_of(c.cu ? (unsigned long long)(c.T >> A.rows) + c.n : c.n, NT);
     A.nx = grid.x;
     // rows off 16 bytes share cache lines between lanes: 128 us through the caches, 211 past them

@@ -355,6 +355,32 @@ def test_far_distances(g, desc, kv, msg):
         assert rc == 1 and msg in m, (rc, m)
 
 
+@pytest.mark.parametrize("io,H,hk,d,n,rope", [
+    (0, 2 ** 26, 1, 256, 1, dict(d=256, io_dtype=0)),             # 2^31 pieces of queries
+    (0, 2 ** 27, 1, 256, 1, dict(d=256, io_dtype=0)),             # 2^32
+    (1, 2 ** 25, 2 ** 25, 256, 3, dict(d=256, rot=2)),
+    (1, 2 ** 23, 2 ** 23, 256, 2000, dict(d=256, rot=14)),        # four rows to a workgroup
+    (0, 2 ** 30 - 2, 2 ** 30 - 2, 64, 1, None),
+])
+def test_append_refuses_rows_beyond_its_numbers(g, io, H, hk, d, n, rope):
+    """Rows of more pieces than a workgroup's 31 bits number (hundreds of GB a row)."""
+    far = {k: i << 56 for i, k in enumerate(["q", "q_out", "k", "v", "kvk", "kvv", "acc", "kvpos"], 2)}
+    rc, m = _append(g, desc=dict(H=H, hk=hk, d=d, io_dtype=io, page=8), rope=rope, with_rope=rope is not None, n=n, T=n,
+                    kv=dict(n_pages=1, max_pages=1, n_slots=2000), **far)
+    assert rc == 1 and "too many" in m, (rc, m)
+
+
+def test_append_takes_wide_rows(g):
+    """Past the argument checks, to the launch: rows of 2^28 values are within the numbers."""
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("checks only")
+    far = {k: i << 56 for i, k in enumerate(["q", "q_out", "k", "v", "kvk", "kvv", "acc", "kvpos"], 2)}
+    rc, m = _append(g, desc=dict(H=2 ** 20, hk=2 ** 10, d=256, page=8), rope=dict(d=256), n=2000, T=2000,
+                    kv=dict(n_pages=1, max_pages=1, n_slots=2000), **far)
+    assert rc == 3, (rc, m)
+
+
 def test_workspaces_beyond_any_memory(g):
     """Sizes that 64 bits do not count are refused, by the calls too; none is answered with a small one."""
     out = ctypes.c_size_t()
