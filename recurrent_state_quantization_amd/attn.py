@@ -107,7 +107,8 @@ class Kv:
             if t.dim() != 4 or tuple(t.shape[1:]) != (hk, d.page, d.d) or t.stride(3) != 1:
                 _bad(f"{name} must be [n_pages, {hk}, {d.page}, {d.d}] with consecutive values in a row (got shape "
                      f"{tuple(t.shape)}, strides {t.stride()})")
-        if self.v.shape != self.k.shape or self.v.stride() != self.k.stride():
+        if self.v.shape != self.k.shape or any(
+                a != b for a, b, m in zip(self.v.stride(), self.k.stride(), self.k.shape) if m > 1):
             _bad("v must have the shape and strides of k")
         if self.table.dim() != 2:
             _bad("table must be [n_slots, max_pages]")

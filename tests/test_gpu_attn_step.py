@@ -350,3 +350,27 @@ def test_a_marshalled_cache_says_what_it_is():
         C.kv(acc=C.accd[:1]).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
     with pytest.raises(g.GdnqError, match="lens is"):
         C.kv(lens=C.lensd.long()).c(g.AttnDesc(H=4, hk=2, d=64, page=16))
+
+
+@pytest.mark.parametrize("hk,n_pages", [(1, 5), (2, 1), (1, 1)])
+def test_strides_of_one(hk, n_pages):
+    """A dimension of one has no distance: k and v may state other strides for it."""
+    torch = torch_cuda()
+    g = lib()
+    say("attention cache with dimensions of one", hk, n_pages)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    k, v = (torch.randn(n_pages, hk, 16, 64, generator=gen, device="cuda").bfloat16() for _ in "kv")
+    other = v.clone().as_strided(v.shape, [st if m > 1 else 8 * st + 64 for st, m in zip(v.stride(), v.shape)])
+    assert other.stride() != v.stride() and torch.equal(other, v)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    lens = torch.tensor([16 * n_pages - 3], dtype=torch.int32, device="cuda")
+    desc = g.AttnDesc(H=2 * hk, hk=hk, d=64, page=16)
+    q = torch.randn(1, 2 * hk * 64, generator=gen, device="cuda").bfloat16()
+    o = []
+    for w in (v, other):
+        kv = g.Kv(k, w, table, lens)
+        ws = torch.empty(max(16, g.gdnq_attn_workspace(desc, kv, 1)), dtype=torch.uint8, device="cuda")
+        o.append(torch.empty_like(q))
+        g.gdnq_attn_step(desc, kv, q, o[-1], None, 1, ws)
+    assert same(*o)
