@@ -117,7 +117,9 @@ typedef struct {
  * [n_pages,2,hk,page,d]), where no row of the one shares a byte with one of the
  * other.
  * acc and pos belong to rows and heads too: [n_pages,hk,page] each.
- *   acc  the attention weight that the row has received, or NULL
+ *   acc  the attention weight that the row has received, or NULL: gdnq_kv_append
+ *        sets it to 0 and gdnq_attn_step adds to it; that of a prompt's own
+ *        attention, which is not a call of this library, is the caller's to add
  *   pos  the position of its token, or NULL
  * An entry whose slot is outside [0, n_slots), or whose lens is outside
  * [0, max_pages page], is skipped on the device (nothing read or written for
@@ -159,7 +161,8 @@ int gdnq_kv_append(const gdnq_attn_desc *desc, const gdnq_rope_desc *rope, const
 /*
  * Bytes of device workspace that gdnq_attn_step needs for this descriptor, cache
  * (its sizes, and whether it has acc) and number of entries.  Never less for
- * more entries.
+ * more entries.  With acc it has room for the scores of every row of the pool,
+ * n_pages page H 4 bytes, whatever the entries hold.
  */
 int gdnq_attn_workspace(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32_t n, size_t *bytes_out);
 
@@ -171,24 +174,34 @@ int gdnq_attn_workspace(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32_t n
  * NaN in a query, or in a key that is attended to, makes the outputs and sums of
  * its heads NaN, whatever else is in the call.
  * With kv->acc, for every row that was attended: acc = acc_decay acc + the sum
- * of w_r over the query heads of its cache head.  Entries that attend to rows of
- * one page must then not be in the same call.  (Pages that lie before every
- * row of a window are not attended to: their table entries may be anything.)
+ * of w_r over the query heads of its cache head.  No page may then be attended to
+ * twice in a call, by two entries or by one whose table names it twice.  (Pages
+ * that lie before every row of a window are not attended to: their table entries
+ * may be anything.)
  * workspace: device, 16-byte aligned, at least gdnq_attn_workspace bytes, free
  * for other use once the call has run; calls that may run at the same time need
  * one each.  n == 0 is a no-op.
+ * The work is dealt out by the rows that a slot may hold, max_pages page or the
+ * window, before the lens are known: batches of short caches (up to some hundred
+ * rows) take up to 1.8 times as long in a table that is wider than they need.
  */
 int gdnq_attn_step(const gdnq_attn_desc *desc, const gdnq_kv *kv, const void *q, int64_t ldq, void *o, int64_t ldo,
                    const int32_t *slots, int32_t n, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of device workspace that gdnq_kv_evict needs; never less for more entries. */
+/*
+ * Bytes of device workspace that gdnq_kv_evict needs; never less for more entries.
+ * It follows the rows that a slot may hold, max_pages page: above the budget 8
+ * bytes for each row that could move (the lesser of the budget and the rows behind
+ * it, none up to 64), and above 32768 rows 4 more for every row, for each entry and
+ * head.
+ */
 int gdnq_kv_evict_workspace(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32_t budget, int32_t n,
                             size_t *bytes_out);
 
 /*
  * Cuts every entry that holds more than `budget` rows down to that many, each
  * head by itself.  The lens - budget rows of least acc leave, of equal ones the
- * lower row first.  Rows whose pos is below `sink`, or above the entry's largest
+ * lower row first.  Rows whose pos is below `sink`, or above the head's largest
  * minus `recent`, stay (sink + recent <= budget; where more rows than the
  * budget are such, the lower of them leave).  Kept rows behind the budget move,
  * in order, into the rows before it that became free, in order: K, V, acc and
@@ -196,8 +209,12 @@ int gdnq_kv_evict_workspace(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32
  * The entry then holds min(lens, budget) rows: lens is the caller's to lower.
  * Keys carry their positions already, so attention does not see the order (a
  * window would: it counts rows).  kv->acc and kv->pos must be there, acc without
- * NaN.  Slots of one call must be distinct, and so must their pages.  workspace
- * as for gdnq_attn_step.  n == 0 is a no-op.
+ * NaN.  Behind prompts acc is 0 everywhere unless the caller has added their
+ * attention's weights: the lowest unprotected rows would leave.  Slots of one call
+ * must be distinct, and so must their pages.  workspace as for gdnq_attn_step.
+ * n == 0 is a no-op.  A table that is wider than the rows held costs time here too
+ * (64 entries of 2049 rows, 8 heads, one row of each leaving: 16 us in tables of
+ * 2080 rows, 22 of 20000, 23 of 131072).
  */
 int gdnq_kv_evict(const gdnq_attn_desc *desc, const gdnq_kv *kv, int32_t budget, int32_t sink, int32_t recent,
                   const int32_t *slots, int32_t n, void *workspace, size_t workspace_bytes, void *stream);
